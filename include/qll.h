@@ -64,7 +64,8 @@ enum {
     QLL_ERR_WORKSPACE = -4, /* ws is NULL or smaller than qll_workspace_bytes() */
     QLL_ERR_LAUNCH = -5,    /* the HIP launch itself failed */
     QLL_ERR_DEVICE = -6,    /* no usable device, or the current device is not gfx950 */
-    QLL_ERR_SCRATCH = -7    /* qll_q4_0_q8_0_gemm_noalloc: the shape needs more than its static scratch */
+    QLL_ERR_SCRATCH = -7,   /* qll_q4_0_q8_0_gemm_noalloc: the shape needs more than its static scratch */
+    QLL_ERR_VALUE = -8      /* an argument that is not a size has a value outside its documented set */
 };
 
 /* Operations that may need a caller-owned device workspace. */
@@ -342,6 +343,39 @@ int qll_ternary_gemv(const uint32_t *w, float w_scale, const int8_t *xq, const f
                      const int32_t *act_sum, float *y, int64_t n, int64_t k, void *stream);
 int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const float *act_scale,
                      const int32_t *act_sum, float *y, int64_t m, int64_t n, int64_t k, void *stream);
+
+/* ------------------------------------------------- norms into activations */
+
+/* Residual sum, root-mean-square norm and quantization of the stream in one
+ * pass, the step before a linear layer.  For every row
+ *     h = T(f32(x) + f32(residual))   (h = x where residual is NULL)
+ *     v_t = h_t * weight_t / rms,  rms = sqrt(sum_t h_t^2 / k + eps)
+ * with T the stream's type `dtype` (QLL_DTYPE_F32, _BF16 or _F16; the sum is
+ * rounded to it once, to nearest even, and the norm is taken of the rounded
+ * sum).  h, where not NULL, receives the sum; it may be x or residual itself
+ * (the update in place) and must not overlap an input otherwise.  x,
+ * residual, h: [m][k] of type T; weight: float[k]; eps >= 0 and finite (else
+ * QLL_ERR_VALUE, like an unknown dtype).  k < 2^24 (else QLL_ERR_SHAPE, as in
+ * the GEMMs that take the result).
+ *
+ * The codes are those of exact products and a correctly rounded f64 quotient:
+ * with p_t = h_t * weight_t and A = max |p_t| over the block (or row),
+ *     q_t = round-half-away(127 * p_t / A)      (0 where A is 0)
+ * -- rms cancels from them -- so they do not depend on how a kernel splits
+ * the row.  Against qll_quantize_q8_0 on an f32 v they can differ by one at
+ * values within f32 rounding of a border. */
+
+/* Q8_0 blocks: d = binary16(f32(A / (127 rms))) per 32-block.  xq:
+ * block_q8_0[m][k/32].  k % 32 == 0. */
+int qll_rmsnorm_q8_0(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
+                     void *xq, int64_t m, int64_t k, void *stream);
+
+/* int8 rows: act_scale = f32(127 rms / A) and act_sum = sum_t q_t per row; a
+ * row with A = 0, or whose act_scale is not finite, gets q = 0, act_scale = 0
+ * and act_sum = 0.  xq: int8[m][k], act_scale: float[m], act_sum: int32[m].
+ * Any k >= 1. */
+int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
+                        int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k, void *stream);
 
 #ifdef __cplusplus
 }

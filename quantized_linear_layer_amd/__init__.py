@@ -68,6 +68,8 @@ def load(path=LIB_PATH):
         "qll_quantize_i8_rows": [P, P, P, P, I, I, P],
         "qll_ternary_gemv": [P, F, P, P, P, P, I, I, P],
         "qll_ternary_gemm": [P, F, P, P, P, P, I, I, I, P],
+        "qll_rmsnorm_q8_0": [P, ctypes.c_int, P, P, F, P, P, I, I, P],
+        "qll_rmsnorm_i8_rows": [P, ctypes.c_int, P, P, F, P, P, P, P, I, I, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -112,6 +114,21 @@ def _ptr(t, nbytes, what):
 def _stream(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream, *tensors):
+    """Torch's current stream (or `stream`) as a handle, after checking that
+    every tensor given is on that stream's device and that it is the current
+    one: a kernel is launched on the current device."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream()
+    dev = s.device_index
+    if stream is not None and dev != torch.cuda.current_device():
+        raise ValueError(f"the stream is on device {dev}, the current device is {torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on device {t.get_device()}, the call runs on device {dev}")
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -299,3 +316,27 @@ def qll_ternary_gemm(w, w_scale, xq, act_scale, act_sum, y, m, n, k, stream=None
     _call("qll_ternary_gemm", _ptr(w, n * (k // 16) * 4, "w"), ctypes.c_float(float(w_scale)),
           _ptr(xq, m * k, "xq"), _ptr(act_scale, m * 4, "act_scale"), _ptr(act_sum, m * 4, "act_sum"),
           _ptr(y, m * n * 4, "y"), m, n, k, _stream(stream))
+
+
+# ----------------------------------------------------------------- norms into activations
+
+def _esize(dtype):
+    return 4 if dtype == QLL_DTYPE_F32 else 2
+
+
+def qll_rmsnorm_q8_0(x, dtype, residual, weight, eps, h, xq, m, k, stream=None):
+    """xq = Q8_0(rmsnorm(x + residual) * weight), h = x + residual; residual
+    and h may be None, h may be x or residual."""
+    nb = m * k * _esize(dtype)
+    _call("qll_rmsnorm_q8_0", _ptr(x, nb, "x"), int(dtype), _ptr(residual, nb, "residual"),
+          _ptr(weight, k * 4, "weight"), float(eps), _ptr(h, nb, "h"),
+          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), m, k, _on(stream, x, residual, weight, h, xq))
+
+
+def qll_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_sum, m, k, stream=None):
+    """As qll_rmsnorm_q8_0, into int8 rows with act_scale and act_sum."""
+    nb = m * k * _esize(dtype)
+    _call("qll_rmsnorm_i8_rows", _ptr(x, nb, "x"), int(dtype), _ptr(residual, nb, "residual"),
+          _ptr(weight, k * 4, "weight"), float(eps), _ptr(h, nb, "h"), _ptr(xq, m * k, "xq"),
+          _ptr(act_scale, m * 4, "act_scale"), _ptr(act_sum, m * 4, "act_sum"), m, k,
+          _on(stream, x, residual, weight, h, xq, act_scale, act_sum))

@@ -110,6 +110,8 @@ const char *qll_status_string(int status)
         return "no usable device or the current device is not gfx950";
     case QLL_ERR_SCRATCH:
         return "the shape needs more scratch than the allocation-free entry's static array holds";
+    case QLL_ERR_VALUE:
+        return "an argument (dtype, activation, eps or a count) has a value outside its documented set";
     default:
         return "unknown status";
     }
@@ -510,6 +512,51 @@ int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const f
     if (int rc = check_device())
         return rc;
     return launched(launch_ternary_gemm(w, w_scale, xq, act_scale, act_sum, y, m, n, k, as_stream(stream)));
+}
+
+// Checks the two norms share; QLL_OK or the status to return.
+static int norm_args(const void *x, int dtype, const void *residual, const float *weight, float eps, const void *h,
+                     int64_t m, int64_t k)
+{
+    if (dtype < QLL_DTYPE_F32 || dtype > QLL_DTYPE_F16 || !(eps >= 0.0f) || !__builtin_isfinite(eps))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h))
+        return QLL_ERR_ALIGN;
+    return QLL_OK;
+}
+
+int qll_rmsnorm_q8_0(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
+                     void *xq, int64_t m, int64_t k, void *stream)
+{
+    if (!x || !weight || !xq)
+        return QLL_ERR_NULL;
+    if (int rc = norm_args(x, dtype, residual, weight, eps, h, m, k))
+        return rc;
+    if (k % 32 != 0)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(xq))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_rmsnorm_q8_0(x, dtype, residual, weight, eps, h, static_cast<uint8_t *>(xq), m, k,
+                                        as_stream(stream)));
+}
+
+int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
+                        int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k, void *stream)
+{
+    if (!x || !weight || !xq || !act_scale || !act_sum)
+        return QLL_ERR_NULL;
+    if (int rc = norm_args(x, dtype, residual, weight, eps, h, m, k))
+        return rc;
+    if (!aligned16(xq) || !aligned16(act_scale) || !aligned16(act_sum))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_sum, m, k,
+                                           as_stream(stream)));
 }
 
 } // extern "C"

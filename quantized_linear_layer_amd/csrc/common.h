@@ -169,6 +169,13 @@ hipError_t launch_ternary_gemv(const uint32_t *w, float w_scale, const int8_t *x
 hipError_t launch_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const float *act_scale,
                                const int32_t *act_sum, float *y, int64_t m, int64_t n, int64_t k, hipStream_t s);
 
+// Residual sum, root-mean-square norm and quantization of the stream (dtype: a
+// QLL_W_* value) to Q8_0 blocks or int8 rows; res and h may be null.
+hipError_t launch_rmsnorm_q8_0(const void *x, int dtype, const void *res, const float *w, float eps, void *h,
+                               uint8_t *xq, int64_t m, int64_t k, hipStream_t s);
+hipError_t launch_rmsnorm_i8_rows(const void *x, int dtype, const void *res, const float *w, float eps, void *h,
+                                  int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k,
+                                  hipStream_t s);
 // Largest k the LDS-staged decode kernels accept (the activation of one row
 // is kept whole in LDS).
 constexpr int64_t kMaxKQ4Gemv = 49152;
