@@ -79,7 +79,10 @@ enum {
     QLL_OP_GEMM_NT_F16 = 7,  /* qll_gemm_nt with QLL_DTYPE_F16 weights on the bf16 matrix core */
     QLL_OP_GEMM_NT_F32 = 8,  /* qll_gemm_nt with QLL_DTYPE_F32 weights on the bf16 matrix core */
     QLL_OP_SGEMM_BF16 = 9,   /* qll_sgemm at m > 1 on the bf16 matrix core */
-    QLL_OP_Q4_0_GEMV_F32 = 10 /* qll_q4_0_q8_0_gemv_f32's optional workspace */
+    QLL_OP_Q4_0_GEMV_F32 = 10, /* qll_q4_0_q8_0_gemv_f32's optional workspace */
+    QLL_OP_Q4_0_LINEAR = 11,         /* qll_q4_0_q8_0_linear (the repacked form: QLL_OP_Q4_0_REPACKED_GEMM) */
+    QLL_OP_Q4_0_GATED = 12,          /* qll_q4_0_q8_0_gated */
+    QLL_OP_Q4_0_REPACKED_GATED = 13  /* qll_q4_0_repacked_q8_0_gated */
 };
 
 /* Bytes of device workspace `op` needs at this shape (0 if none); SIZE_MAX if
@@ -88,6 +91,11 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k);
 
 /* Element types of the weights of qll_gemm_nt. */
 enum { QLL_DTYPE_F32 = 0, QLL_DTYPE_BF16 = 1, QLL_DTYPE_F16 = 2 };
+
+/* Activations of the linear and gated entries: none, max(x, 0),
+ * x Phi(x) (the erf form), 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))),
+ * x / (1 + exp(-x)). */
+enum { QLL_ACT_NONE = 0, QLL_ACT_RELU = 1, QLL_ACT_GELU = 2, QLL_ACT_GELU_TANH = 3, QLL_ACT_SILU = 4 };
 
 /* Static string naming a status code. */
 const char *qll_status_string(int status);
@@ -343,6 +351,53 @@ int qll_ternary_gemv(const uint32_t *w, float w_scale, const int8_t *xq, const f
                      const int32_t *act_sum, float *y, int64_t n, int64_t k, void *stream);
 int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const float *act_scale,
                      const int32_t *act_sum, float *y, int64_t m, int64_t n, int64_t k, void *stream);
+
+/* ------------------------------------- Q4_0 linear layer with its epilogue */
+
+/* Y[m][n] = act(X.W^T + bias) + residual, the products those of
+ * qll_q4_0_q8_0_gemm (the same kernels, limits on k and workspace, which
+ * QLL_OP_Q4_0_LINEAR names) and the epilogue applied to each f32 sum before
+ * it is stored: bias float[n] or NULL, act a QLL_ACT_* value, residual
+ * float[m][n] or NULL.  residual may be y itself (an accumulation in place);
+ * otherwise y must not overlap an input.  Without bias, activation and
+ * residual the result is that of qll_q4_0_q8_0_gemm bit for bit.
+ * QLL_ERR_VALUE for an unknown act. */
+int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int act, const float *residual, float *y,
+                         int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);
+
+/* The same on weights repacked by qll_q4_0_repack: the products of
+ * qll_q4_0_repacked_q8_0_gemm, its limits and its workspace. */
+int qll_q4_0_repacked_q8_0_linear(const void *wp, const void *xq, const float *bias, int act, const float *residual,
+                                  float *y, int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------ Q4_0 gated projection (GLU) */
+
+/* Y[m][n] = act(X.Wg^T) * (X.Wu^T), the two projections of a gated
+ * feed-forward block and their product in one kernel: neither projection is
+ * written to memory.  wg, wu: block_q4_0[n][k/32]; xq: block_q8_0[m][k/32];
+ * y: float[m][n]; each product with the arithmetic of qll_q4_0_q8_0_gemm
+ * (exact int32 block sums, f32 scaling).  k % 32 == 0 and k < 2^24.
+ * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4_0_GATED, m, n, k) bytes
+ * (0 for m <= 64 with k >= 256, and for m == 1); contents on return are
+ * unspecified. */
+int qll_q4_0_q8_0_gated(const void *wg, const void *wu, const void *xq, int act, float *y, int64_t m, int64_t n,
+                        int64_t k, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of the repacked form of a gate and up pair W[n][k/32] (SIZE_MAX if the
+ * shape is invalid): ceil(n/64) * (k/32) * 3328. */
+size_t qll_q4_0_repacked_gated_bytes(int64_t n, int64_t k);
+
+/* Load-time repack of a gate and up pair for qll_q4_0_repacked_q8_0_gated: the
+ * layout of qll_q4_0_repack with rows 0..63 of 128-row tile t holding rows
+ * 64 t .. 64 t + 63 of wg and rows 64..127 the same rows of wu (rows past n
+ * zero).  wp: qll_q4_0_repacked_gated_bytes(n, k) bytes, written in full. */
+int qll_q4_0_repack_gated(const void *wg, const void *wu, void *wp, int64_t n, int64_t k, void *stream);
+
+/* qll_q4_0_q8_0_gated on a repacked pair, on the 6-bit matrix-core path of
+ * qll_q4_0_repacked_q8_0_gemm.  m >= 1; ws/ws_bytes: at least
+ * qll_workspace_bytes(QLL_OP_Q4_0_REPACKED_GATED, m, n, k) bytes. */
+int qll_q4_0_repacked_q8_0_gated(const void *wp, const void *xq, int act, float *y, int64_t m, int64_t n, int64_t k,
+                                 void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------- norms into activations */
 

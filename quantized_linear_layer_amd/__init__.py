@@ -25,6 +25,10 @@ QLL_OP_GEMM_NT_F16 = 7
 QLL_OP_GEMM_NT_F32 = 8
 QLL_OP_SGEMM_BF16 = 9
 QLL_OP_Q4_0_GEMV_F32 = 10
+QLL_OP_Q4_0_LINEAR = 11
+QLL_OP_Q4_0_GATED = 12
+QLL_OP_Q4_0_REPACKED_GATED = 13
+QLL_ACT_NONE, QLL_ACT_RELU, QLL_ACT_GELU, QLL_ACT_GELU_TANH, QLL_ACT_SILU = 0, 1, 2, 3, 4
 QLL_DTYPE_F32, QLL_DTYPE_BF16, QLL_DTYPE_F16 = 0, 1, 2
 
 Q4_0_BLOCK_BYTES = 18
@@ -68,6 +72,11 @@ def load(path=LIB_PATH):
         "qll_quantize_i8_rows": [P, P, P, P, I, I, P],
         "qll_ternary_gemv": [P, F, P, P, P, P, I, I, P],
         "qll_ternary_gemm": [P, F, P, P, P, P, I, I, I, P],
+        "qll_q4_0_q8_0_linear": [P, P, P, ctypes.c_int, P, P, I, I, I, P, S, P],
+        "qll_q4_0_repacked_q8_0_linear": [P, P, P, ctypes.c_int, P, P, I, I, I, P, S, P],
+        "qll_q4_0_q8_0_gated": [P, P, P, ctypes.c_int, P, I, I, I, P, S, P],
+        "qll_q4_0_repack_gated": [P, P, P, I, I, P],
+        "qll_q4_0_repacked_q8_0_gated": [P, P, ctypes.c_int, P, I, I, I, P, S, P],
         "qll_rmsnorm_q8_0": [P, ctypes.c_int, P, P, F, P, P, I, I, P],
         "qll_rmsnorm_i8_rows": [P, ctypes.c_int, P, P, F, P, P, P, P, I, I, P],
     }
@@ -79,6 +88,8 @@ def load(path=LIB_PATH):
     L.qll_workspace_bytes.restype = ctypes.c_size_t
     L.qll_q4_0_repacked_bytes.argtypes = [I, I]
     L.qll_q4_0_repacked_bytes.restype = ctypes.c_size_t
+    L.qll_q4_0_repacked_gated_bytes.argtypes = [I, I]
+    L.qll_q4_0_repacked_gated_bytes.restype = ctypes.c_size_t
     L.qll_q4_0_decode_packed_bytes.argtypes = [I, I]
     L.qll_q4_0_decode_packed_bytes.restype = ctypes.c_size_t
     L.qll_q8_0_repacked_bytes.argtypes = [I, I]
@@ -316,6 +327,65 @@ def qll_ternary_gemm(w, w_scale, xq, act_scale, act_sum, y, m, n, k, stream=None
     _call("qll_ternary_gemm", _ptr(w, n * (k // 16) * 4, "w"), ctypes.c_float(float(w_scale)),
           _ptr(xq, m * k, "xq"), _ptr(act_scale, m * 4, "act_scale"), _ptr(act_sum, m * 4, "act_sum"),
           _ptr(y, m * n * 4, "y"), m, n, k, _stream(stream))
+
+
+# ----------------------------------------------------------------- Q4_0 linear and gated
+
+def _op_ws(ws, op, m, n, k):
+    """ws as (pointer, bytes) for an operation that may need none; a shape
+    the library refuses is left for it to name."""
+    need = qll_workspace_bytes(op, m, n, k)
+    return (None, 0) if need == 2 ** 64 - 1 else _ws(ws, need)
+
+
+def qll_q4_0_q8_0_linear(w, xq, bias, act, residual, y, m, n, k, ws=None, stream=None):
+    """y = act(x.W^T + bias) + residual; bias and residual may be None,
+    residual may be y."""
+    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_LINEAR, m, n, k)
+    _call("qll_q4_0_q8_0_linear", _ptr(w, n * (k // 32) * Q4_0_BLOCK_BYTES, "w"),
+          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), _ptr(bias, n * 4, "bias"), int(act),
+          _ptr(residual, m * n * 4, "residual"), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
+          _on(stream, w, xq, bias, residual, y, ws))
+
+
+def qll_q4_0_repacked_q8_0_linear(wp, xq, bias, act, residual, y, m, n, k, ws=None, stream=None):
+    """qll_q4_0_q8_0_linear on weights repacked by qll_q4_0_repack."""
+    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_REPACKED_GEMM, m, n, k)
+    need = qll_q4_0_repacked_bytes(n, k)
+    _call("qll_q4_0_repacked_q8_0_linear", _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"),
+          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), _ptr(bias, n * 4, "bias"), int(act),
+          _ptr(residual, m * n * 4, "residual"), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
+          _on(stream, wp, xq, bias, residual, y, ws))
+
+
+def qll_q4_0_q8_0_gated(wg, wu, xq, act, y, m, n, k, ws=None, stream=None):
+    """y = act(x.Wg^T) * (x.Wu^T)."""
+    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_GATED, m, n, k)
+    nb = n * (k // 32) * Q4_0_BLOCK_BYTES
+    _call("qll_q4_0_q8_0_gated", _ptr(wg, nb, "wg"), _ptr(wu, nb, "wu"),
+          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), int(act), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
+          _on(stream, wg, wu, xq, y, ws))
+
+
+def qll_q4_0_repacked_gated_bytes(n, k):
+    return int(load().qll_q4_0_repacked_gated_bytes(int(n), int(k)))
+
+
+def qll_q4_0_repack_gated(wg, wu, wp, n, k, stream=None):
+    """Load-time repack of a gate and up pair into the matrix-core operand form."""
+    need = qll_q4_0_repacked_gated_bytes(n, k)
+    nb = n * (k // 32) * Q4_0_BLOCK_BYTES
+    _call("qll_q4_0_repack_gated", _ptr(wg, nb, "wg"), _ptr(wu, nb, "wu"),
+          _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"), n, k, _on(stream, wg, wu, wp))
+
+
+def qll_q4_0_repacked_q8_0_gated(wp, xq, act, y, m, n, k, ws=None, stream=None):
+    """qll_q4_0_q8_0_gated on a pair repacked by qll_q4_0_repack_gated."""
+    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_REPACKED_GATED, m, n, k)
+    need = qll_q4_0_repacked_gated_bytes(n, k)
+    _call("qll_q4_0_repacked_q8_0_gated", _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"),
+          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), int(act), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
+          _on(stream, wp, xq, y, ws))
 
 
 # ----------------------------------------------------------------- norms into activations

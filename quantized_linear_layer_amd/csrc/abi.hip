@@ -85,6 +85,12 @@ int scratch_address(void **out)
     return QLL_OK;
 }
 
+bool act_ok(int act) { return act >= QLL_ACT_NONE && act <= QLL_ACT_SILU; }
+static_assert((int)QLL_ACT_NONE == (int)QLL_A_NONE && (int)QLL_ACT_RELU == (int)QLL_A_RELU &&
+                  (int)QLL_ACT_GELU == (int)QLL_A_GELU && (int)QLL_ACT_GELU_TANH == (int)QLL_A_GELU_TANH &&
+                  (int)QLL_ACT_SILU == (int)QLL_A_SILU,
+              "activation codes");
+
 hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
 } // namespace
@@ -125,6 +131,7 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
             return SIZE_MAX;
         return m == 1 ? sgemv_workspace(n, k) : 0;
     case QLL_OP_Q4_0_Q8_0_GEMM:
+    case QLL_OP_Q4_0_LINEAR:
         if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || (m > kMaxMSmall && k >= kMaxGemmK))
             return SIZE_MAX;
         return q4_small_m_path(m, n, k) ? 0 : q4_0_q8_0_gemm_workspace(m, n, k);
@@ -152,6 +159,13 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
             return SIZE_MAX;
         return q4_0_packed_gemm_workspace(m, n, k);
+    case QLL_OP_Q4_0_GATED:
+    case QLL_OP_Q4_0_REPACKED_GATED:
+        if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
+            return SIZE_MAX;
+        if (op == QLL_OP_Q4_0_REPACKED_GATED)
+            return q4_0_packed_gated_workspace(m, n, k);
+        return q4_gated_small(m, k) ? 0 : q4_0_gated_gemm_workspace(m, n, k);
     default:
         return SIZE_MAX;
     }
@@ -512,6 +526,124 @@ int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const f
     if (int rc = check_device())
         return rc;
     return launched(launch_ternary_gemm(w, w_scale, xq, act_scale, act_sum, y, m, n, k, as_stream(stream)));
+}
+
+int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int act, const float *residual, float *y,
+                         int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!w || !xq || !y)
+        return QLL_ERR_NULL;
+    if (!act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || (m == 1 && k > kMaxKQ4Gemv) ||
+        (m > kMaxMSmall && k >= kMaxGemmK))
+        return QLL_ERR_SHAPE;
+    if (!aligned16(w) || !aligned16(xq) || !aligned16(bias) || !aligned16(residual) || !aligned16(y))
+        return QLL_ERR_ALIGN;
+    const uint8_t *wb = static_cast<const uint8_t *>(w), *xb = static_cast<const uint8_t *>(xq);
+    const LinearEpilogue ep{bias, residual, act};
+    if (q4_small_m_path(m, n, k)) {
+        if (int rc = check_device())
+            return rc;
+        return launched(launch_q4_0_q8_0_gemv_m_linear(wb, xb, y, m, n, k, ep, as_stream(stream)));
+    }
+    if (!ws || ws_bytes < q4_0_q8_0_gemm_workspace(m, n, k))
+        return QLL_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4_0_q8_0_gemm_linear(wb, xb, y, m, n, k, ep, ws, as_stream(stream)));
+}
+
+int qll_q4_0_repacked_q8_0_linear(const void *wp, const void *xq, const float *bias, int act, const float *residual,
+                                  float *y, int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!wp || !xq || !y || !ws)
+        return QLL_ERR_NULL;
+    if (!act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(wp) || !aligned16(xq) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) ||
+        !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (ws_bytes < q4_0_packed_gemm_workspace(m, n, k))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4_0_packed_gemm_linear(static_cast<const uint8_t *>(wp),
+                                                   static_cast<const uint8_t *>(xq), y, m, n, k,
+                                                   LinearEpilogue{bias, residual, act}, ws, as_stream(stream)));
+}
+
+int qll_q4_0_q8_0_gated(const void *wg, const void *wu, const void *xq, int act, float *y, int64_t m, int64_t n,
+                        int64_t k, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!wg || !wu || !xq || !y)
+        return QLL_ERR_NULL;
+    if (!act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(wg) || !aligned16(wu) || !aligned16(xq) || !aligned16(y))
+        return QLL_ERR_ALIGN;
+    const uint8_t *g = static_cast<const uint8_t *>(wg), *u = static_cast<const uint8_t *>(wu),
+                  *x = static_cast<const uint8_t *>(xq);
+    if (q4_gated_small(m, k)) {
+        if (int rc = check_device())
+            return rc;
+        if (m == 1 && k <= kMaxKQ4Gemv)
+            return launched(launch_q4_0_gated_gemv(g, u, x, act, y, n, k, as_stream(stream)));
+        return launched(launch_q4_0_gated_small_m(g, u, x, act, y, m, n, k, as_stream(stream)));
+    }
+    if (!ws || ws_bytes < q4_0_gated_gemm_workspace(m, n, k))
+        return QLL_ERR_WORKSPACE;
+    if (!aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4_0_gated_gemm(g, u, x, act, y, m, n, k, ws, as_stream(stream)));
+}
+
+size_t qll_q4_0_repacked_gated_bytes(int64_t n, int64_t k)
+{
+    if (!dims_ok(n, k) || k % 32 != 0)
+        return SIZE_MAX;
+    return q4_0_repacked_gated_bytes(n, k);
+}
+
+int qll_q4_0_repack_gated(const void *wg, const void *wu, void *wp, int64_t n, int64_t k, void *stream)
+{
+    if (!wg || !wu || !wp)
+        return QLL_ERR_NULL;
+    if (!dims_ok(n, k) || k % 32 != 0)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(wg) || !aligned16(wu) || !aligned16(wp))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4_0_repack_gated(static_cast<const uint8_t *>(wg), static_cast<const uint8_t *>(wu),
+                                             static_cast<uint8_t *>(wp), n, k, as_stream(stream)));
+}
+
+int qll_q4_0_repacked_q8_0_gated(const void *wp, const void *xq, int act, float *y, int64_t m, int64_t n, int64_t k,
+                                 void *ws, size_t ws_bytes, void *stream)
+{
+    if (!wp || !xq || !y || !ws)
+        return QLL_ERR_NULL;
+    if (!act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(wp) || !aligned16(xq) || !aligned16(y) || !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (ws_bytes < q4_0_packed_gated_workspace(m, n, k))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4_0_packed_gated(static_cast<const uint8_t *>(wp), static_cast<const uint8_t *>(xq), act,
+                                             y, m, n, k, ws, as_stream(stream)));
 }
 
 // Checks the two norms share; QLL_OK or the status to return.

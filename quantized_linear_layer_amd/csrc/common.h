@@ -85,6 +85,98 @@ __device__ __forceinline__ void load_q8_0_block(const uint8_t *base, int64_t o, 
     }
 }
 
+// ------------------------------------------------------------ epilogues
+
+// Activations of the fused linear and gated entries (the ABI's QLL_ACT_*).
+enum { QLL_A_NONE = 0, QLL_A_RELU = 1, QLL_A_GELU = 2, QLL_A_GELU_TANH = 3, QLL_A_SILU = 4 };
+
+// x / (1 + exp(-t)) with the hardware's exp2 and reciprocal (each within about
+// one unit in the last place; exp2's argument rounding adds |t| 2^-24 relative
+// where exp(-t) counts): exp(-t) = inf gives x * 0.
+__device__ __forceinline__ float times_sigmoid(float x, float t)
+{
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * t));
+}
+
+__device__ __forceinline__ float act_relu(float x) { return x > 0.0f ? x : 0.0f; }
+__device__ __forceinline__ float act_gelu(float x) { return 0.5f * x * erfcf(-0.70710678f * x); }
+// 0.5 (1 + tanh(u)) = sigmoid(2 u)
+__device__ __forceinline__ float act_gelu_tanh(float x)
+{
+    return times_sigmoid(x, 1.59576912f * (x + 0.044715f * x * x * x));
+}
+__device__ __forceinline__ float act_silu(float x) { return times_sigmoid(x, x); }
+
+__device__ __forceinline__ float activate(float x, int act)
+{
+    switch (act) { // uniform
+    case QLL_A_RELU: return act_relu(x);
+    case QLL_A_GELU: return act_gelu(x);
+    case QLL_A_GELU_TANH: return act_gelu_tanh(x);
+    case QLL_A_SILU: return act_silu(x);
+    default: return x;
+    }
+}
+
+// The 16 values of a matrix-core tile register group, the choice made once.
+template <typename V16>
+__device__ __forceinline__ void activate16(V16 &v, int act)
+{
+    switch (act) { // uniform
+    case QLL_A_RELU:
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = act_relu(v[i]);
+        break;
+    case QLL_A_GELU:
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = act_gelu(v[i]);
+        break;
+    case QLL_A_GELU_TANH:
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = act_gelu_tanh(v[i]);
+        break;
+    case QLL_A_SILU:
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            v[i] = act_silu(v[i]);
+        break;
+    default: break;
+    }
+}
+
+// What a product kernel does with output (i, j) of [m][n], as a template
+// argument, so that the plain entries keep their kernels.
+struct PlainEpilogue { // y = v
+    static constexpr bool kLinear = false, kGated = false;
+    PlainEpilogue rows(int64_t, int64_t) const { return *this; }
+};
+struct LinearEpilogue { // y = act(v + bias[j]) + res[i][j]; bias and res may be null, res may be y
+    static constexpr bool kLinear = true, kGated = false;
+    const float *bias, *res;
+    int act;
+    // the same for rows i0, i0 + 1, ... as rows 0, 1, ...
+    LinearEpilogue rows(int64_t i0, int64_t n) const { return {bias, res ? res + i0 * n : nullptr, act}; }
+};
+struct GatedEpilogue { // y = act(v of w) * (v of wu); raw: both products as planes (a k-split's partials)
+    static constexpr bool kLinear = false, kGated = true;
+    const uint8_t *wu; // null where the weights are interleaved at load time
+    int act;
+    bool raw;
+};
+
+template <class EP>
+__device__ __forceinline__ float epilogue(const EP &ep, float v, int64_t i, int64_t j, int64_t n)
+{
+    if constexpr (EP::kLinear) {
+        v = activate(ep.bias ? v + ep.bias[j] : v, ep.act);
+        return ep.res ? v + ep.res[i * n + j] : v;
+    }
+    return v;
+}
+
 // ------------------------------------------------------------ launchers
 // Each returns a hipError_t of the launch; arguments are already validated.
 
@@ -134,6 +226,38 @@ hipError_t launch_q4_0_q8_0_gemv_f32(const uint8_t *w, const float *x, float *y,
                                      uint8_t *ws, hipStream_t s);
 size_t q4_0_gemv_f32_workspace(int64_t m, int64_t n, int64_t k);
 size_t q4_0_q8_0_gemm_workspace(int64_t m, int64_t n, int64_t k);
+// The same products with an epilogue, on the same kernels and workspaces.
+hipError_t launch_sum_splits_linear(const float *parts, float *y, int64_t m, int64_t n, int splits,
+                                    const LinearEpilogue &ep, hipStream_t s);
+hipError_t launch_q4_0_q8_0_gemv_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k,
+                                        const LinearEpilogue &ep, hipStream_t s);
+hipError_t launch_q4_0_q8_0_gemv_m_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                          int64_t k, const LinearEpilogue &ep, hipStream_t s);
+hipError_t launch_q4_0_q8_0_small_m_mfma_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                                int64_t k, const LinearEpilogue &ep, hipStream_t s);
+hipError_t launch_q4_0_q8_0_gemm_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                        int64_t k, const LinearEpilogue &ep, void *ws, hipStream_t s);
+hipError_t launch_q4_0_packed_gemm_linear(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                          int64_t k, const LinearEpilogue &ep, void *ws, hipStream_t s);
+// Gated products y = act(X.Wg^T) * (X.Wu^T): the GEMV at m = 1 up to
+// kMaxKQ4Gemv, the small-m matrix-core kernel where q4_gated_small holds
+// (groups of at most 32 rows), the 128-row GEMM otherwise.
+inline bool q4_gated_small(int64_t m, int64_t k) { return m == 1 || (m <= 64 && k >= kMinKMfma); }
+hipError_t launch_q4_0_gated_gemv(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                  int64_t n, int64_t k, hipStream_t s);
+hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                     int64_t m, int64_t n, int64_t k, hipStream_t s);
+hipError_t launch_sum_splits_gated(const float *parts, float *y, int64_t m, int64_t n, int splits, int act,
+                                   hipStream_t s);
+size_t q4_0_gated_gemm_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_q4_0_gated_gemm(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                  int64_t m, int64_t n, int64_t k, void *ws, hipStream_t s);
+size_t q4_0_repacked_gated_bytes(int64_t n, int64_t k);
+hipError_t launch_q4_0_repack_gated(const uint8_t *wg, const uint8_t *wu, uint8_t *wp, int64_t n, int64_t k,
+                                    hipStream_t s);
+size_t q4_0_packed_gated_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_q4_0_packed_gated(const uint8_t *wp, const uint8_t *xq, int act, float *y, int64_t m, int64_t n,
+                                    int64_t k, void *ws, hipStream_t s);
 // Decode GEMV with Q8_0 weights.
 hipError_t launch_q8_0_q8_0_gemv(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k, hipStream_t s);
 // Transposed-B (W stored [n][k]) f32 GEMV and GEMM with f32, bf16 or f16

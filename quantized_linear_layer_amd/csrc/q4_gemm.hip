@@ -36,6 +36,7 @@
 // Weights stay as nibbles in LDS (a quarter of the bytes of f16) and are
 // widened when the fragments are read.  (m <= 32 runs the small-m kernels.)
 #include "common.h"
+#include "q4_store.h"
 
 namespace qll {
 
@@ -54,7 +55,16 @@ constexpr int QTI = 2, QTJ = 2;
 constexpr int QXLoads = QKB * QBM / 16 / 4; // 1 KB activation loads per wave and stage
 constexpr int QDma = QXLoads + 1 + 2;       // + d_x or C0, + the weight codes and d_w
 __device__ __forceinline__ int q4gemm_wm(int wave) { return (wave >> 1) * 64; }
-__device__ __forceinline__ int q4gemm_wn(int wave) { return (wave & 1) * 64; }
+
+// Gated products: the workgroup's 128 weight rows are 64 of the gate (rows 0
+// to 63) and the same 64 of the up projection, and a wave's two column tiles
+// are 32 of each for the same outputs, so act(g) * u is a register operation.
+template <class EP>
+struct Q4GemmCols {
+    static constexpr int kStep = EP::kGated ? 64 : 32;          // weight rows from column tile 0 to 1
+    static constexpr int kOut = EP::kGated ? QBN / 2 : QBN;     // output columns of a workgroup
+    static __device__ __forceinline__ int first(int wave) { return (wave & 1) * (EP::kGated ? 32 : 64); }
+};
 
 constexpr int kQ4GemmThreads = 256;
 
@@ -189,6 +199,7 @@ struct Q4GemmSrc {
     uint32_t wo;    // byte offset of this lane's weight block, from (row n0, block b)
 };
 
+template <class EP>
 __device__ __forceinline__ Q4GemmSrc q4gemm_src(const Q4GemmPrep &p, int64_t n0, int64_t n, int nb)
 {
     constexpr int XL = QXLoads, RPB = QBM / 16; // 1 KB regions per block
@@ -202,7 +213,7 @@ __device__ __forceinline__ Q4GemmSrc q4gemm_src(const Q4GemmPrep &p, int64_t n0,
         c.xo[j] = (uint32_t)((row * p.nbp + kb) * 64 + q4gemm_slot(kb, row, lane & 3) * 16);
     }
     c.so = (uint32_t)(16 * lane);
-    const int row = (wave & 1) * 64 + lane;
+    const int row = (EP::kGated ? 0 : (wave & 1) * 64) + lane;
     const int64_t wrow = (n0 + row < n) ? row : n - 1 - n0; // rows past n: any valid row, output dropped
     c.wo = (uint32_t)(18 * wrow * nb);
     return c;
@@ -352,6 +363,7 @@ __device__ __forceinline__ T q4gemm_lds(const QLL_LDS char *base, uint32_t off)
 // both d_x[r] d_w[c]: S = 2 d_x d_w exactly (a product of two halves is
 // exact in f32, and so is its double).  The factor 2 leaves the kernel as an
 // exact halving of the outputs.
+template <int STEP>
 __device__ __forceinline__ void q4gemm_compute(const QLL_LDS char *base, const Q4GemmLaneOff &o, uint32_t bias,
                                                f32x16 acc[QTI][QTJ])
 {
@@ -366,8 +378,8 @@ __device__ __forceinline__ void q4gemm_compute(const QLL_LDS char *base, const Q
         static_assert(TI == TJ, "reads interleave row and column tiles");
 #pragma unroll
         for (int i = 0; i < TI; i++) {
-            const u32x2 wv = q4gemm_lds<u32x2>(base, o.w + kb * QBN * 16 + 512 * i);
-            const uint32_t dwb = q4gemm_lds<uint32_t>(base, o.dw + kb * QBN * 4 + 128 * i);
+            const u32x2 wv = q4gemm_lds<u32x2>(base, o.w + kb * QBN * 16 + 16 * STEP * i);
+            const uint32_t dwb = q4gemm_lds<uint32_t>(base, o.dw + kb * QBN * 4 + 4 * STEP * i);
 #pragma unroll
             for (int st = 0; st < 2; st++) {
                 a[i][st] = __builtin_bit_cast(f16x8, q4gemm_lds<u32x4>(base, o.x[kb][st] + 2048 * i));
@@ -448,22 +460,24 @@ __device__ __forceinline__ void q4gemm_sync()
     asm volatile("" ::: "memory");
 }
 
+template <class EP>
 __global__ __launch_bounds__(kQ4GemmThreads) void q4_0_q8_0_gemm_kernel(const uint8_t *__restrict__ w, Q4GemmPrep prep,
                                                                            float *__restrict__ y, int64_t m,
-                                                                           int64_t n, int nb, int per_split)
+                                                                           int64_t n, int nb, int per_split, EP ep)
 {
     constexpr int TI = QTI, TJ = QTJ, DMA = QDma;
     __shared__ Q4GemmLds lds[QNBUF];
     int64_t m_tile, n_tile;
-    q4gemm_tile(prep.mp / QBM, (n + QBN - 1) / QBN, m_tile, n_tile);
-    const int64_t m0 = m_tile * QBM, n0 = n_tile * QBN;
+    typedef Q4GemmCols<EP> Cols;
+    q4gemm_tile(prep.mp / QBM, (n + Cols::kOut - 1) / Cols::kOut, m_tile, n_tile);
+    const int64_t m0 = m_tile * QBM, n0 = n_tile * Cols::kOut;
     // split-k: blockIdx.y takes blocks [b_begin, b_begin + per_split) and
     // writes its partial tile to y + blockIdx.y * m * n (the workspace when
     // there are splits); blocks past nb have d_x = 0 in the prepared arrays
     const int b_begin = blockIdx.y * per_split;
-    y += (int64_t)blockIdx.y * m * n;
+    y += (int64_t)blockIdx.y * (EP::kGated ? 2 * m * n : m * n);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = q4gemm_wm(wave), wn = q4gemm_wn(wave);
+    const int wm = q4gemm_wm(wave), wn = Cols::first(wave);
 
     f32x16 acc[TI][TJ];
 #pragma unroll
@@ -472,7 +486,7 @@ __global__ __launch_bounds__(kQ4GemmThreads) void q4_0_q8_0_gemm_kernel(const ui
         for (int j = 0; j < TJ; j++)
             acc[i][j] = f32x16{};
 
-    const Q4GemmSrc src = q4gemm_src(prep, n0, n, nb);
+    const Q4GemmSrc src = q4gemm_src<EP>(prep, n0, n, nb);
     const int nstages = per_split / QKB;
     const Q4GemmLaneOff lo = q4gemm_lane_offsets(wm, wn, lane);
     uint32_t bias; // 0x64006400, opaque to the compiler (see q4gemm_wfrag)
@@ -488,9 +502,12 @@ __global__ __launch_bounds__(kQ4GemmThreads) void q4_0_q8_0_gemm_kernel(const ui
     g.x = reinterpret_cast<const uint8_t *>(prep.x) + m0 * prep.nbp * 64;
     g.dx = reinterpret_cast<const uint8_t *>(prep.dx + m0);
     g.c0 = reinterpret_cast<const uint8_t *>(prep.c0 + m0);
-    g.w = w + 18 * n0 * (int64_t)nb;
-    g.sblk = prep.mp * 8;
     const int swave = __builtin_amdgcn_readfirstlane(wave);
+    g.w = w + 18 * n0 * (int64_t)nb;
+    if constexpr (EP::kGated)
+        if (swave & 1)
+            g.w = ep.wu + 18 * n0 * (int64_t)nb;
+    g.sblk = prep.mp * 8;
     q4gemm_load_stage(g, src, nb, b_begin, swave, lds[0]);
     q4gemm_load_stage(g, src, nb, b_begin + QKB, swave, lds[1]);
     q4gemm_sync<DMA>();
@@ -498,24 +515,14 @@ __global__ __launch_bounds__(kQ4GemmThreads) void q4_0_q8_0_gemm_kernel(const ui
     for (int st = 0; st < nstages; st++) {
         const int nx2 = cur == 0 ? 2 : cur - 1;
         q4gemm_load_stage(g, src, nb, b_begin + (st + 2) * QKB, swave, lds[nx2]);
-        q4gemm_compute((const QLL_LDS char *)&lds[cur], lo, bias, acc);
+        q4gemm_compute<Cols::kStep>((const QLL_LDS char *)&lds[cur], lo, bias, acc);
         q4gemm_sync<DMA>();
         cur = cur == 2 ? 0 : cur + 1;
     }
     // no load may still be writing this workgroup's LDS when it ends
     __builtin_amdgcn_s_waitcnt(0x7 << 4); // vmcnt(0) expcnt(7) lgkmcnt(0)
 
-#pragma unroll
-    for (int i = 0; i < TI; i++)
-#pragma unroll
-        for (int j = 0; j < TJ; j++)
-#pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int64_t row = m0 + wm + 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                const int64_t col = n0 + wn + 32 * j + (lane & 31);
-                if (row < m && col < n)
-                    y[row * n + col] = 0.5f * acc[i][j][v]; // the scale tiles are 2 d_x d_w
-            }
+    q4_tile_store(ep, acc, y, m, n, m0 + wm, n0 + wn, lane);
 }
 
 // y[i] = sum over s of parts[s][i], in split order; four outputs per thread,
@@ -551,6 +558,92 @@ hipError_t launch_sum_splits(const float *parts, float *y, int64_t count, int sp
     else
         hipLaunchKernelGGL(sum_splits_kernel<false>, grid, dim3(256), 0, s, parts, y, count, splits);
     return hipGetLastError();
+}
+
+// The split sum with an epilogue: V columns of one row per thread (V = 4
+// where n % 4 == 0), the splits added in order.  PLANES = 2: each split holds
+// the gate's and the up projection's plane.
+template <int V>
+struct SplitSum {
+    float v[V];
+    __device__ __forceinline__ void add(const float *p)
+    {
+        if constexpr (V == 4) {
+            const f32x4 t = *reinterpret_cast<const f32x4 *>(p);
+            v[0] += t[0]; v[1] += t[1]; v[2] += t[2]; v[3] += t[3];
+        } else {
+            v[0] += *p;
+        }
+    }
+    __device__ __forceinline__ void store(float *p) const
+    {
+        if constexpr (V == 4)
+            *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+            *p = v[0];
+    }
+};
+
+template <int V, bool GATED>
+__global__ __launch_bounds__(256) void sum_splits_epilogue_kernel(const float *__restrict__ parts, float *y,
+                                                                  int64_t m, int64_t n, int splits, int64_t cgroups,
+                                                                  LinearEpilogue ep)
+{
+    const int64_t i = blockIdx.x / cgroups, j = ((int64_t)(blockIdx.x % cgroups) * 256 + threadIdx.x) * V;
+    if (j >= n)
+        return;
+    const int64_t at = i * n + j, plane = m * n;
+    SplitSum<V> a{}, b{};
+    if constexpr (GATED) {
+        for (int s = 0; s < splits; s++) {
+            a.add(parts + 2 * s * plane + at);
+            b.add(parts + (2 * s + 1) * plane + at);
+        }
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            a.v[e] = activate(a.v[e], ep.act) * b.v[e];
+    } else {
+        for (int s = 0; s < splits; s++)
+            a.add(parts + s * plane + at);
+        if (ep.bias)
+            a.add(ep.bias + j);
+#pragma unroll
+        for (int e = 0; e < V; e++)
+            a.v[e] = activate(a.v[e], ep.act);
+        if (ep.res)
+            a.add(ep.res + at);
+    }
+    a.store(y + at);
+}
+
+template <bool GATED>
+static hipError_t launch_sum_splits_epilogue(const float *parts, float *y, int64_t m, int64_t n, int splits,
+                                             const LinearEpilogue &ep, hipStream_t s)
+{
+    const int v = n % 4 == 0 ? 4 : 1; // every base is 16-byte aligned
+    const int64_t cgroups = (n + 256 * v - 1) / (256 * v);
+    if (m * cgroups > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(m * cgroups));
+    if (v == 4)
+        hipLaunchKernelGGL((sum_splits_epilogue_kernel<4, GATED>), grid, dim3(256), 0, s, parts, y, m, n, splits,
+                           cgroups, ep);
+    else
+        hipLaunchKernelGGL((sum_splits_epilogue_kernel<1, GATED>), grid, dim3(256), 0, s, parts, y, m, n, splits,
+                           cgroups, ep);
+    return hipGetLastError();
+}
+
+hipError_t launch_sum_splits_linear(const float *parts, float *y, int64_t m, int64_t n, int splits,
+                                    const LinearEpilogue &ep, hipStream_t s)
+{
+    return launch_sum_splits_epilogue<false>(parts, y, m, n, splits, ep, s);
+}
+
+hipError_t launch_sum_splits_gated(const float *parts, float *y, int64_t m, int64_t n, int splits, int act,
+                                   hipStream_t s)
+{
+    return launch_sum_splits_epilogue<true>(parts, y, m, n, splits, LinearEpilogue{nullptr, nullptr, act}, s);
 }
 
 // Split k when the output tiles alone leave workgroup slots empty (two
@@ -600,10 +693,13 @@ size_t q4_0_q8_0_gemm_workspace(int64_t m, int64_t n, int64_t k)
     return q4gemm_plan(m, n, k).total;
 }
 
-hipError_t launch_q4_0_q8_0_gemm(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
-                                 void *ws, hipStream_t s)
+// The activation prepass, then the GEMM; partial tiles go to the workspace
+// where k is split (a linear epilogue then belongs to the sum, so the GEMM
+// runs plain; a gated one writes both products).
+template <class EP>
+static hipError_t launch_gemm_kernel(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                                     const Q4GemmPlan &plan, const EP &ep, void *ws, hipStream_t s)
 {
-    const Q4GemmPlan plan = q4gemm_plan(m, n, k);
     uint8_t *base = static_cast<uint8_t *>(ws);
     Q4GemmPrep prep;
     prep.x = reinterpret_cast<u32x4 *>(base + plan.x_off);
@@ -619,12 +715,48 @@ hipError_t launch_q4_0_q8_0_gemm(const uint8_t *w, const uint8_t *xq, float *y, 
         return e;
     float *out = plan.splits > 1 ? reinterpret_cast<float *>(base) : y;
     const dim3 grid((unsigned)plan.tiles, (unsigned)plan.splits);
-    hipLaunchKernelGGL(q4_0_q8_0_gemm_kernel, grid, dim3(kQ4GemmThreads), 0, s, w, prep, out, m, n, (int)nb,
-                       plan.per_split);
-    e = hipGetLastError();
+    hipLaunchKernelGGL(q4_0_q8_0_gemm_kernel<EP>, grid, dim3(kQ4GemmThreads), 0, s, w, prep, out, m, n, (int)nb,
+                       plan.per_split, ep);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_0_q8_0_gemm(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                                 void *ws, hipStream_t s)
+{
+    const Q4GemmPlan plan = q4gemm_plan(m, n, k);
+    const hipError_t e = launch_gemm_kernel(w, xq, y, m, n, k, plan, PlainEpilogue{}, ws, s);
     if (e != hipSuccess || plan.splits == 1)
         return e;
-    return launch_sum_splits(out, y, m * n, plan.splits, s);
+    return launch_sum_splits(static_cast<const float *>(ws), y, m * n, plan.splits, s);
+}
+
+hipError_t launch_q4_0_q8_0_gemm_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                        int64_t k, const LinearEpilogue &ep, void *ws, hipStream_t s)
+{
+    const Q4GemmPlan plan = q4gemm_plan(m, n, k);
+    if (plan.splits == 1)
+        return launch_gemm_kernel(w, xq, y, m, n, k, plan, ep, ws, s);
+    const hipError_t e = launch_gemm_kernel(w, xq, y, m, n, k, plan, PlainEpilogue{}, ws, s);
+    if (e != hipSuccess)
+        return e;
+    return launch_sum_splits_linear(static_cast<const float *>(ws), y, m, n, plan.splits, ep, s);
+}
+
+// Gated: 64 output columns are 128 weight rows, so the plan is that of a GEMM
+// with twice the columns, rounded up to whole tiles.
+static Q4GemmPlan gated_plan(int64_t m, int64_t n, int64_t k) { return q4gemm_plan(m, (n + 63) / 64 * 128, k); }
+
+size_t q4_0_gated_gemm_workspace(int64_t m, int64_t n, int64_t k) { return gated_plan(m, n, k).total; }
+
+hipError_t launch_q4_0_gated_gemm(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                  int64_t m, int64_t n, int64_t k, void *ws, hipStream_t s)
+{
+    const Q4GemmPlan plan = gated_plan(m, n, k);
+    const hipError_t e =
+        launch_gemm_kernel(wg, xq, y, m, n, k, plan, GatedEpilogue{wu, act, plan.splits > 1}, ws, s);
+    if (e != hipSuccess || plan.splits == 1)
+        return e;
+    return launch_sum_splits_gated(static_cast<const float *>(ws), y, m, n, plan.splits, act, s);
 }
 
 } // namespace qll

@@ -337,10 +337,40 @@ __device__ __forceinline__ float gemv_compute(const GemvRaw<U> &raw, int64_t row
 // order, so the staging waits only for its own bytes and HBM traffic starts
 // at once.  (xq is deliberately not __restrict__: with it, the compiler may
 // move the activation loads past the barrier that keeps them ahead.)
-template <int L, int U, bool PAIR, bool F32>
+// A linear epilogue's bias and residual values are requested with the row's
+// weights, so that the store does not wait for a second trip to memory.
+struct RowEpilogue {
+    float bias, res;
+};
+template <class EP>
+__device__ __forceinline__ RowEpilogue row_epilogue(const EP &ep, int64_t row, int64_t n)
+{
+    RowEpilogue v{0.0f, 0.0f};
+    if constexpr (EP::kLinear) {
+        const int64_t j = row < n ? row : 0;
+        if (ep.bias)
+            v.bias = ep.bias[j];
+        if (ep.res)
+            v.res = ep.res[j];
+    }
+    return v;
+}
+
+template <class EP>
+__device__ __forceinline__ float activate_row(const EP &ep, float v, const RowEpilogue &r)
+{
+    if constexpr (EP::kLinear) {
+        v = activate(v + r.bias, ep.act);
+        return ep.res ? v + r.res : v;
+    }
+    return v;
+}
+
+template <int L, int U, bool PAIR, bool F32, class EP>
 __global__ __launch_bounds__(kGemvThreads) void q4_0_q8_0_gemv_kernel(const uint8_t *__restrict__ w,
                                                                       const void *xin,
-                                                                      float *__restrict__ y, int64_t n, int nb)
+                                                                      float *__restrict__ y, int64_t n, int nb,
+                                                                      EP ep)
 {
     extern __shared__ u32x4 smem[];
     constexpr int R = 64 / L; // rows per wave
@@ -369,6 +399,7 @@ __global__ __launch_bounds__(kGemvThreads) void q4_0_q8_0_gemv_kernel(const uint
     GemvRaw<U> cur;
     // unconditional (a wave without work loads masked dummies): see gemv_load
     gemv_load<L, U, PAIR>(w, grp * R + g, n, row_bytes, nu, 0, r, cur);
+    RowEpilogue rcur = row_epilogue(ep, grp * R + g, n);
 
     const ActLds act = F32 ? stage_f32_finish(xf, nb, fraw, smem) : stage_q8_finish(xq, nb, araw, smem);
 
@@ -381,8 +412,12 @@ __global__ __launch_bounds__(kGemvThreads) void q4_0_q8_0_gemv_kernel(const uint
             grp2 += stride;
         }
         GemvRaw<U> nxt;
-        if (grp2 < n_groups)
+        RowEpilogue rnxt = rcur;
+        if (grp2 < n_groups) {
+            if (c2 == 0)
+                rnxt = row_epilogue(ep, grp2 * R + g, n);
             gemv_load<L, U, PAIR>(w, grp2 * R + g, n, row_bytes, nu, c2 * chunk_units, r, nxt);
+        }
         const int64_t row = grp * R + g;
         acc += gemv_compute<L, U, PAIR>(cur, row, n, row_bytes, nu, c * chunk_units, r, act);
         if (c == chunks - 1) {
@@ -390,10 +425,11 @@ __global__ __launch_bounds__(kGemvThreads) void q4_0_q8_0_gemv_kernel(const uint
             for (int off = L / 2; off > 0; off >>= 1)
                 acc += __shfl_xor(acc, off);
             if (row < n && r == 0)
-                y[row] = acc;
+                y[row] = EP::kLinear ? activate_row(ep, acc, rcur) : acc;
             acc = 0.0f;
         }
         cur = nxt;
+        rcur = rnxt;
         grp = grp2;
         c = c2;
     }
@@ -407,8 +443,9 @@ constexpr int64_t kF32GemvGrid = 512;
 // finish, which measured faster on the 296 MB vocabulary projection than
 // looping resident waves over items (47 vs 53 us), and equal on one-pass
 // shapes.  The kernel still loops if the grid limit were ever reached.
-template <int L, int U, bool PAIR, bool F32>
-static hipError_t launch_l(const uint8_t *w, const void *xin, float *y, int64_t n, int nb, hipStream_t s)
+template <int L, int U, bool PAIR, bool F32, class EP>
+static hipError_t launch_l(const uint8_t *w, const void *xin, float *y, int64_t n, int nb, const EP &ep,
+                           hipStream_t s)
 {
     constexpr int R = 64 / L;
     const int64_t groups = (n + R - 1) / R;
@@ -421,13 +458,14 @@ static hipError_t launch_l(const uint8_t *w, const void *xin, float *y, int64_t 
         grid = kF32GemvGrid;
     if (grid > 0x7fffffff)
         grid = 0x7fffffff;
-    hipLaunchKernelGGL((q4_0_q8_0_gemv_kernel<L, U, PAIR, F32>), dim3((unsigned)grid), dim3(kGemvThreads),
-                       q4_gemv_lds_bytes(nb), s, w, xin, y, n, nb);
+    hipLaunchKernelGGL((q4_0_q8_0_gemv_kernel<L, U, PAIR, F32, EP>), dim3((unsigned)grid), dim3(kGemvThreads),
+                       q4_gemv_lds_bytes(nb), s, w, xin, y, n, nb, ep);
     return hipGetLastError();
 }
 
-template <bool PAIR, bool F32 = false>
-static hipError_t launch_pair(const uint8_t *w, const void *xq, float *y, int64_t n, int nb, hipStream_t s)
+template <bool PAIR, bool F32 = false, class EP = PlainEpilogue>
+static hipError_t launch_pair(const uint8_t *w, const void *xq, float *y, int64_t n, int nb, hipStream_t s,
+                              const EP &ep = EP{})
 {
     const int nu = PAIR ? nb / 2 : nb;
     // Lanes per row (8..64).  A matrix that fits in one pass of the resident
@@ -436,20 +474,20 @@ static hipError_t launch_pair(const uint8_t *w, const void *xq, float *y, int64_
     // per-row overhead in the persistent loop).
     if (n <= 16384) {
         if (nu > 64)
-            return launch_l<64, 4, PAIR, F32>(w, xq, y, n, nb, s);
+            return launch_l<64, 4, PAIR, F32>(w, xq, y, n, nb, ep, s);
         if (nu > 32)
-            return launch_l<32, 2, PAIR, F32>(w, xq, y, n, nb, s);
+            return launch_l<32, 2, PAIR, F32>(w, xq, y, n, nb, ep, s);
         if (nu > 16)
-            return launch_l<16, 2, PAIR, F32>(w, xq, y, n, nb, s);
-        return launch_l<8, 2, PAIR, F32>(w, xq, y, n, nb, s);
+            return launch_l<16, 2, PAIR, F32>(w, xq, y, n, nb, ep, s);
+        return launch_l<8, 2, PAIR, F32>(w, xq, y, n, nb, ep, s);
     }
     if (nu > 128)
-        return launch_l<64, 4, PAIR, F32>(w, xq, y, n, nb, s);
+        return launch_l<64, 4, PAIR, F32>(w, xq, y, n, nb, ep, s);
     if (nu > 64)
-        return launch_l<32, 4, PAIR, F32>(w, xq, y, n, nb, s);
+        return launch_l<32, 4, PAIR, F32>(w, xq, y, n, nb, ep, s);
     if (nu > 32)
-        return launch_l<16, 4, PAIR, F32>(w, xq, y, n, nb, s);
-    return launch_l<8, 4, PAIR, F32>(w, xq, y, n, nb, s);
+        return launch_l<16, 4, PAIR, F32>(w, xq, y, n, nb, ep, s);
+    return launch_l<8, 4, PAIR, F32>(w, xq, y, n, nb, ep, s);
 }
 
 hipError_t launch_q4_0_q8_0_gemv(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k,
@@ -459,6 +497,97 @@ hipError_t launch_q4_0_q8_0_gemv(const uint8_t *w, const uint8_t *xq, float *y, 
     if (nb % 2 == 0)
         return launch_pair<true>(w, xq, y, n, nb, s);
     return launch_pair<false>(w, xq, y, n, nb, s);
+}
+
+hipError_t launch_q4_0_q8_0_gemv_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k,
+                                        const LinearEpilogue &ep, hipStream_t s)
+{
+    const int nb = (int)(k / 32);
+    if (nb % 2 == 0)
+        return launch_pair<true, false>(w, xq, y, n, nb, s, ep);
+    return launch_pair<false, false>(w, xq, y, n, nb, s, ep);
+}
+
+// ------------------------------------------------------------------ gated decode
+// y_j = act(x . Wg_j) * (x . Wu_j), m = 1: the GEMV above with each lane
+// group holding the same units of row j of both matrices, so the product is
+// formed where the two sums are.  One launch and one staging of the activation
+// row for both matrices; the weight stream (twice 18/32 bytes a weight) bounds
+// it.  Two units per lane and matrix: four loads in flight, as in the GEMV.
+template <int L, bool PAIR>
+__global__ __launch_bounds__(kGemvThreads) void q4_0_gated_gemv_kernel(const uint8_t *__restrict__ wg,
+                                                                       const uint8_t *__restrict__ wu,
+                                                                       const uint8_t *xq, int act,
+                                                                       float *__restrict__ y, int64_t n, int nb)
+{
+    extern __shared__ u32x4 smem[];
+    constexpr int R = 64 / L, U = 2, WAVES = kGemvThreads / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane / L, r = lane % L;
+    const int nu = PAIR ? nb / 2 : nb;
+    const int chunks = (nu + U * L - 1) / (U * L);
+    const int64_t row_bytes = (int64_t)nb * 18;
+
+    ActRaw araw;
+    stage_q8_load(xq, nb, araw);
+    asm volatile("" ::: "memory"); // keep these loads ahead of the weight loads
+
+    const int64_t row = ((int64_t)blockIdx.x * WAVES + wave) * R + g;
+    GemvRaw<U> cg, cu;
+    gemv_load<L, U, PAIR>(wg, row, n, row_bytes, nu, 0, r, cg);
+    gemv_load<L, U, PAIR>(wu, row, n, row_bytes, nu, 0, r, cu);
+    const ActLds a = stage_q8_finish(xq, nb, araw, smem);
+
+    float sg = 0.0f, su = 0.0f;
+    for (int c = 0; c < chunks; c++) {
+        GemvRaw<U> ng, nu_;
+        if (c + 1 < chunks) {
+            gemv_load<L, U, PAIR>(wg, row, n, row_bytes, nu, (c + 1) * U * L, r, ng);
+            gemv_load<L, U, PAIR>(wu, row, n, row_bytes, nu, (c + 1) * U * L, r, nu_);
+        }
+        sg += gemv_compute<L, U, PAIR>(cg, row, n, row_bytes, nu, c * U * L, r, a);
+        su += gemv_compute<L, U, PAIR>(cu, row, n, row_bytes, nu, c * U * L, r, a);
+        cg = ng;
+        cu = nu_;
+    }
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) {
+        sg += __shfl_xor(sg, off);
+        su += __shfl_xor(su, off);
+    }
+    if (row < n && r == 0)
+        y[row] = activate(sg, act) * su;
+}
+
+template <int L>
+static hipError_t launch_gated_l(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                 int64_t n, int nb, hipStream_t s)
+{
+    constexpr int rows = 64 / L * (kGemvThreads / 64);
+    const int64_t grid = (n + rows - 1) / rows;
+    if (grid > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    const dim3 gd((unsigned)grid), bd(kGemvThreads);
+    if (nb % 2 == 0)
+        hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, true>), gd, bd, q4_gemv_lds_bytes(nb), s, wg, wu, xq, act, y,
+                           n, nb);
+    else
+        hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, false>), gd, bd, q4_gemv_lds_bytes(nb), s, wg, wu, xq, act, y,
+                           n, nb);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_0_gated_gemv(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                  int64_t n, int64_t k, hipStream_t s)
+{
+    const int nb = (int)(k / 32), nu = nb % 2 == 0 ? nb / 2 : nb;
+    if (nu > 64)
+        return launch_gated_l<64>(wg, wu, xq, act, y, n, nb, s);
+    if (nu > 32)
+        return launch_gated_l<32>(wg, wu, xq, act, y, n, nb, s);
+    if (nu > 16)
+        return launch_gated_l<16>(wg, wu, xq, act, y, n, nb, s);
+    return launch_gated_l<8>(wg, wu, xq, act, y, n, nb, s);
 }
 
 // ------------------------------------------------------------------ decode-packed Q4_0 weights
@@ -1045,9 +1174,10 @@ __device__ __forceinline__ void gm_compute(const GemvRaw<U> raw[RW], int64_t row
     }
 }
 
-template <int M, int RW, int U, bool PAIR, bool F32>
+template <int M, int RW, int U, bool PAIR, bool F32, class EP>
 __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *__restrict__ w, const void *xin,
-                                                                  float *__restrict__ y, int64_t m, int64_t n, int nb)
+                                                                  float *__restrict__ y, int64_t m, int64_t n, int nb,
+                                                                  EP ep)
 {
     __shared__ GmLds<M, U, PAIR> s;
     constexpr int CB = GmLds<M, U, PAIR>::CB;
@@ -1098,13 +1228,13 @@ __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *
             for (int off = kGmL / 2; off > 0; off >>= 1)
                 v += __shfl_xor(v, off);
             if (r == 0 && row0 + q < n && a < m)
-                y[(int64_t)a * n + row0 + q] = v;
+                y[(int64_t)a * n + row0 + q] = epilogue(ep, v, a, row0 + q, n);
         }
 }
 
-template <int RW, int U, bool F32>
+template <int RW, int U, bool F32, class EP>
 static hipError_t launch_gm_l(const uint8_t *w, const void *xin, float *y, int64_t m, int64_t n, int nb,
-                              hipStream_t s)
+                              const EP &ep, hipStream_t s)
 {
     constexpr int R = 64 / kGmL * RW; // weight rows per wave
     const int64_t groups = (n + R - 1) / R;
@@ -1115,9 +1245,10 @@ static hipError_t launch_gm_l(const uint8_t *w, const void *xin, float *y, int64
 #define QLL_GM(MM)                                                                                                    \
     do {                                                                                                              \
         if (nb % 2 == 0)                                                                                              \
-            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, true, F32>), gd, bd, 0, s, w, xin, y, m, n, nb);        \
+            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, true, F32, EP>), gd, bd, 0, s, w, xin, y, m, n, nb, ep); \
         else                                                                                                          \
-            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, false, F32>), gd, bd, 0, s, w, xin, y, m, n, nb);       \
+            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, false, F32, EP>), gd, bd, 0, s, w, xin, y, m, n, nb,     \
+                               ep);                                                                                   \
     } while (0)
     if (m <= 1)
         QLL_GM(1);
@@ -1135,33 +1266,57 @@ static hipError_t launch_gm_l(const uint8_t *w, const void *xin, float *y, int64
 // or 128 with f32 activations, whose in-launch quantization each workgroup
 // repeats (measured: at n = 14336 the f32 entry runs 1.3 to 2.6 times faster
 // with 64-row workgroups, at n = 4096 1.4 to 1.6 times slower).
-template <bool F32>
+template <bool F32, class EP = PlainEpilogue>
 static hipError_t launch_gm(const uint8_t *w, const void *xin, float *y, int64_t m, int64_t n, int64_t k,
-                            hipStream_t s)
+                            hipStream_t s, const EP &ep = EP{})
 {
     const int nb = (int)(k / 32);
     if (n >= (F32 ? 128 : 512) * 64)
-        return launch_gm_l<4, 1, F32>(w, xin, y, m, n, nb, s);
+        return launch_gm_l<4, 1, F32>(w, xin, y, m, n, nb, ep, s);
     // two rows per lane once the LDS reads bound (m > 2) and the matrix is
     // tall enough to keep workgroups for them (4096 -> 14336 at m = 8: 17.6
     // against 26.0 us; m = 4: 12.4 against 14.5; at n = 4096 the grid gets
     // too small: 16.2 against 12.9 us)
     if (!F32 && m > 2 && n >= 8192)
-        return launch_gm_l<2, 1, F32>(w, xin, y, m, n, nb, s);
-    return launch_gm_l<1, 4, F32>(w, xin, y, m, n, nb, s);
+        return launch_gm_l<2, 1, F32>(w, xin, y, m, n, nb, ep, s);
+    return launch_gm_l<1, 4, F32>(w, xin, y, m, n, nb, ep, s);
 }
 
-hipError_t launch_q4_0_q8_0_gemv_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
-                                   hipStream_t s)
+// The small-m kernels' own entries, by epilogue.
+static hipError_t gemv_one(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k, const PlainEpilogue &,
+                           hipStream_t s)
+{
+    return launch_q4_0_q8_0_gemv(w, xq, y, n, k, s);
+}
+static hipError_t gemv_one(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k,
+                           const LinearEpilogue &ep, hipStream_t s)
+{
+    return launch_q4_0_q8_0_gemv_linear(w, xq, y, n, k, ep, s);
+}
+static hipError_t small_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                          const PlainEpilogue &, hipStream_t s)
+{
+    return launch_q4_0_q8_0_small_m_mfma(w, xq, y, m, n, k, s);
+}
+static hipError_t small_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                          const LinearEpilogue &ep, hipStream_t s)
+{
+    return launch_q4_0_q8_0_small_m_mfma_linear(w, xq, y, m, n, k, ep, s);
+}
+
+template <class EP>
+static hipError_t launch_small(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                               const EP &ep, hipStream_t s)
 {
     if (m > kMaxMMfma || (m == 1 && k <= kMaxKQ4Gemv)) {
         // groups of at most 32 activation rows (a last group of one row: the
         // GEMV); each group's outputs are its own rows of y
         if (m == 1)
-            return launch_q4_0_q8_0_gemv(w, xq, y, n, k, s);
+            return gemv_one(w, xq, y, n, k, ep, s);
         for (int64_t a0 = 0; a0 < m; a0 += kMaxMMfma) {
             const int64_t mm = m - a0 < kMaxMMfma ? m - a0 : kMaxMMfma;
-            const hipError_t e = launch_q4_0_q8_0_gemv_m(w, xq + a0 * (k / 32) * 34, y + a0 * n, mm, n, k, s);
+            const hipError_t e =
+                launch_small(w, xq + a0 * (k / 32) * 34, y + a0 * n, mm, n, k, ep.rows(a0, n), s);
             if (e != hipSuccess)
                 return e;
         }
@@ -1173,16 +1328,29 @@ hipError_t launch_q4_0_q8_0_gemv_m(const uint8_t *w, const uint8_t *xq, float *y
     // 4096 -> 128256 at m = 2 / 4: 57 / 67.5 against 65 / 71.6 us)
     const bool gemv_style = (m == 2 && n >= 8192) || (m <= 4 && n >= 32768);
     if (m >= 2 && k >= kMinKMfma && k < kMaxKMfma && !gemv_style)
-        return launch_q4_0_q8_0_small_m_mfma(w, xq, y, m, n, k, s);
+        return small_m(w, xq, y, m, n, k, ep, s);
     // rows of fewer than eight blocks (or very long rows at m <= 8): the
     // kernel above by groups of at most eight activation rows
     for (int64_t a0 = 0; a0 < m; a0 += kMaxMSmall) {
         const int64_t mm = m - a0 < kMaxMSmall ? m - a0 : kMaxMSmall;
-        const hipError_t e = launch_gm<false>(w, xq + a0 * (k / 32) * 34, y + a0 * n, mm, n, k, s);
+        const hipError_t e =
+            launch_gm<false>(w, xq + a0 * (k / 32) * 34, y + a0 * n, mm, n, k, s, ep.rows(a0, n));
         if (e != hipSuccess)
             return e;
     }
     return hipSuccess;
+}
+
+hipError_t launch_q4_0_q8_0_gemv_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                                   hipStream_t s)
+{
+    return launch_small(w, xq, y, m, n, k, PlainEpilogue{}, s);
+}
+
+hipError_t launch_q4_0_q8_0_gemv_m_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                          int64_t k, const LinearEpilogue &ep, hipStream_t s)
+{
+    return launch_small(w, xq, y, m, n, k, ep, s);
 }
 
 // The single launch wins only where the weights take one pass of the

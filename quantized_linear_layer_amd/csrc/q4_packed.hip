@@ -35,6 +35,7 @@
 // over 128-row tiles of X: 6144 bytes per chunk (h codes as planes 0 and 1,
 // then l codes as planes 0 and 1) and 128 binary16 d_x per chunk.
 #include "common.h"
+#include "q4_store.h"
 
 namespace qll {
 
@@ -96,8 +97,11 @@ __device__ __forceinline__ void store_planes(uint8_t *chunk, int r, const uint32
 // ------------------------------------------------------------------ repack
 
 // One thread per (tile row r, chunk c), r fastest so the plane stores of a
-// wave are contiguous.  Rows at or past n get zero codes and d_w = 0.
-__global__ __launch_bounds__(256) void q4p_repack_kernel(const uint8_t *__restrict__ w, uint8_t *__restrict__ codes,
+// wave are contiguous.  Rows at or past n get zero codes and d_w = 0.  GATED:
+// tile t holds rows 64 t .. 64 t + 63 of w, then the same rows of wu.
+template <bool GATED>
+__global__ __launch_bounds__(256) void q4p_repack_kernel(const uint8_t *__restrict__ w,
+                                                         const uint8_t *__restrict__ wu, uint8_t *__restrict__ codes,
                                                          uint16_t *__restrict__ dws, int64_t n, int nb, int64_t total)
 {
     const int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -107,11 +111,12 @@ __global__ __launch_bounds__(256) void q4p_repack_kernel(const uint8_t *__restri
     const int64_t c = g >> 7;
     const int64_t t = c / nb;
     const int b = (int)(c % nb);
-    const int64_t row = t * PBN + r;
+    const int64_t row = GATED ? t * (PBN / 2) + (r & 63) : t * PBN + r;
+    const uint8_t *src = GATED && r >= 64 ? wu : w;
     uint32_t code[32];
     uint16_t d = 0;
     if (row < n) {
-        const uint8_t *blk = w + (row * nb + b) * 18;
+        const uint8_t *blk = src + (row * nb + b) * 18;
         d = (uint16_t)(blk[0] | (blk[1] << 8));
 #pragma unroll
         for (int i = 0; i < 16; i++) {
@@ -134,17 +139,34 @@ size_t q4_0_repacked_bytes(int64_t n, int64_t k)
     return (size_t)nt * (size_t)(k / 32) * (kPWChunk + kPSChunk);
 }
 
-hipError_t launch_q4_0_repack(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
+template <bool GATED>
+static hipError_t launch_repack(const uint8_t *w, const uint8_t *wu, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
 {
     const int nb = (int)(k / 32);
-    const int64_t nt = (n + PBN - 1) / PBN;
+    const int64_t rows = GATED ? PBN / 2 : PBN, nt = (n + rows - 1) / rows;
     const int64_t total = nt * nb * PBN;
     uint16_t *dws = reinterpret_cast<uint16_t *>(wp + (size_t)nt * nb * kPWChunk);
     const int64_t grid = (total + 255) / 256;
     if (grid > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(q4p_repack_kernel, dim3((unsigned)grid), dim3(256), 0, s, w, wp, dws, n, nb, total);
+    hipLaunchKernelGGL(q4p_repack_kernel<GATED>, dim3((unsigned)grid), dim3(256), 0, s, w, wu, wp, dws, n, nb, total);
     return hipGetLastError();
+}
+
+hipError_t launch_q4_0_repack(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
+{
+    return launch_repack<false>(w, nullptr, wp, n, k, s);
+}
+
+size_t q4_0_repacked_gated_bytes(int64_t n, int64_t k)
+{
+    return (size_t)((n + PBN / 2 - 1) / (PBN / 2)) * (size_t)(k / 32) * (kPWChunk + kPSChunk);
+}
+
+hipError_t launch_q4_0_repack_gated(const uint8_t *wg, const uint8_t *wu, uint8_t *wp, int64_t n, int64_t k,
+                                    hipStream_t s)
+{
+    return launch_repack<true>(wg, wu, wp, n, k, s);
 }
 
 // ------------------------------------------------------------------ activations
@@ -311,6 +333,16 @@ __device__ __forceinline__ T q4p_lds(const QLL_LDS char *base, uint32_t off)
     return *reinterpret_cast<const QLL_LDS T *>(base + off);
 }
 
+// Weight rows between a wave's two column tiles.  Gated products: a tile's
+// rows 0..63 are gate rows and 64..127 the up projection's for the same
+// outputs (q4p_repack_kernel), and a wave takes 32 of each.
+template <class EP>
+struct Q4pCols {
+    static constexpr int kStep = EP::kGated ? 64 : 32;
+    static constexpr int kOut = EP::kGated ? PBN / 2 : PBN; // output columns of a workgroup
+    static __device__ __forceinline__ int first(int wave) { return (wave & 1) * (EP::kGated ? 32 : 64); }
+};
+
 // Per-lane LDS byte offsets from the start of a stage buffer; reads add only
 // immediates (block, tile) to them.
 struct Q4pLaneOff {
@@ -319,7 +351,7 @@ struct Q4pLaneOff {
     uint32_t dx, dw;
 };
 
-template <bool Q8W>
+template <bool Q8W, int STEP>
 __device__ __forceinline__ Q4pLaneOff q4p_lane_offsets(int wm, int wn, int lane)
 {
     typedef Q4pLds<Q8W> Lds;
@@ -332,7 +364,7 @@ __device__ __forceinline__ Q4pLaneOff q4p_lane_offsets(int wm, int wn, int lane)
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         o.x1[i] = (uint32_t)(offsetof(Lds, xs) + lh * 3072 + 2048 + 8 * (wm + 32 * i + lr));
-        o.w1[i] = (uint32_t)(offsetof(Lds, wq) + 2048 + 8 * (wn + 32 * i + lr));
+        o.w1[i] = (uint32_t)(offsetof(Lds, wq) + 2048 + 8 * (wn + STEP * i + lr));
     }
     // Opaque to the compiler, so that the two 8-byte reads of a block (tiles
     // 0 and 1, different base registers) are not merged into one read of
@@ -368,20 +400,20 @@ __device__ __forceinline__ void q4p_read_a(const QLL_LDS char *base, const Q4pLa
     a.s = __builtin_bit_cast(f16x4, u32x2{d, 0u});
 }
 
-template <bool Q8W>
+template <bool Q8W, int STEP>
 __device__ __forceinline__ void q4p_read_b(const QLL_LDS char *base, const Q4pLaneOff &o, int kb, int j,
                                            Q4pB<Q8W> &b)
 {
     constexpr int WC = PFmt<Q8W>::kWChunk;
-    const u32x4 w0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + 512 * j);
+    const u32x4 w0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + 16 * STEP * j);
     const u32x2 w1 = q4p_lds<u32x2>(base, o.w1[j] + kb * WC);
     b.m = i32x8{(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], 0, 0};
     if (Q8W) { // the l half of the weight codes, 3072 bytes further
-        const u32x4 v0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + 3072 + 512 * j);
+        const u32x4 v0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + 3072 + 16 * STEP * j);
         const u32x2 v1 = q4p_lds<u32x2>(base, o.w1[j] + kb * WC + 3072);
         b.l = i32x8{(int)v0[0], (int)v0[1], (int)v0[2], (int)v0[3], (int)v1[0], (int)v1[1], 0, 0};
     }
-    const uint32_t d = q4p_lds<uint16_t>(base, o.dw + kb * 2 * PBN + 64 * j);
+    const uint32_t d = q4p_lds<uint16_t>(base, o.dw + kb * 2 * PBN + 2 * STEP * j);
     b.s = __builtin_bit_cast(f16x4, u32x2{d, 0u});
 }
 
@@ -436,7 +468,7 @@ __device__ __forceinline__ void q4p_sync()
 // read this buffer whole (block 1 is in registers) and the next one is
 // complete, so the loads of the stage three ahead go into this buffer at
 // once, and steps 5..7 read the next stage's block 0.
-template <bool Q8W, int CUR>
+template <bool Q8W, int STEP, int CUR>
 __device__ __forceinline__ void q4p_stage(Q4pLds<Q8W> *lds, const Q4pLaneOff &lo, uint32_t scale_a,
                                           f32x16 (&acc)[2][2], Q4pA (&A)[2], Q4pB<Q8W> (&B)[2], const Q4pSrc &src,
                                           int nb, int b_load, int swave)
@@ -460,10 +492,10 @@ __device__ __forceinline__ void q4p_stage(Q4pLds<Q8W> *lds, const Q4pLaneOff &lo
             if ((t & 3) == 1)
                 q4p_read_a(rb, lo, rkb, 0, A[0]);
             if ((t & 3) == 2)
-                q4p_read_b<Q8W>(rb, lo, rkb, 0, B[0]);
+                q4p_read_b<Q8W, STEP>(rb, lo, rkb, 0, B[0]);
             if ((t & 3) == 3) {
                 q4p_read_a(rb, lo, rkb, 1, A[1]);
-                q4p_read_b<Q8W>(rb, lo, rkb, 1, B[1]);
+                q4p_read_b<Q8W, STEP>(rb, lo, rkb, 1, B[1]);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -481,21 +513,22 @@ __device__ __forceinline__ void q4p_stage(Q4pLds<Q8W> *lds, const Q4pLaneOff &lo
     }
 }
 
-template <bool Q8W>
+template <bool Q8W, class EP>
 __global__ __launch_bounds__(kPThreads) void packed_gemm_kernel(const uint8_t *__restrict__ wcodes,
                                                                 const uint16_t *__restrict__ dws, Q4pPrep prep,
                                                                 float *__restrict__ y, int64_t m, int64_t n, int nb,
-                                                                int per_split)
+                                                                int per_split, EP ep)
 {
-    constexpr int DMA = PFmt<Q8W>::kDma;
+    typedef Q4pCols<EP> Cols;
+    constexpr int DMA = PFmt<Q8W>::kDma, STEP = Cols::kStep;
     __shared__ Q4pLds<Q8W> lds[PNBUF];
     int64_t m_tile, n_tile;
-    q4p_tile(prep.mp / PBM, (n + PBN - 1) / PBN, m_tile, n_tile);
-    const int64_t m0 = m_tile * PBM, n0 = n_tile * PBN;
+    q4p_tile(prep.mp / PBM, (n + Cols::kOut - 1) / Cols::kOut, m_tile, n_tile);
+    const int64_t m0 = m_tile * PBM, n0 = n_tile * Cols::kOut;
     const int b_begin = blockIdx.y * per_split;
-    y += (int64_t)blockIdx.y * m * n;
+    y += (int64_t)blockIdx.y * (EP::kGated ? 2 * m * n : m * n);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+    const int wm = (wave >> 1) * 64, wn = Cols::first(wave);
 
     f32x16 acc[2][2];
 #pragma unroll
@@ -505,7 +538,7 @@ __global__ __launch_bounds__(kPThreads) void packed_gemm_kernel(const uint8_t *_
             acc[i][j] = f32x16{};
 
     const int nstages = per_split / PKB;
-    const Q4pLaneOff lo = q4p_lane_offsets<Q8W>(wm, wn, lane);
+    const Q4pLaneOff lo = q4p_lane_offsets<Q8W, STEP>(wm, wn, lane);
     const uint32_t scale_a = lane < 32 ? kE8M0Sixteen : kE8M0One;
 
     // Three stage buffers, stage st computed from buffer st % 3 (the loop
@@ -529,32 +562,22 @@ __global__ __launch_bounds__(kPThreads) void packed_gemm_kernel(const uint8_t *_
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         q4p_read_a((const QLL_LDS char *)&lds[0], lo, 0, i, A[i]);
-        q4p_read_b<Q8W>((const QLL_LDS char *)&lds[0], lo, 0, i, B[i]);
+        q4p_read_b<Q8W, STEP>((const QLL_LDS char *)&lds[0], lo, 0, i, B[i]);
     }
     int st = 0;
     for (; st + PNBUF <= nstages; st += PNBUF) {
-        q4p_stage<Q8W, 0>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 3) * PKB, swave);
-        q4p_stage<Q8W, 1>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 4) * PKB, swave);
-        q4p_stage<Q8W, 2>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 5) * PKB, swave);
+        q4p_stage<Q8W, STEP, 0>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 3) * PKB, swave);
+        q4p_stage<Q8W, STEP, 1>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 4) * PKB, swave);
+        q4p_stage<Q8W, STEP, 2>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 5) * PKB, swave);
     }
     if (st < nstages)
-        q4p_stage<Q8W, 0>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 3) * PKB, swave);
+        q4p_stage<Q8W, STEP, 0>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 3) * PKB, swave);
     if (st + 1 < nstages)
-        q4p_stage<Q8W, 1>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 4) * PKB, swave);
+        q4p_stage<Q8W, STEP, 1>(lds, lo, scale_a, acc, A, B, src, nb, b_begin + (st + 4) * PKB, swave);
     // no load may still be writing this workgroup's LDS when it ends
     __builtin_amdgcn_s_waitcnt(0x7 << 4); // vmcnt(0) expcnt(7) lgkmcnt(0)
 
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++)
-#pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int64_t row = m0 + wm + 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                const int64_t col = n0 + wn + 32 * j + (lane & 31);
-                if (row < m && col < n)
-                    y[row * n + col] = 0.5f * acc[i][j][v]; // the scale tiles are 2 d_x d_w
-            }
+    q4_tile_store(ep, acc, y, m, n, m0 + wm, n0 + wn, lane);
 }
 
 
@@ -603,11 +626,12 @@ size_t q4_0_packed_gemm_workspace(int64_t m, int64_t n, int64_t k)
     return q4p_plan(m, n, k).total;
 }
 
-template <bool Q8W>
-static hipError_t launch_packed_gemm(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
-                                     void *ws, hipStream_t s)
+// The activation prepass, then the GEMM (see launch_gemm_kernel of the direct
+// layout for which epilogue runs where).
+template <bool Q8W, class EP>
+static hipError_t launch_packed_kernel(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                       int64_t k, const Q4pPlan &plan, const EP &ep, void *ws, hipStream_t s)
 {
-    const Q4pPlan plan = q4p_plan(m, n, k);
     uint8_t *base = static_cast<uint8_t *>(ws);
     Q4pPrep prep;
     prep.x = base + plan.x_off;
@@ -621,22 +645,58 @@ static hipError_t launch_packed_gemm(const uint8_t *wp, const uint8_t *xq, float
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int64_t nt = (n + PBN - 1) / PBN;
+    const int64_t nt = (n + Q4pCols<EP>::kOut - 1) / Q4pCols<EP>::kOut;
     const uint16_t *dws = reinterpret_cast<const uint16_t *>(wp + (size_t)nt * nb * PFmt<Q8W>::kWChunk);
     const int64_t tiles = nt * (plan.mp / PBM);
     float *out = plan.splits > 1 ? reinterpret_cast<float *>(base) : y;
-    hipLaunchKernelGGL(packed_gemm_kernel<Q8W>, dim3((unsigned)tiles, (unsigned)plan.splits), dim3(kPThreads), 0, s,
-                       wp, dws, prep, out, m, n, nb, plan.per_split);
-    e = hipGetLastError();
+    hipLaunchKernelGGL((packed_gemm_kernel<Q8W, EP>), dim3((unsigned)tiles, (unsigned)plan.splits), dim3(kPThreads),
+                       0, s, wp, dws, prep, out, m, n, nb, plan.per_split, ep);
+    return hipGetLastError();
+}
+
+template <bool Q8W>
+static hipError_t launch_packed_gemm(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                                     void *ws, hipStream_t s)
+{
+    const Q4pPlan plan = q4p_plan(m, n, k);
+    const hipError_t e = launch_packed_kernel<Q8W>(wp, xq, y, m, n, k, plan, PlainEpilogue{}, ws, s);
     if (e != hipSuccess || plan.splits == 1)
         return e;
-    return launch_sum_splits(out, y, m * n, plan.splits, s);
+    return launch_sum_splits(static_cast<const float *>(ws), y, m * n, plan.splits, s);
 }
 
 hipError_t launch_q4_0_packed_gemm(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
                                    void *ws, hipStream_t s)
 {
     return launch_packed_gemm<false>(wp, xq, y, m, n, k, ws, s);
+}
+
+hipError_t launch_q4_0_packed_gemm_linear(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                          int64_t k, const LinearEpilogue &ep, void *ws, hipStream_t s)
+{
+    const Q4pPlan plan = q4p_plan(m, n, k);
+    if (plan.splits == 1)
+        return launch_packed_kernel<false>(wp, xq, y, m, n, k, plan, ep, ws, s);
+    const hipError_t e = launch_packed_kernel<false>(wp, xq, y, m, n, k, plan, PlainEpilogue{}, ws, s);
+    if (e != hipSuccess)
+        return e;
+    return launch_sum_splits_linear(static_cast<const float *>(ws), y, m, n, plan.splits, ep, s);
+}
+
+// Gated: a GEMM with 128 weight rows per 64 output columns.
+static Q4pPlan gated_packed_plan(int64_t m, int64_t n, int64_t k) { return q4p_plan(m, (n + 63) / 64 * 128, k); }
+
+size_t q4_0_packed_gated_workspace(int64_t m, int64_t n, int64_t k) { return gated_packed_plan(m, n, k).total; }
+
+hipError_t launch_q4_0_packed_gated(const uint8_t *wp, const uint8_t *xq, int act, float *y, int64_t m, int64_t n,
+                                    int64_t k, void *ws, hipStream_t s)
+{
+    const Q4pPlan plan = gated_packed_plan(m, n, k);
+    const hipError_t e =
+        launch_packed_kernel<false>(wp, xq, y, m, n, k, plan, GatedEpilogue{nullptr, act, plan.splits > 1}, ws, s);
+    if (e != hipSuccess || plan.splits == 1)
+        return e;
+    return launch_sum_splits_gated(static_cast<const float *>(ws), y, m, n, plan.splits, act, s);
 }
 
 // ------------------------------------------------------------------ Q8_0 weights

@@ -54,13 +54,17 @@ constexpr int sm_mt(int mp) { return mp > 16 ? mp / 16 : 1; }
 // exactly as stored (144 bytes of weights, 272 of activations: whole 16-byte
 // pieces), rows one after another (so every load instruction reads
 // contiguous runs), each region padded to whole 1 KB loads.
-template <int T, int MP>
+template <int T, int MP, bool GATED = false>
 struct SmLayout {
     static constexpr int WR = 16 * T;                          // weight rows
     static constexpr int WROW = 18 * kSmSB, XROW = 34 * kSmSB; // bytes per row
     static constexpr int WP = WROW / 16, XP = XROW / 16;       // 16-byte pieces per row: 9 and 17
-    // wave-wide loads per stage (64 lanes of 16 bytes each)
-    static constexpr int NW = (WR * WP + 63) / 64, NX = (MP * XP + 63) / 64;
+    // wave-wide loads per stage (64 lanes of 16 bytes each).  GATED (T = 2):
+    // tile 0 is the gate's, tile 1 the up projection's, each with loads and a
+    // padded region of its own, since their rows lie in two matrices.
+    static constexpr int NG = (16 * WP + 63) / 64;
+    static constexpr int NW = GATED ? 2 * NG : (WR * WP + 63) / 64, NX = (MP * XP + 63) / 64;
+    static constexpr int TILE = GATED ? 1024 * NG : 16 * WROW; // bytes from one weight tile to the next
     static constexpr int DMA = NW + NX;
     static constexpr int W = 0;             // [WR weight rows][144 B], then padding
     static constexpr int X = W + 1024 * NW; // [MP activation rows][272 B], then padding
@@ -72,22 +76,25 @@ struct SmLayout {
 // of load i writes LDS bytes 16 (64 i + l) of its region, so it fetches
 // piece 64 i + l of the rows laid end to end; lanes past the last piece
 // fetch the first piece again into the padding.
-template <int T, int MP>
+// Gated: the offsets of one matrix's rows serve both.
+template <int T, int MP, bool GATED = false>
 struct SmOff {
-    uint32_t w[SmLayout<T, MP>::NW], x[SmLayout<T, MP>::NX];
+    static constexpr int NW = GATED ? SmLayout<T, MP, true>::NG : SmLayout<T, MP>::NW;
+    uint32_t w[NW], x[SmLayout<T, MP>::NX];
 };
 
-template <int T, int MP>
-__device__ __forceinline__ void sm_offsets(int64_t m, int64_t n, int nb, int64_t row0, SmOff<T, MP> &o)
+template <int T, int MP, bool GATED = false>
+__device__ __forceinline__ void sm_offsets(int64_t m, int64_t n, int nb, int64_t row0, SmOff<T, MP, GATED> &o)
 {
-    using L = SmLayout<T, MP>;
+    using L = SmLayout<T, MP, GATED>;
+    constexpr int WR = GATED ? 16 : L::WR;
     const int lane = threadIdx.x & 63;
     // n, m < 2^31 and k < 2^24 at the boundary: 32 rows of weights or of
     // activations span far less than 4 GiB
     const uint32_t rb = (uint32_t)nb * 18u, xr = (uint32_t)nb * 34u;
 #pragma unroll
-    for (int i = 0; i < L::NW; i++) {
-        const int p = 64 * i + lane < L::WR * L::WP ? 64 * i + lane : 0, r = p / L::WP, c = p % L::WP;
+    for (int i = 0; i < SmOff<T, MP, GATED>::NW; i++) {
+        const int p = 64 * i + lane < WR * L::WP ? 64 * i + lane : 0, r = p / L::WP, c = p % L::WP;
         const uint32_t rr = (uint32_t)(row0 + r < n ? r : n - 1 - row0);
         o.w[i] = rr * rb + 16u * (uint32_t)c;
     }
@@ -128,18 +135,25 @@ __device__ __forceinline__ void sm_wait_lds()
 
 // The loads of the stage whose first block is be (be + 8 <= nb), into the
 // buffer at lds: L::DMA wave-wide loads, all lanes active.
-template <int T, int MP>
-__device__ __forceinline__ void sm_load(const uint8_t *wt, const uint8_t *xq, int be, const SmOff<T, MP> &o,
-                                        uint32_t lds)
+// wt2: the up projection's first row (gated).
+template <int T, int MP, bool GATED = false>
+__device__ __forceinline__ void sm_load(const uint8_t *wt, const uint8_t *wt2, const uint8_t *xq, int be,
+                                        const SmOff<T, MP, GATED> &o, uint32_t lds)
 {
-    using L = SmLayout<T, MP>;
+    using L = SmLayout<T, MP, GATED>;
     const uint8_t *wb = wt + 18 * (int64_t)be, *xb = xq + 34 * (int64_t)be;
 #pragma unroll
     for (int i = 0; i < L::NX; i++)
         sm_dma16(xb, o.x[i], lds + L::X + 1024 * i);
 #pragma unroll
-    for (int i = 0; i < L::NW; i++)
+    for (int i = 0; i < SmOff<T, MP, GATED>::NW; i++)
         sm_dma16(wb, o.w[i], lds + L::W + 1024 * i);
+    if constexpr (GATED) {
+        const uint8_t *wb2 = wt2 + 18 * (int64_t)be;
+#pragma unroll
+        for (int i = 0; i < L::NG; i++)
+            sm_dma16(wb2, o.w[i], lds + L::W + L::TILE + 1024 * i);
+    }
 }
 
 // A stage's weight rows and activation rows in LDS.
@@ -191,11 +205,11 @@ __device__ __forceinline__ uint32_t sm_half_bits(const QLL_LDS_M char *p, uint32
 // (v_mfma_f32_16x16x16_f16 with only k = 0 nonzero: lanes 0..15 hold their
 // row's d_w and d_x, the others zeros), every entry the exact f32 product of
 // two halves.
-template <int T, int MP, int BL>
+template <int T, int MP, bool GATED, int BL>
 __device__ __forceinline__ void sm_mfma(const SmBufs &s, uint32_t width, i32x4 (&p)[T * sm_mt(MP)],
                                         f32x4_m (&sc)[T * sm_mt(MP)])
 {
-    using L = SmLayout<T, MP>;
+    using L = SmLayout<T, MP, GATED>;
     constexpr bool ODD = BL & 1;
     constexpr int MT = sm_mt(MP);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -205,7 +219,7 @@ __device__ __forceinline__ void sm_mfma(const SmBufs &s, uint32_t width, i32x4 (
     f16x4_m sa[T];
 #pragma unroll
     for (int u = 0; u < T; u++) {
-        const QLL_LDS_M char *wrow = s.w + (16 * u + r) * L::WROW + 18 * BL;
+        const QLL_LDS_M char *wrow = s.w + u * L::TILE + r * L::WROW + 18 * BL;
         const uint32_t wt = sm_word<!ODD>(wrow + 2 + 4 * g) ^ 0x88888888u;
         aop[u] = (long)(((uint64_t)(wt & 0xf0f0f0f0u) << 32) | ((wt << 4) & 0xf0f0f0f0u));
         sa[u] = __builtin_bit_cast(f16x4_m, (uint64_t)sm_half_bits<ODD>(wrow, width));
@@ -234,31 +248,31 @@ __device__ __forceinline__ void sm_apply(const i32x4 (&p)[N], const f32x4_m (&sc
             acc[t][i] += sc[t][i] * (float)p[t][i];
 }
 
-template <int T, int MP, int BL>
+template <int T, int MP, bool GATED, int BL>
 __device__ __forceinline__ void sm_block(const SmBufs &s, uint32_t width, float (&acc)[T * sm_mt(MP)][4])
 {
     i32x4 p[T * sm_mt(MP)];
     f32x4_m sc[T * sm_mt(MP)];
-    sm_mfma<T, MP, BL>(s, width, p, sc);
+    sm_mfma<T, MP, GATED, BL>(s, width, p, sc);
     sm_apply(p, sc, acc);
 }
 
 // Blocks B0 .. B0 + G - 1: every block's products first, then their sums
 // in block order (the matrix core's latency covered by the later blocks).
-template <int T, int MP, int B0, int G>
+template <int T, int MP, bool GATED, int B0, int G>
 __device__ __forceinline__ void sm_group(const SmBufs &s, uint32_t width, float (&acc)[T * sm_mt(MP)][4])
 {
     constexpr int N = T * sm_mt(MP);
     i32x4 p[G][N];
     f32x4_m sc[G][N];
-    if constexpr (G > 0) sm_mfma<T, MP, B0 + 0>(s, width, p[0], sc[0]);
-    if constexpr (G > 1) sm_mfma<T, MP, B0 + 1>(s, width, p[1], sc[1]);
-    if constexpr (G > 2) sm_mfma<T, MP, B0 + 2>(s, width, p[2], sc[2]);
-    if constexpr (G > 3) sm_mfma<T, MP, B0 + 3>(s, width, p[3], sc[3]);
-    if constexpr (G > 4) sm_mfma<T, MP, B0 + 4>(s, width, p[4], sc[4]);
-    if constexpr (G > 5) sm_mfma<T, MP, B0 + 5>(s, width, p[5], sc[5]);
-    if constexpr (G > 6) sm_mfma<T, MP, B0 + 6>(s, width, p[6], sc[6]);
-    if constexpr (G > 7) sm_mfma<T, MP, B0 + 7>(s, width, p[7], sc[7]);
+    if constexpr (G > 0) sm_mfma<T, MP, GATED, B0 + 0>(s, width, p[0], sc[0]);
+    if constexpr (G > 1) sm_mfma<T, MP, GATED, B0 + 1>(s, width, p[1], sc[1]);
+    if constexpr (G > 2) sm_mfma<T, MP, GATED, B0 + 2>(s, width, p[2], sc[2]);
+    if constexpr (G > 3) sm_mfma<T, MP, GATED, B0 + 3>(s, width, p[3], sc[3]);
+    if constexpr (G > 4) sm_mfma<T, MP, GATED, B0 + 4>(s, width, p[4], sc[4]);
+    if constexpr (G > 5) sm_mfma<T, MP, GATED, B0 + 5>(s, width, p[5], sc[5]);
+    if constexpr (G > 6) sm_mfma<T, MP, GATED, B0 + 6>(s, width, p[6], sc[6]);
+    if constexpr (G > 7) sm_mfma<T, MP, GATED, B0 + 7>(s, width, p[7], sc[7]);
 #pragma unroll
     for (int b = 0; b < G; b++)
         sm_apply(p[b], sc[b], acc);
@@ -266,48 +280,55 @@ __device__ __forceinline__ void sm_group(const SmBufs &s, uint32_t width, float 
 
 // Blocks lo .. 7 of a stage buffer (lo > 0 only for a row's last stage,
 // which starts inside the one before).
-template <int T, int MP>
+template <int T, int MP, bool GATED = false>
 __device__ __forceinline__ void sm_stage(const SmBufs &s, int lo, uint32_t width, float (&acc)[T * sm_mt(MP)][4])
 {
     if (lo == 0) { // uniform
         constexpr int G = kSmGroup / (T * sm_mt(MP)); // 8, 4 or 2 blocks
         static_assert(G >= 1 && kSmSB % G == 0, "whole groups per stage");
-        sm_group<T, MP, 0, G>(s, width, acc);
-        if constexpr (G < kSmSB) sm_group<T, MP, G % kSmSB, G>(s, width, acc);
-        if constexpr (3 * G <= kSmSB) sm_group<T, MP, (2 * G) % kSmSB, G>(s, width, acc);
-        if constexpr (4 * G <= kSmSB) sm_group<T, MP, (3 * G) % kSmSB, G>(s, width, acc);
+        sm_group<T, MP, GATED, 0, G>(s, width, acc);
+        if constexpr (G < kSmSB) sm_group<T, MP, GATED, G % kSmSB, G>(s, width, acc);
+        if constexpr (3 * G <= kSmSB) sm_group<T, MP, GATED, (2 * G) % kSmSB, G>(s, width, acc);
+        if constexpr (4 * G <= kSmSB) sm_group<T, MP, GATED, (3 * G) % kSmSB, G>(s, width, acc);
         return;
     }
-    if (lo <= 1) sm_block<T, MP, 1>(s, width, acc);
-    if (lo <= 2) sm_block<T, MP, 2>(s, width, acc);
-    if (lo <= 3) sm_block<T, MP, 3>(s, width, acc);
-    if (lo <= 4) sm_block<T, MP, 4>(s, width, acc);
-    if (lo <= 5) sm_block<T, MP, 5>(s, width, acc);
-    if (lo <= 6) sm_block<T, MP, 6>(s, width, acc);
-    sm_block<T, MP, 7>(s, width, acc);
+    if (lo <= 1) sm_block<T, MP, GATED, 1>(s, width, acc);
+    if (lo <= 2) sm_block<T, MP, GATED, 2>(s, width, acc);
+    if (lo <= 3) sm_block<T, MP, GATED, 3>(s, width, acc);
+    if (lo <= 4) sm_block<T, MP, GATED, 4>(s, width, acc);
+    if (lo <= 5) sm_block<T, MP, GATED, 5>(s, width, acc);
+    if (lo <= 6) sm_block<T, MP, GATED, 6>(s, width, acc);
+    sm_block<T, MP, GATED, 7>(s, width, acc);
 }
 
-template <int T, int MP, int KS>
+// Gated (T = 2): weight tile 0 is 16 rows of the gate, tile 1 the same rows of
+// the up projection, so the two products of an output meet in the last sum.
+template <int T, int MP, int KS, class EP>
 __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_t *__restrict__ w,
                                                                     const uint8_t *__restrict__ xq,
                                                                     float *__restrict__ y, int64_t m, int64_t n,
-                                                                    int nb)
+                                                                    int nb, EP ep)
 {
-    using L = SmLayout<T, MP>;
+    constexpr bool GATED = EP::kGated;
+    static_assert(!GATED || T == 2, "a gate tile and an up tile");
+    using L = SmLayout<T, MP, GATED>;
+    constexpr int OR = GATED ? 16 : L::WR; // output columns of a workgroup
     constexpr int MT = sm_mt(MP), N = T * MT;
     static_assert(N * 4 * 64 * 4 <= kSmNS * L::STAGE, "a wave's partial tile fits in its stage buffers");
     static_assert(kSmNS == 1 || kSmNS == 2, "one stage in flight at most");
     __shared__ __attribute__((aligned(16))) char stage[KS][kSmNS][L::STAGE];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row0 = (int64_t)blockIdx.x * L::WR;
-    const uint8_t *wt = w + row0 * ((int64_t)nb * 18);
+    const int64_t row0 = (int64_t)blockIdx.x * OR;
+    const uint8_t *wt = w + row0 * ((int64_t)nb * 18), *wt2 = nullptr;
+    if constexpr (GATED)
+        wt2 = ep.wu + row0 * ((int64_t)nb * 18);
     // this wave's stages: s0 .. s1 - 1 of the row's nst
     const int nst = (nb + kSmSB - 1) / kSmSB;
     const int s0 = nst * wave / KS, s1 = nst * (wave + 1) / KS;
     const int blast = nb - kSmSB; // first block of the row's last stage
-    SmOff<T, MP> o;
-    sm_offsets<T, MP>(m, n, nb, row0, o);
+    SmOff<T, MP, GATED> o;
+    sm_offsets<T, MP, GATED>(m, n, nb, row0, o);
     const QLL_LDS_M char *buf = (const QLL_LDS_M char *)&stage[wave][0][0];
     const uint32_t lds = (uint32_t)(uintptr_t)buf;
 
@@ -323,7 +344,7 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
 #pragma unroll
     for (int j = 0; j < kSmNS; j++)
         if (s0 + j < s1)
-            sm_load<T, MP>(wt, xq, min((s0 + j) * kSmSB, blast), o, lds + j * L::STAGE);
+            sm_load<T, MP, GATED>(wt, wt2, xq, min((s0 + j) * kSmSB, blast), o, lds + j * L::STAGE);
     for (int s2 = s0; s2 < s1; s2 += kSmNS) {
 #pragma unroll
         for (int j = 0; j < kSmNS; j++) { // buffer j: a constant offset
@@ -335,10 +356,10 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
             else
                 sm_wait<0>();
             const SmBufs sb{buf + j * L::STAGE + L::W, buf + j * L::STAGE + L::X};
-            sm_stage<T, MP>(sb, s * kSmSB - min(s * kSmSB, blast), width, acc);
+            sm_stage<T, MP, GATED>(sb, s * kSmSB - min(s * kSmSB, blast), width, acc);
             if (s + kSmNS < s1) {
                 sm_wait_lds(); // this buffer's reads have completed
-                sm_load<T, MP>(wt, xq, min((s + kSmNS) * kSmSB, blast), o, lds + j * L::STAGE);
+                sm_load<T, MP, GATED>(wt, wt2, xq, min((s + kSmNS) * kSmSB, blast), o, lds + j * L::STAGE);
             }
         }
     }
@@ -353,17 +374,28 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
         for (int i = 0; i < 4; i++)
             (*reinterpret_cast<Part *>(&stage[wave][0][0]))[4 * t + i][lane] = acc[t][i];
     __syncthreads();
-    for (int oi = threadIdx.x; oi < 256 * N; oi += 64 * KS) {
-        // activation row col and weight row row of the workgroup's tile
-        const int col = oi / L::WR, row = oi % L::WR;
-        const int u = row >> 4, t = col >> 4;
-        const int reg = 4 * (u * MT + t) + (row & 3), ln = 16 * ((row & 15) >> 2) + (col & 15);
+    // the sum over the waves of register reg of lane ln, an output's 16 P sum
+    const auto total = [&](int reg, int ln) {
         float v = (*reinterpret_cast<const Part *>(&stage[0][0][0]))[reg][ln];
 #pragma unroll
         for (int q = 1; q < KS; q++)
             v += (*reinterpret_cast<const Part *>(&stage[q][0][0]))[reg][ln];
-        if (col < m && row0 + row < n)
-            y[(int64_t)col * n + row0 + row] = v * 0.0625f; // the sums were of 16 P
+        return v * 0.0625f;
+    };
+    for (int oi = threadIdx.x; oi < 16 * MT * OR; oi += 64 * KS) {
+        // activation row col and weight row row of the workgroup's tile
+        const int col = oi / OR, row = oi % OR;
+        const int u = row >> 4, t = col >> 4;
+        const int reg = 4 * (u * MT + t) + (row & 3), ln = 16 * ((row & 15) >> 2) + (col & 15);
+        if constexpr (GATED) {
+            const float g = total(reg, ln), up = total(reg + 4 * MT, ln);
+            if (col < m && row0 + row < n)
+                y[(int64_t)col * n + row0 + row] = activate(g, ep.act) * up;
+        } else {
+            const float v = total(reg, ln);
+            if (col < m && row0 + row < n)
+                y[(int64_t)col * n + row0 + row] = epilogue(ep, v, col, row0 + row, n);
+        }
     }
 }
 
@@ -398,11 +430,11 @@ __device__ __forceinline__ void sm_wait_n(int n)
 // landed), computes, and meets them again before the buffer it read is
 // refilled.  The activation rows are read from L2 once per R T weight tiles
 // instead of once per tile, and a wave needs only its weight rows' LDS.
-template <int T, int MP, int R>
+template <int T, int MP, int R, class EP>
 __global__ __launch_bounds__(64 * R) void q4_0_small_m_shared_kernel(const uint8_t *__restrict__ w,
                                                                      const uint8_t *__restrict__ xq,
                                                                      float *__restrict__ y, int64_t m, int64_t n,
-                                                                     int nb)
+                                                                     int nb, EP ep)
 {
     using L = SmLayout<T, MP>;
     constexpr int MT = sm_mt(MP), N = T * MT, WB = 1024 * L::NW, XB = 1024 * L::NX;
@@ -476,25 +508,38 @@ __global__ __launch_bounds__(64 * R) void q4_0_small_m_shared_kernel(const uint8
         const int u = row >> 4, t = col >> 4;
         const int reg = 4 * (u * MT + t) + (row & 3), ln = 16 * ((row & 15) >> 2) + (col & 15);
         if (col < m && row0 + row < n)
-            y[(int64_t)col * n + row0 + row] = part[reg][ln] * 0.0625f; // the sums were of 16 P
+            y[(int64_t)col * n + row0 + row] =
+                epilogue(ep, part[reg][ln] * 0.0625f, col, row0 + row, n); // the sums were of 16 P
     }
 }
 
 // Workgroups of one split that fit on a CU at once (the LDS bounds them).
-template <int T, int MP>
+template <int T, int MP, bool GATED = false>
 constexpr int sm_per_cu(int ks)
 {
-    return 160 * 1024 / (ks * kSmNS * SmLayout<T, MP>::STAGE);
+    return 160 * 1024 / (ks * kSmNS * SmLayout<T, MP, GATED>::STAGE);
 }
 
-template <int T, int MP, int KS>
-static void launch_sm(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int nb, hipStream_t s)
+// The arguments every variant takes.
+template <class EP>
+struct SmArgs {
+    const uint8_t *w, *xq;
+    float *y;
+    int64_t m, n;
+    int nb;
+    EP ep;
+    hipStream_t s;
+};
+
+template <int T, int MP, int KS, class EP>
+static void launch_sm(const SmArgs<EP> &a)
 {
     // splits whose workgroup does not fit are never chosen
-    if constexpr (sm_per_cu<T, MP>(KS) >= 1) {
-        const unsigned tiles = (unsigned)((n + 16 * T - 1) / (16 * T));
-        hipLaunchKernelGGL((q4_0_small_m_mfma_kernel<T, MP, KS>), dim3(tiles), dim3(64 * KS), 0, s, w, xq, y, m, n,
-                           nb);
+    if constexpr (sm_per_cu<T, MP, EP::kGated>(KS) >= 1) {
+        const int rows = EP::kGated ? 16 : 16 * T;
+        const unsigned tiles = (unsigned)((a.n + rows - 1) / rows);
+        hipLaunchKernelGGL((q4_0_small_m_mfma_kernel<T, MP, KS, EP>), dim3(tiles), dim3(64 * KS), 0, a.s, a.w, a.xq,
+                           a.y, a.m, a.n, a.nb, a.ep);
     }
 }
 
@@ -535,15 +580,14 @@ static int small_m_mfma_split(int64_t m, int64_t n, int64_t k)
     return 1;
 }
 
-template <int MP>
-static void launch_sm_ks(int ks, const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int nb,
-                         hipStream_t s)
+template <int T, int MP, class EP>
+static void launch_sm_ks(int ks, const SmArgs<EP> &a)
 {
     switch (ks) {
-    case 1: launch_sm<1, MP, 1>(w, xq, y, m, n, nb, s); break;
-    case 2: launch_sm<1, MP, 2>(w, xq, y, m, n, nb, s); break;
-    case 4: launch_sm<1, MP, 4>(w, xq, y, m, n, nb, s); break;
-    default: launch_sm<1, MP, 8>(w, xq, y, m, n, nb, s); break;
+    case 1: launch_sm<T, MP, 1>(a); break;
+    case 2: launch_sm<T, MP, 2>(a); break;
+    case 4: launch_sm<T, MP, 4>(a); break;
+    default: launch_sm<T, MP, 8>(a); break;
     }
 }
 
@@ -560,44 +604,94 @@ static bool small_m_mfma_shared(int64_t m, int64_t n, int64_t k)
     return n >= 32768 && m > 4;
 }
 
-template <int MP>
-static void launch_sh(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int nb, hipStream_t s)
+template <int MP, class EP>
+static void launch_sh(const SmArgs<EP> &a)
 {
-    const unsigned groups = (unsigned)((n + 16 * kShT * kShR - 1) / (16 * kShT * kShR));
-    hipLaunchKernelGGL((q4_0_small_m_shared_kernel<kShT, MP, kShR>), dim3(groups), dim3(64 * kShR), 0, s, w, xq, y,
-                       m, n, nb);
+    const unsigned groups = (unsigned)((a.n + 16 * kShT * kShR - 1) / (16 * kShT * kShR));
+    hipLaunchKernelGGL((q4_0_small_m_shared_kernel<kShT, MP, kShR, EP>), dim3(groups), dim3(64 * kShR), 0, a.s, a.w,
+                       a.xq, a.y, a.m, a.n, a.nb, a.ep);
 }
 
-hipError_t launch_q4_0_q8_0_small_m_mfma(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
-                                         int64_t k, hipStream_t s)
+template <class EP>
+static hipError_t launch_small_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
+                                 const EP &ep, hipStream_t s)
 {
     if (m < 1 || m > kMaxMMfma || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
     if ((n + 15) / 16 > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    const int nb = (int)(k / 32), mp = sm_rows(m);
+    const int mp = sm_rows(m);
+    const SmArgs<EP> a{w, xq, y, m, n, (int)(k / 32), ep, s};
     if (small_m_mfma_shared(m, n, k)) { // m > 4: 8, 16 or 32 staged rows
         if (mp == 8)
-            launch_sh<8>(w, xq, y, m, n, nb, s);
+            launch_sh<8>(a);
         else if (mp == 16)
-            launch_sh<16>(w, xq, y, m, n, nb, s);
+            launch_sh<16>(a);
         else
-            launch_sh<32>(w, xq, y, m, n, nb, s);
+            launch_sh<32>(a);
     } else if (small_m_mfma_row_tiles(m, n, k) == 2) { // m > 16: 32 staged rows
         if (small_m_mfma_split(m, n, k) == 1)
-            launch_sm<2, 32, 1>(w, xq, y, m, n, nb, s);
+            launch_sm<2, 32, 1>(a);
         else
-            launch_sm<2, 32, 2>(w, xq, y, m, n, nb, s);
+            launch_sm<2, 32, 2>(a);
     } else {
         const int ks = small_m_mfma_split(m, n, k);
         switch (mp) {
-        case 4: launch_sm_ks<4>(ks, w, xq, y, m, n, nb, s); break;
-        case 8: launch_sm_ks<8>(ks, w, xq, y, m, n, nb, s); break;
-        case 16: launch_sm_ks<16>(ks, w, xq, y, m, n, nb, s); break;
-        default: launch_sm_ks<32>(ks, w, xq, y, m, n, nb, s); break;
+        case 4: launch_sm_ks<1, 4>(ks, a); break;
+        case 8: launch_sm_ks<1, 8>(ks, a); break;
+        case 16: launch_sm_ks<1, 16>(ks, a); break;
+        default: launch_sm_ks<1, 32>(ks, a); break;
         }
     }
     return hipGetLastError();
+}
+
+hipError_t launch_q4_0_q8_0_small_m_mfma(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                         int64_t k, hipStream_t s)
+{
+    return launch_small_m(w, xq, y, m, n, k, PlainEpilogue{}, s);
+}
+
+hipError_t launch_q4_0_q8_0_small_m_mfma_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n,
+                                                int64_t k, const LinearEpilogue &ep, hipStream_t s)
+{
+    return launch_small_m(w, xq, y, m, n, k, ep, s);
+}
+
+// Gated products: waves per 16 output columns by the rule above (the largest
+// split whose workgroups are resident at once, two stages a wave at least).
+template <int MP>
+static void launch_gated_mp(const SmArgs<GatedEpilogue> &a)
+{
+    const int64_t tiles = (a.n + 15) / 16, nst = (a.nb + kSmSB - 1) / kSmSB;
+    int ks = 8;
+    while (ks > 1 && (nst < 2 * ks || tiles > 256 * sm_per_cu<2, MP, true>(ks)))
+        ks /= 2;
+    launch_sm_ks<2, MP>(ks, a);
+}
+
+hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
+                                     int64_t m, int64_t n, int64_t k, hipStream_t s)
+{
+    if (k < kMinKMfma || k >= kMaxKMfma)
+        return hipErrorInvalidValue;
+    if ((n + 15) / 16 > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    for (int64_t a0 = 0; a0 < m; a0 += kMaxMMfma) {
+        const int64_t mm = m - a0 < kMaxMMfma ? m - a0 : kMaxMMfma;
+        const SmArgs<GatedEpilogue> a{wg, xq + a0 * (k / 32) * 34, y + a0 * n, mm, n, (int)(k / 32),
+                                      GatedEpilogue{wu, act, false}, s};
+        switch (sm_rows(mm)) {
+        case 4: launch_gated_mp<4>(a); break;
+        case 8: launch_gated_mp<8>(a); break;
+        case 16: launch_gated_mp<16>(a); break;
+        default: launch_gated_mp<32>(a); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace qll

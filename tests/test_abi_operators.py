@@ -68,3 +68,77 @@ def test_binding_refuses_host_and_short_tensors():
         qll.qll_rmsnorm_q8_0(x, 0, None, x, 1e-5, None, x, 1, 64)
     with pytest.raises(ValueError, match="CUDA"):
         qll.qll_rmsnorm_i8_rows(x, 0, None, x, 1e-5, None, x, x, x, 1, 64)
+
+
+def refusals(f, ok, at, expect):
+    """f with the arguments `at` (index: value) of `ok` replaced returns expect."""
+    a = list(ok)
+    for i, v in at.items():
+        a[i] = v
+    assert f(*a) == expect, at
+
+
+def test_linear(L):
+    big = 2 ** 40
+    ok = [GOOD, GOOD, GOOD, 2, GOOD, GOOD, 100, 8, 256, GOOD, big, None]
+    for f, ws_null in ((L.qll_q4_0_q8_0_linear, WORKSPACE), (L.qll_q4_0_repacked_q8_0_linear, NULL)):
+        for i in (0, 1, 5):
+            refusals(f, ok, {i: NUL}, NULL)
+        for i in (0, 1, 2, 4, 5, 9):
+            refusals(f, ok, {i: MIS}, ALIGN)
+        for act in (-1, 5):
+            refusals(f, ok, {3: act}, VALUE)
+        for m, n, k in ((0, 8, 256), (100, 0, 256), (100, 8, 0), (100, 8, 48), (100, 8, 2 ** 24), (2 ** 31, 8, 256)):
+            refusals(f, ok, {6: m, 7: n, 8: k}, SHAPE)
+        refusals(f, ok, {9: NUL, 10: 0}, ws_null)
+        refusals(f, ok, {10: 16}, WORKSPACE)
+    # one row: the GEMV's limit on k
+    refusals(L.qll_q4_0_q8_0_linear, ok, {6: 1, 8: 49152 + 32}, SHAPE)
+    for m, n, k in ((1, 4096, 4096), (64, 4096, 4096), (65, 257, 1024), (512, 4096, 14336)):
+        assert qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k) == \
+            qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_Q8_0_GEMM, m, n, k)
+    assert qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, 2, 8, 40) == SIZE_MAX
+
+
+def test_gated(L):
+    big = 2 ** 40
+    ok = [GOOD, GOOD, GOOD, 4, GOOD, 100, 8, 256, GOOD, big, None]
+    f = L.qll_q4_0_q8_0_gated
+    for i in (0, 1, 2, 4):
+        refusals(f, ok, {i: NUL}, NULL)
+    for i in (0, 1, 2, 4, 8):
+        refusals(f, ok, {i: MIS}, ALIGN)
+    for act in (-1, 5):
+        refusals(f, ok, {3: act}, VALUE)
+    for m, n, k in ((0, 8, 256), (100, -1, 256), (100, 8, 33), (100, 8, 2 ** 24), (1, 8, 2 ** 24)):
+        refusals(f, ok, {5: m, 6: n, 7: k}, SHAPE)
+    refusals(f, ok, {8: NUL, 9: 0}, WORKSPACE)
+    refusals(f, ok, {5: 2, 7: 224, 8: NUL, 9: 0}, WORKSPACE)  # rows under eight blocks take the GEMM
+    refusals(f, ok, {9: 16}, WORKSPACE)
+    ok = [GOOD, GOOD, 4, GOOD, 100, 8, 256, GOOD, big, None]
+    f = L.qll_q4_0_repacked_q8_0_gated
+    for i in (0, 1, 3, 7):
+        refusals(f, ok, {i: NUL}, NULL)
+    for i in (0, 1, 3, 7):
+        refusals(f, ok, {i: MIS}, ALIGN)
+    refusals(f, ok, {2: 9}, VALUE)
+    refusals(f, ok, {6: 2 ** 24}, SHAPE)
+    refusals(f, ok, {8: 255}, WORKSPACE)
+    ok = [GOOD, GOOD, GOOD, 8, 64, None]
+    f = L.qll_q4_0_repack_gated
+    for i in range(3):
+        refusals(f, ok, {i: NUL}, NULL)
+        refusals(f, ok, {i: MIS}, ALIGN)
+    for n, k in ((0, 64), (8, 40)):
+        refusals(f, ok, {3: n, 4: k}, SHAPE)
+    W = qll.qll_workspace_bytes
+    for m, n, k in ((1, 14336, 4096), (1, 64, 32), (1, 64, 65536), (64, 14336, 4096), (2, 7, 256)):
+        assert W(qll.QLL_OP_Q4_0_GATED, m, n, k) == 0
+    for m, n, k in ((2, 7, 224), (65, 14336, 4096)):
+        assert 0 < W(qll.QLL_OP_Q4_0_GATED, m, n, k) < SIZE_MAX
+    assert W(qll.QLL_OP_Q4_0_REPACKED_GATED, 1, 1, 32) > 0
+    for op in (qll.QLL_OP_Q4_0_GATED, qll.QLL_OP_Q4_0_REPACKED_GATED):
+        assert W(op, 2, 7, 40) == SIZE_MAX and W(op, 2, 7, 2 ** 24) == SIZE_MAX
+    assert qll.qll_q4_0_repacked_gated_bytes(1, 32) == 3328
+    assert qll.qll_q4_0_repacked_gated_bytes(65, 64) == 2 * 2 * 3328
+    assert qll.qll_q4_0_repacked_gated_bytes(8, 48) == SIZE_MAX
