@@ -82,7 +82,8 @@ enum {
     QLL_OP_Q4_0_GEMV_F32 = 10, /* qll_q4_0_q8_0_gemv_f32's optional workspace */
     QLL_OP_Q4_0_LINEAR = 11,         /* qll_q4_0_q8_0_linear (the repacked form: QLL_OP_Q4_0_REPACKED_GEMM) */
     QLL_OP_Q4_0_GATED = 12,          /* qll_q4_0_q8_0_gated */
-    QLL_OP_Q4_0_REPACKED_GATED = 13  /* qll_q4_0_repacked_q8_0_gated */
+    QLL_OP_Q4_0_REPACKED_GATED = 13, /* qll_q4_0_repacked_q8_0_gated */
+    QLL_OP_TOKEN_LOGPROBS = 14       /* qll_token_logprobs: n is its v, k its top */
 };
 
 /* Bytes of device workspace `op` needs at this shape (0 if none); SIZE_MAX if
@@ -431,6 +432,30 @@ int qll_rmsnorm_q8_0(const void *x, int dtype, const void *residual, const float
  * Any k >= 1. */
 int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
                         int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k, void *stream);
+
+/* ------------------------------------------------- token log probabilities */
+
+/* What is read off the logits of a vocabulary projection.  For every row
+ * x[0..v) of logits: [m][v] of type dtype (QLL_DTYPE_F32, _BF16 or _F16), with
+ * M = max x, S = sum_j exp(x_j - M) and log p_j = x_j - M - log S:
+ *   logprob[m][t]      log p of the row's t given tokens (int32 ids); NaN for
+ *                      an id outside [0, v) (padding), which is not read
+ *   entropy[m]         -sum_j p_j log p_j, in nats
+ *   top_ids[m][top],   the `top` largest logits, largest first, the lower
+ *   top_logprob        index first among equal ones, and their log p
+ * t == 0 leaves tokens and logprob unused (may be NULL), top == 0 top_ids and
+ * top_logprob; entropy may be NULL.  A logit of -inf is a masked token: p = 0,
+ * log p = -inf.  In a row with nothing but -inf, or with NaN or +inf in it,
+ * every float output is NaN (its top_ids are the lowest indices, resp.
+ * unspecified ids below v).
+ * Sums are f32 over a wave's logits, joined in f64; outputs are within
+ * 2^-18 (1 + |log p|) of exact ones.  1 <= v <= 2^20, t >= 0,
+ * 0 <= top <= min(64, v) (else QLL_ERR_SHAPE); QLL_ERR_VALUE for an unknown
+ * dtype.  ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_TOKEN_LOGPROBS, m,
+ * v, top) bytes; contents on return are unspecified. */
+int qll_token_logprobs(const void *logits, int dtype, const int32_t *tokens, int64_t t, float *logprob,
+                       float *entropy, int64_t top, int32_t *top_ids, float *top_logprob, int64_t m, int64_t v,
+                       void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

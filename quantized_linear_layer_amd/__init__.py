@@ -28,6 +28,7 @@ QLL_OP_Q4_0_GEMV_F32 = 10
 QLL_OP_Q4_0_LINEAR = 11
 QLL_OP_Q4_0_GATED = 12
 QLL_OP_Q4_0_REPACKED_GATED = 13
+QLL_OP_TOKEN_LOGPROBS = 14
 QLL_ACT_NONE, QLL_ACT_RELU, QLL_ACT_GELU, QLL_ACT_GELU_TANH, QLL_ACT_SILU = 0, 1, 2, 3, 4
 QLL_DTYPE_F32, QLL_DTYPE_BF16, QLL_DTYPE_F16 = 0, 1, 2
 
@@ -77,6 +78,7 @@ def load(path=LIB_PATH):
         "qll_q4_0_q8_0_gated": [P, P, P, ctypes.c_int, P, I, I, I, P, S, P],
         "qll_q4_0_repack_gated": [P, P, P, I, I, P],
         "qll_q4_0_repacked_q8_0_gated": [P, P, ctypes.c_int, P, I, I, I, P, S, P],
+        "qll_token_logprobs": [P, ctypes.c_int, P, I, P, P, I, P, P, I, I, P, S, P],
         "qll_rmsnorm_q8_0": [P, ctypes.c_int, P, P, F, P, P, I, I, P],
         "qll_rmsnorm_i8_rows": [P, ctypes.c_int, P, P, F, P, P, P, P, I, I, P],
     }
@@ -410,3 +412,17 @@ def qll_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_s
           _ptr(weight, k * 4, "weight"), float(eps), _ptr(h, nb, "h"), _ptr(xq, m * k, "xq"),
           _ptr(act_scale, m * 4, "act_scale"), _ptr(act_sum, m * 4, "act_sum"), m, k,
           _on(stream, x, residual, weight, h, xq, act_scale, act_sum))
+
+
+# ----------------------------------------------------------------- token log probabilities
+
+def qll_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids, top_logprob, m, v, ws=None,
+                       stream=None):
+    """Log probabilities of t given tokens a row (int32 ids), entropy, and the
+    top largest; tokens and logprob may be None at t = 0, top_ids and
+    top_logprob at top = 0, entropy always."""
+    wsp, wsb = _op_ws(ws, QLL_OP_TOKEN_LOGPROBS, m, v, top)
+    _call("qll_token_logprobs", _ptr(logits, m * v * _esize(dtype), "logits"), int(dtype),
+          _ptr(tokens, m * t * 4, "tokens"), t, _ptr(logprob, m * t * 4, "logprob"), _ptr(entropy, m * 4, "entropy"),
+          top, _ptr(top_ids, m * top * 4, "top_ids"), _ptr(top_logprob, m * top * 4, "top_logprob"), m, v, wsp, wsb,
+          _on(stream, logits, tokens, logprob, entropy, top_ids, top_logprob, ws))

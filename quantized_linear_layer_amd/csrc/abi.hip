@@ -91,6 +91,11 @@ static_assert((int)QLL_ACT_NONE == (int)QLL_A_NONE && (int)QLL_ACT_RELU == (int)
                   (int)QLL_ACT_SILU == (int)QLL_A_SILU,
               "activation codes");
 
+bool logprob_dims_ok(int64_t m, int64_t v, int64_t top)
+{
+    return dims_ok(m, v) && v <= kMaxLpVocab && top >= 0 && top <= kMaxLpTop && top <= v;
+}
+
 hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
 } // namespace
@@ -166,6 +171,10 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (op == QLL_OP_Q4_0_REPACKED_GATED)
             return q4_0_packed_gated_workspace(m, n, k);
         return q4_gated_small(m, k) ? 0 : q4_0_gated_gemm_workspace(m, n, k);
+    case QLL_OP_TOKEN_LOGPROBS:
+        if (!logprob_dims_ok(m, n, k))
+            return SIZE_MAX;
+        return token_logprobs_workspace(m, n, k);
     default:
         return SIZE_MAX;
     }
@@ -689,6 +698,27 @@ int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const fl
         return rc;
     return launched(launch_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_sum, m, k,
                                            as_stream(stream)));
+}
+
+int qll_token_logprobs(const void *logits, int dtype, const int32_t *tokens, int64_t t, float *logprob,
+                       float *entropy, int64_t top, int32_t *top_ids, float *top_logprob, int64_t m, int64_t v,
+                       void *ws, size_t ws_bytes, void *stream)
+{
+    if (!logits || !ws || (t > 0 && (!tokens || !logprob)) || (top > 0 && (!top_ids || !top_logprob)))
+        return QLL_ERR_NULL;
+    if (dtype < QLL_DTYPE_F32 || dtype > QLL_DTYPE_F16)
+        return QLL_ERR_VALUE;
+    if (!logprob_dims_ok(m, v, top) || t < 0 || (t > 0 && !dims_ok(m, t)))
+        return QLL_ERR_SHAPE;
+    if (!aligned16(logits) || !aligned16(tokens) || !aligned16(logprob) || !aligned16(entropy) ||
+        !aligned16(top_ids) || !aligned16(top_logprob) || !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (ws_bytes < token_logprobs_workspace(m, v, top))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids, top_logprob, m, v,
+                                          ws, as_stream(stream)));
 }
 
 } // extern "C"

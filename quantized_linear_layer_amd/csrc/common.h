@@ -300,6 +300,13 @@ hipError_t launch_rmsnorm_q8_0(const void *x, int dtype, const void *res, const 
 hipError_t launch_rmsnorm_i8_rows(const void *x, int dtype, const void *res, const float *w, float eps, void *h,
                                   int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k,
                                   hipStream_t s);
+// Token log probabilities, entropy and the `top` best of each row of logits.
+constexpr int64_t kMaxLpVocab = (int64_t)1 << 20, kMaxLpTop = 64;
+size_t token_logprobs_workspace(int64_t m, int64_t v, int64_t top);
+hipError_t launch_token_logprobs(const void *logits, int dtype, const int32_t *tokens, int64_t nt, float *logprob,
+                                 float *entropy, int64_t top, int32_t *top_ids, float *top_logprob, int64_t m,
+                                 int64_t v, void *ws, hipStream_t s);
+
 // Largest k the LDS-staged decode kernels accept (the activation of one row
 // is kept whole in LDS).
 constexpr int64_t kMaxKQ4Gemv = 49152;

@@ -142,3 +142,25 @@ def test_gated(L):
     assert qll.qll_q4_0_repacked_gated_bytes(1, 32) == 3328
     assert qll.qll_q4_0_repacked_gated_bytes(65, 64) == 2 * 2 * 3328
     assert qll.qll_q4_0_repacked_gated_bytes(8, 48) == SIZE_MAX
+
+
+def test_logprobs(L):
+    big = 2 ** 40
+    ok = [GOOD, 0, GOOD, 2, GOOD, GOOD, 5, GOOD, GOOD, 3, 1000, GOOD, big, None]
+    f = L.qll_token_logprobs
+    for i in (0, 2, 4, 7, 8, 11):
+        refusals(f, ok, {i: NUL}, NULL)
+    for i in (0, 2, 4, 5, 7, 8, 11):
+        refusals(f, ok, {i: MIS}, ALIGN)
+    for dtype in (-1, 3):
+        refusals(f, ok, {1: dtype}, VALUE)
+    for t, top, m, v in ((-1, 5, 3, 1000), (2, -1, 3, 1000), (2, 65, 3, 1000), (2, 5, 0, 1000), (2, 5, 3, 0),
+                         (2, 5, 3, 4), (2, 5, 3, 2 ** 20 + 1), (2 ** 31, 5, 3, 1000), (2, 5, 2 ** 31, 1000)):
+        refusals(f, ok, {3: t, 6: top, 9: m, 10: v}, SHAPE)
+    refusals(f, ok, {12: qll.qll_workspace_bytes(qll.QLL_OP_TOKEN_LOGPROBS, 3, 1000, 5) - 1}, WORKSPACE)
+    refusals(f, ok, {3: 0, 2: NUL, 4: NUL, 6: 0, 7: NUL, 8: NUL, 12: 0}, WORKSPACE)  # the parts left out are not asked for
+    W = qll.qll_workspace_bytes
+    assert W(qll.QLL_OP_TOKEN_LOGPROBS, 1, 1, 0) > 0
+    assert W(qll.QLL_OP_TOKEN_LOGPROBS, 1, 2 ** 20, 64) < SIZE_MAX
+    for m, v, top in ((0, 10, 1), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 2 ** 20 + 1, 1), (1, 10, -1)):
+        assert W(qll.QLL_OP_TOKEN_LOGPROBS, m, v, top) == SIZE_MAX
