@@ -1,10 +1,11 @@
 """Token log probabilities in 64 bits, with the error the kernel may make.
 
 u = 2^-24.  With d = M - x over the logits that count (exp(-80) is far below
-an f32 sum's rounding), log S is off by at most (40 + 8 max d) u: 32 f32
-additions in a lane and 6 across the wave, and per term the roundings of the
-difference, of its product with log2(e) and of that constant, each d u or
-less, and of exp2.  The entropy's sum of p d has that relative error too."""
+an f32 sum's rounding), log S is off by at most (40 + 8 max d) u: at most 16
+f32 additions (f64 beyond) and the weights that bring lanes, waves and
+segments to one reference, and per term the roundings of the difference, of
+its product with log2(e) and of that constant, each d u or less, and of
+exp2.  The entropy's sum of p d has that relative error too."""
 import numpy as np
 
 U = 2.0 ** -24
