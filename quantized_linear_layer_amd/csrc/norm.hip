@@ -46,11 +46,7 @@ __device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
 // f32 -> T, round to nearest even.
 __device__ __forceinline__ void narrow(float f, float &o) { o = f; }
 __device__ __forceinline__ void narrow(float f, _Float16 &o) { o = (_Float16)f; }
-__device__ __forceinline__ void narrow(float f, uint16_t &o)
-{
-    const uint32_t u = __float_as_uint(f);
-    o = f != f ? (uint16_t)0x7fc0 : (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
+__device__ __forceinline__ void narrow(float f, uint16_t &o) { o = __builtin_bit_cast(uint16_t, (__bf16)f); }
 
 // V consecutive elements at p (V = 4: aligned to four elements).
 template <int V, typename T>
@@ -87,18 +83,83 @@ __device__ __forceinline__ double code_factor(double a)
     return a > 0.0 ? 127.0 * r : 0.0;
 }
 
-// Half away from zero of 127 p / a as f64 arithmetic has it.  f = 127 / a to a
-// few 1e-16, so |p| f is within 1e-13 of the quotient: only within 1e-6 of a
-// border is the division itself needed (values drawn from few significant
-// bits do land on borders, and then the quotient is exactly k + 1/2).
-__device__ __forceinline__ int norm_code(double p, double a, double f)
+// 1 / sqrt(v), v > 0, the same way.
+__device__ __forceinline__ double inverse_root(double v)
 {
-    double t = fma(fabs(p), f, 0.5);
-    double c = floor(t);
-    if (fabs(t - c - 0.5) > 0.5 - 1e-6)
-        c = a > 0.0 ? floor(127.0 * fabs(p) / a + 0.5) : 0.0;
-    const int q = (int)c;
-    return p < 0.0 ? -q : q;
+    double r = __builtin_amdgcn_rsq(v);
+    r = fma(fma(-v * r, r, 1.0), 0.5 * r, r);
+    return fma(fma(-v * r, r, 1.0), 0.5 * r, r);
+}
+
+// The codes of V products, round-half-away(127 p / a) as f64 arithmetic has it,
+// f = 127 / a.  p f is within 1e-13 of the quotient: adding 1.5 2^52 rounds it to
+// the nearest integer, which then stands in the low bits, and only within 1e-6 of
+// a border is the division itself needed (values drawn from few significant bits
+// do land on borders, and then the quotient is exactly k + 1/2).
+template <int V>
+__device__ __forceinline__ void norm_codes(const double (&p)[V], double a, double f, int (&q)[V])
+{
+    constexpr double kMagic = 6755399441055744.0;
+    double y[V], worst = 0.0;
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        y[e] = fma(p[e], f, kMagic);
+        worst = fmax(worst, fabs(fma(p[e], f, kMagic - y[e])));
+        q[e] = (int)(uint32_t)__builtin_bit_cast(uint64_t, y[e]);
+    }
+    if (worst > 0.5 - 1e-6) {
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            const int c = a > 0.0 ? (int)floor(127.0 * fabs(p[e]) / a + 0.5) : 0;
+            q[e] = p[e] < 0.0 ? -c : c;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack4(const int (&q)[4])
+{
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)q[1], (uint32_t)q[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)q[3], (uint32_t)q[2], 0x04000c0cu);
+    return lo | hi;
+}
+
+// v as another lane of the same 16 has it: the neighbour (kXor1), the other pair
+// of the quad (kXor2), the other quad of eight lanes (kHalf: what holds after the
+// two before), the other eight of sixteen (kRow).
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalf = 0x141, kRow = 0x140;
+template <int CTRL>
+__device__ __forceinline__ double lane_f64(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int LANE>
+__device__ __forceinline__ double from_lane_f64(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, LANE);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), LANE);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Over the 64 lanes, in every lane.
+__device__ __forceinline__ double wave_sum(double v)
+{
+    v += lane_f64<kXor1>(v);
+    v += lane_f64<kXor2>(v);
+    v += lane_f64<kHalf>(v);
+    v += lane_f64<kRow>(v);
+    return (from_lane_f64<0>(v) + from_lane_f64<16>(v)) + (from_lane_f64<32>(v) + from_lane_f64<48>(v));
+}
+__device__ __forceinline__ double wave_max(double v)
+{
+    v = fmax(v, lane_f64<kXor1>(v));
+    v = fmax(v, lane_f64<kXor2>(v));
+    v = fmax(v, lane_f64<kHalf>(v));
+    v = fmax(v, lane_f64<kRow>(v));
+    return fmax(fmax(from_lane_f64<0>(v), from_lane_f64<16>(v)), fmax(from_lane_f64<32>(v), from_lane_f64<48>(v)));
 }
 
 // Sum (and, with MAX, the largest `mx`) over the TPR threads of a row; `red`:
@@ -106,12 +167,9 @@ __device__ __forceinline__ int norm_code(double p, double a, double f)
 template <int TPR, bool MAX>
 __device__ __forceinline__ void row_reduce(double &sum, double &mx, double (*red)[2])
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        sum += __shfl_xor(sum, off);
-        if (MAX)
-            mx = fmax(mx, __shfl_xor(mx, off));
-    }
+    sum = wave_sum(sum);
+    if (MAX)
+        mx = wave_max(mx);
     if constexpr (TPR > 64) {
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
@@ -156,17 +214,17 @@ __device__ __forceinline__ void norm_products(const Elems<V, T> &x, const Elems<
 __device__ __forceinline__ uint32_t block_codes(const double (&p)[4], double &a)
 {
     double mx = fmax(fmax(fabs(p[0]), fabs(p[1])), fmax(fabs(p[2]), fabs(p[3])));
-    mx = fmax(mx, __shfl_xor(mx, 1));
-    mx = fmax(mx, __shfl_xor(mx, 2));
-    mx = fmax(mx, __shfl_xor(mx, 4));
-    const double f = code_factor(mx);
-    uint32_t c = 0u;
-#pragma unroll
-    for (int e = 0; e < 4; e++)
-        c |= ((uint32_t)norm_code(p[e], mx, f) & 0xffu) << (8 * e);
+    mx = fmax(mx, lane_f64<kXor1>(mx));
+    mx = fmax(mx, lane_f64<kXor2>(mx));
+    mx = fmax(mx, lane_f64<kHalf>(mx));
+    int q[4];
+    norm_codes<4>(p, mx, code_factor(mx), q);
     a = mx;
-    return c;
+    return pack4(q);
 }
+
+// Pieces whose loads a thread has out at once.
+constexpr int kNormGroup = 4;
 
 // Dword that only promises 2-byte alignment (codes of a Q8_0 block).
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
@@ -187,11 +245,11 @@ __device__ __forceinline__ void store_scale(uint8_t *blk, double a, double scale
     *reinterpret_cast<uint16_t *>(blk) = float_to_half_bits(d);
 }
 
-// 127 rms / a as the int8 quantizer keeps it: a row whose scale is not finite,
+// 127 rms / a, v = rms^2, as the int8 quantizer keeps it: a row whose scale is not finite,
 // or that is all zeros, has scale 0.
-__device__ __forceinline__ float row_scale(double ss, int k, double eps, double a)
+__device__ __forceinline__ float row_scale(double v, double a)
 {
-    const float sc = a > 0.0 ? (float)(127.0 * sqrt(ss / (double)k + eps) / a) : 0.0f;
+    const float sc = a > 0.0 ? (float)(code_factor(a) * (v * inverse_root(v))) : 0.0f;
     return __builtin_isfinite(sc) ? sc : 0.0f;
 }
 
@@ -200,14 +258,12 @@ template <int V>
 __device__ __forceinline__ int store_i8(int8_t *q8, const double (&p)[V], double a, double f)
 {
     int q[V], sum = 0;
+    norm_codes<V>(p, a, f, q);
 #pragma unroll
-    for (int e = 0; e < V; e++) {
-        q[e] = norm_code(p[e], a, f);
+    for (int e = 0; e < V; e++)
         sum += q[e];
-    }
     if constexpr (V == 4)
-        *reinterpret_cast<uint32_t *>(q8) = (uint32_t)(q[0] & 0xff) | ((uint32_t)(q[1] & 0xff) << 8) |
-                                            ((uint32_t)(q[2] & 0xff) << 16) | ((uint32_t)(q[3] & 0xff) << 24);
+        *reinterpret_cast<uint32_t *>(q8) = pack4(q);
     else
         *q8 = (int8_t)q[0];
     return sum;
@@ -237,7 +293,7 @@ __device__ __forceinline__ int row_sum(int sum, int *red)
 // and held (three registers for four elements) until the row's sum is known.
 template <typename T, bool RES, int TPR, int P>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_q8_0_kernel(const T *x, const T *res,
-                                                                             const float *__restrict__ w, double eps,
+                                                                             const float *__restrict__ w, double eps, double inv_k,
                                                                              T *h, uint8_t *__restrict__ xq,
                                                                              int64_t m, int k)
 {
@@ -249,31 +305,35 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_q8_0_kernel(con
         return; // a whole wave: nothing below meets across waves when RPW > 1
     const int np = k / 4;
     const int64_t base = row * k;
-    Elems<4, T> xe[P], re[P];
-    Elems<4, float> we[P];
-#pragma unroll
-    for (int j = 0; j < P; j++) {
-        const int i = t + TPR * j;
-        const int o = 4 * (i < np ? i : 0); // past the row: its first piece, masked below
-        xe[j] = load_elems<4>(x + base + o);
-        if (RES)
-            re[j] = load_elems<4>(res + base + o);
-        we[j] = load_elems<4>(w + o);
-    }
+    constexpr int G = P < kNormGroup ? P : kNormGroup;
     double ss = 0.0, a[P];
     uint32_t code[P];
 #pragma unroll
-    for (int j = 0; j < P; j++) {
-        const int i = t + TPR * j;
-        const bool ok = i < np;
-        double s1 = 0.0, p[4];
-        norm_products<T, RES, 4>(xe[j], re[j], we[j], h && ok ? h + base + 4 * i : nullptr, s1, p);
-        ss += ok ? s1 : 0.0;
-        code[j] = block_codes(p, a[j]);
+    for (int g = 0; g < P; g += G) {
+        Elems<4, T> xe[G], re[G];
+        Elems<4, float> we[G];
+#pragma unroll
+        for (int j = 0; j < G; j++) {
+            const int i = t + TPR * (g + j);
+            const int o = 4 * (i < np ? i : 0); // past the row: its first piece, masked below
+            xe[j] = load_elems<4>(x + base + o);
+            if (RES)
+                re[j] = load_elems<4>(res + base + o);
+            we[j] = load_elems<4>(w + o);
+        }
+#pragma unroll
+        for (int j = 0; j < G; j++) {
+            const int i = t + TPR * (g + j);
+            const bool ok = i < np;
+            double s1 = 0.0, p[4];
+            norm_products<T, RES, 4>(xe[j], re[j], we[j], h && ok ? h + base + 4 * i : nullptr, s1, p);
+            ss += ok ? s1 : 0.0;
+            code[g + j] = block_codes(p, a[g + j]);
+        }
     }
     double unused = 0.0;
     row_reduce<TPR, false>(ss, unused, red);
-    const double scale = 1.0 / (127.0 * sqrt(ss / (double)k + eps));
+    const double scale = inverse_root(fma(ss, inv_k, eps)) * (1.0 / 127.0);
 #pragma unroll
     for (int j = 0; j < P; j++) {
         const int i = t + TPR * j;
@@ -290,7 +350,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_q8_0_kernel(con
 // their products taken again.  V = 4 where k % 4 == 0, else 1.
 template <typename T, bool RES, int V, int TPR, int P>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_i8_rows_kernel(
-    const T *x, const T *res, const float *__restrict__ w, double eps, T *h, int8_t *__restrict__ xq,
+    const T *x, const T *res, const float *__restrict__ w, double eps, double inv_k, T *h, int8_t *__restrict__ xq,
     float *__restrict__ act_scale, int32_t *__restrict__ act_sum, int64_t m, int k)
 {
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
@@ -302,45 +362,52 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_i8_rows_kernel(
         return;
     const int np = k / V;
     const int64_t base = row * k;
-    Elems<V, T> xe[P], re[P]; // xe: x, then h
-    Elems<V, float> we[P];
-#pragma unroll
-    for (int j = 0; j < P; j++) {
-        const int i = t + TPR * j;
-        const int o = V * (i < np ? i : 0);
-        xe[j] = load_elems<V>(x + base + o);
-        if (RES)
-            re[j] = load_elems<V>(res + base + o);
-        we[j] = load_elems<V>(w + o);
-    }
+    constexpr int G = P < kNormGroup || V == 1 ? P : kNormGroup;
+    Elems<V, T> xe[P];     // x, then h
+    Elems<V, float> we[G]; // read again below where there is more than one group
     double ss = 0.0, mx = 0.0;
 #pragma unroll
-    for (int j = 0; j < P; j++) {
-        const int i = t + TPR * j;
-        const bool ok = i < np;
+    for (int g = 0; g < P; g += G) {
+        Elems<V, T> re[G];
 #pragma unroll
-        for (int e = 0; e < V; e++) {
+        for (int j = 0; j < G; j++) {
+            const int i = t + TPR * (g + j);
+            const int o = V * (i < np ? i : 0);
+            xe[g + j] = load_elems<V>(x + base + o);
             if (RES)
-                narrow(widen(xe[j].e[e]) + widen(re[j].e[e]), xe[j].e[e]);
-            const double hd = ok ? (double)widen(xe[j].e[e]) : 0.0;
-            ss = fma(hd, hd, ss);
-            mx = fmax(mx, fabs(hd * (double)we[j].e[e]));
+                re[j] = load_elems<V>(res + base + o);
+            we[j] = load_elems<V>(w + o);
         }
-        if (h && ok)
-            store_elems<V>(h + base + V * i, xe[j]);
+#pragma unroll
+        for (int j = 0; j < G; j++) {
+            const int i = t + TPR * (g + j);
+            const bool ok = i < np;
+            Elems<V, T> &hv = xe[g + j];
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                if (RES)
+                    narrow(widen(hv.e[e]) + widen(re[j].e[e]), hv.e[e]);
+                const double hd = ok ? (double)widen(hv.e[e]) : 0.0;
+                ss = fma(hd, hd, ss);
+                mx = fmax(mx, fabs(hd * (double)we[j].e[e]));
+            }
+            if (h && ok)
+                store_elems<V>(h + base + V * i, hv);
+        }
     }
     row_reduce<TPR, true>(ss, mx, red);
-    const float sc = row_scale(ss, k, eps, mx);
+    const float sc = row_scale(fma(ss, inv_k, eps), mx);
     const double a = sc > 0.0f ? mx : 0.0, f = code_factor(a);
     int sum = 0;
 #pragma unroll
     for (int j = 0; j < P; j++) {
         const int i = t + TPR * j;
         if (i < np) {
+            const Elems<V, float> wj = P == G ? we[j % G] : load_elems<V>(w + V * i);
             double p[V];
 #pragma unroll
             for (int e = 0; e < V; e++)
-                p[e] = (double)widen(xe[j].e[e]) * (double)we[j].e[e];
+                p[e] = (double)widen(xe[j].e[e]) * (double)wj.e[e];
             sum += store_i8<V>(xq + base + V * i, p, a, f);
         }
     }
@@ -356,7 +423,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_i8_rows_kernel(
 // back what it wrote) and over the inputs again where it is not.
 template <typename T, bool RES, int V, bool Q8>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const T *x, const T *res, const float *__restrict__ w,
-                                                            double eps, T *h, uint8_t *__restrict__ xq,
+                                                            double eps, double inv_k, T *h, uint8_t *__restrict__ xq,
                                                             float *__restrict__ act_scale,
                                                             int32_t *__restrict__ act_sum, int k)
 {
@@ -378,8 +445,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const T *x, const T 
                 mx = fmax(mx, fabs(p[e]));
     }
     row_reduce<1024, !Q8>(ss, mx, red);
-    const double scale = 1.0 / (127.0 * sqrt(ss / (double)k + eps));
-    const float sc = Q8 ? 0.0f : row_scale(ss, k, eps, mx);
+    const double scale = inverse_root(fma(ss, inv_k, eps)) * (1.0 / 127.0);
+    const float sc = Q8 ? 0.0f : row_scale(fma(ss, inv_k, eps), mx);
     const double a = sc > 0.0f ? mx : 0.0, f = code_factor(a);
     int sum = 0;
     for (int i = threadIdx.x; i < np; i += 1024) {
@@ -432,11 +499,11 @@ static hipError_t launch_norm(const NormArgs &a, hipStream_t s)
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     T *h = static_cast<T *>(a.h);
     if (a.act_scale) {
-        hipLaunchKernelGGL((rmsnorm_i8_rows_kernel<T, RES, V, TPR, P>), grid, block, 0, s, x, res, a.w, a.eps, h,
+        hipLaunchKernelGGL((rmsnorm_i8_rows_kernel<T, RES, V, TPR, P>), grid, block, 0, s, x, res, a.w, a.eps, 1.0 / (double)a.k, h,
                            reinterpret_cast<int8_t *>(a.xq), a.act_scale, a.act_sum, a.m, a.k);
     } else {
         if constexpr (V == 4)
-            hipLaunchKernelGGL((rmsnorm_q8_0_kernel<T, RES, TPR, P>), grid, block, 0, s, x, res, a.w, a.eps, h, a.xq,
+            hipLaunchKernelGGL((rmsnorm_q8_0_kernel<T, RES, TPR, P>), grid, block, 0, s, x, res, a.w, a.eps, 1.0 / (double)a.k, h, a.xq,
                                a.m, a.k);
     }
     return hipGetLastError();
@@ -449,34 +516,36 @@ static hipError_t launch_norm_long(const NormArgs &a, hipStream_t s)
     T *h = static_cast<T *>(a.h);
     const dim3 grid((unsigned)a.m), block(1024);
     if (a.act_scale) {
-        hipLaunchKernelGGL((rmsnorm_long_kernel<T, RES, V, false>), grid, block, 0, s, x, res, a.w, a.eps, h, a.xq,
+        hipLaunchKernelGGL((rmsnorm_long_kernel<T, RES, V, false>), grid, block, 0, s, x, res, a.w, a.eps, 1.0 / (double)a.k, h, a.xq,
                            a.act_scale, a.act_sum, a.k);
     } else {
         if constexpr (V == 4)
-            hipLaunchKernelGGL((rmsnorm_long_kernel<T, RES, V, true>), grid, block, 0, s, x, res, a.w, a.eps, h, a.xq,
+            hipLaunchKernelGGL((rmsnorm_long_kernel<T, RES, V, true>), grid, block, 0, s, x, res, a.w, a.eps, 1.0 / (double)a.k, h, a.xq,
                                a.act_scale, a.act_sum, a.k);
     }
     return hipGetLastError();
 }
 
 // Threads per row.  Rows of at most 256 pieces: one wave each, four rows a
-// workgroup.  Longer ones: 256 threads where there are rows enough to fill
-// the chip and a thread holds at most four pieces, else 1024 (the shortest
-// path for a single row).
+// workgroup.  Longer ones: 1024, the shortest path for a row, where there are
+// fewer rows than CUs; otherwise as few as hold the row in eight pieces each,
+// since what every wave does once (the reductions, the scale) weighs on few
+// pieces and workgroups of 1024 leave a CU to one row.
 template <typename T, bool RES, int V>
 static hipError_t launch_norm_v(const NormArgs &a, hipStream_t s)
 {
     const int np = a.k / V;
+    const bool many = a.m >= 256;
     if (np <= 64)
         return launch_norm<T, RES, V, 64, 1>(a, s);
     if (np <= 256)
         return launch_norm<T, RES, V, 64, 4>(a, s);
     if (np <= 1024)
-        return a.m >= 256 ? launch_norm<T, RES, V, 256, 4>(a, s) : launch_norm<T, RES, V, 1024, 1>(a, s);
+        return many ? launch_norm<T, RES, V, 256, 4>(a, s) : launch_norm<T, RES, V, 1024, 1>(a, s);
     if (np <= 2048)
-        return launch_norm<T, RES, V, 1024, 2>(a, s);
+        return many ? launch_norm<T, RES, V, 256, 8>(a, s) : launch_norm<T, RES, V, 1024, 2>(a, s);
     if (np <= 4096)
-        return launch_norm<T, RES, V, 1024, 4>(a, s);
+        return many ? launch_norm<T, RES, V, 512, 8>(a, s) : launch_norm<T, RES, V, 1024, 4>(a, s);
     if constexpr (V == 1) {
         if (np <= 16384)
             return launch_norm<T, RES, V, 1024, 16>(a, s);
