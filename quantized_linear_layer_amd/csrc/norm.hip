@@ -223,8 +223,11 @@ __device__ __forceinline__ uint32_t block_codes(const double (&p)[4], double &a)
     return pack4(q);
 }
 
-// Pieces whose loads a thread has out at once.
-constexpr int kNormGroup = 4;
+// Pieces whose loads a thread has out at once: the whole row's up to 256 threads
+// (4096 x 6912 bf16 into int8 rows with residual: 42 us, 51 with four, 57 with
+// two), four with more threads, where eight cost too many registers (1024 x
+// 13824: 24 us, 27 with eight).
+constexpr int norm_group(int tpr, int p) { return tpr <= 256 || p < 4 ? p : 4; }
 
 // Dword that only promises 2-byte alignment (codes of a Q8_0 block).
 typedef uint32_t u32_a2 __attribute__((aligned(2)));
@@ -305,7 +308,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_q8_0_kernel(con
         return; // a whole wave: nothing below meets across waves when RPW > 1
     const int np = k / 4;
     const int64_t base = row * k;
-    constexpr int G = P < kNormGroup ? P : kNormGroup;
+    constexpr int G = norm_group(TPR, P);
     double ss = 0.0, a[P];
     uint32_t code[P];
 #pragma unroll
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_i8_rows_kernel(
         return;
     const int np = k / V;
     const int64_t base = row * k;
-    constexpr int G = P < kNormGroup || V == 1 ? P : kNormGroup;
+    constexpr int G = V == 1 ? P : norm_group(TPR, P);
     Elems<V, T> xe[P];     // x, then h
     Elems<V, float> we[G]; // read again below where there is more than one group
     double ss = 0.0, mx = 0.0;
