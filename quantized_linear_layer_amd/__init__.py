@@ -9,6 +9,7 @@ kernels.  There is no fallback of any kind: if libqll.so is missing or does
 not load, `load()` and every call raise.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -130,19 +131,47 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on(stream, *tensors):
-    """Torch's current stream (or `stream`) as a handle, after checking that
-    every tensor given is on that stream's device and that it is the current
-    one: a kernel is launched on the current device."""
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    dev = s.device_index
-    if stream is not None and dev != torch.cuda.current_device():
-        raise ValueError(f"the stream is on device {dev}, the current device is {torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on device {t.get_device()}, the call runs on device {dev}")
-    return ctypes.c_void_p(s.cuda_stream)
+_raw_stream = None  # torch's current stream of a device as a handle, and its current device
+_current_device = None
+
+
+def _device(t, what):
+    """The device that a call on `t` runs on: its own, which has to be the
+    current one (a kernel is launched on the current device)."""
+    global _raw_stream, _current_device
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if _raw_stream is None:
+        import torch
+        # (the calls that torch.cuda.current_stream() and current_device() wrap, without the objects: 2.5 us a call)
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    if dev != _current_device():
+        raise ValueError(f"{what} is on device {dev}, the current device is {_current_device()}")
+    return dev
+
+
+def _arg(t, nbytes, what, dev):
+    """Device pointer of `t` (0 for None) after checking that it lies on `dev`,
+    is contiguous and can hold `nbytes` bytes."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a CUDA tensor on device {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.nbytes < nbytes:
+        raise ValueError(f"{what} holds {t.nbytes} bytes, the call needs {nbytes}")
+    return t.data_ptr()
+
+
+def _on(dev, stream):
+    """Handle of `stream`, or of torch's current stream on `dev`."""
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors are on device {dev}")
+    return stream.cuda_stream
 
 
 def _call(name, *args):
@@ -333,40 +362,45 @@ def qll_ternary_gemm(w, w_scale, xq, act_scale, act_sum, y, m, n, k, stream=None
 
 # ----------------------------------------------------------------- Q4_0 linear and gated
 
-def _op_ws(ws, op, m, n, k):
-    """ws as (pointer, bytes) for an operation that may need none; a shape
-    the library refuses is left for it to name."""
-    need = qll_workspace_bytes(op, m, n, k)
-    return (None, 0) if need == 2 ** 64 - 1 else _ws(ws, need)
+def _scratch(ws, dev):
+    """ws as (pointer, bytes); whether the call needs one, and of what size, is
+    the library's to say."""
+    return (None, 0) if ws is None else (_arg(ws, 0, "ws", dev), ws.nbytes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _repacked_need(n, k, gated):
+    need = qll_q4_0_repacked_gated_bytes(n, k) if gated else qll_q4_0_repacked_bytes(n, k)
+    return need if need != 2 ** 64 - 1 else 0
 
 
 def qll_q4_0_q8_0_linear(w, xq, bias, act, residual, y, m, n, k, ws=None, stream=None):
     """y = act(x.W^T + bias) + residual; bias and residual may be None,
     residual may be y."""
-    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_LINEAR, m, n, k)
-    _call("qll_q4_0_q8_0_linear", _ptr(w, n * (k // 32) * Q4_0_BLOCK_BYTES, "w"),
-          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), _ptr(bias, n * 4, "bias"), int(act),
-          _ptr(residual, m * n * 4, "residual"), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
-          _on(stream, w, xq, bias, residual, y, ws))
+    d = _device(y, "y")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_q4_0_q8_0_linear", _arg(w, n * (k // 32) * Q4_0_BLOCK_BYTES, "w", d),
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d), act,
+          _arg(residual, m * n * 4, "residual", d), _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb, _on(d, stream))
 
 
 def qll_q4_0_repacked_q8_0_linear(wp, xq, bias, act, residual, y, m, n, k, ws=None, stream=None):
     """qll_q4_0_q8_0_linear on weights repacked by qll_q4_0_repack."""
-    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_REPACKED_GEMM, m, n, k)
-    need = qll_q4_0_repacked_bytes(n, k)
-    _call("qll_q4_0_repacked_q8_0_linear", _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"),
-          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), _ptr(bias, n * 4, "bias"), int(act),
-          _ptr(residual, m * n * 4, "residual"), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
-          _on(stream, wp, xq, bias, residual, y, ws))
+    d = _device(y, "y")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_q4_0_repacked_q8_0_linear", _arg(wp, _repacked_need(n, k, False), "wp", d),
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d), act,
+          _arg(residual, m * n * 4, "residual", d), _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb, _on(d, stream))
 
 
 def qll_q4_0_q8_0_gated(wg, wu, xq, act, y, m, n, k, ws=None, stream=None):
     """y = act(x.Wg^T) * (x.Wu^T)."""
-    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_GATED, m, n, k)
+    d = _device(y, "y")
+    wsp, wsb = _scratch(ws, d)
     nb = n * (k // 32) * Q4_0_BLOCK_BYTES
-    _call("qll_q4_0_q8_0_gated", _ptr(wg, nb, "wg"), _ptr(wu, nb, "wu"),
-          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), int(act), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
-          _on(stream, wg, wu, xq, y, ws))
+    _call("qll_q4_0_q8_0_gated", _arg(wg, nb, "wg", d), _arg(wu, nb, "wu", d),
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb,
+          _on(d, stream))
 
 
 def qll_q4_0_repacked_gated_bytes(n, k):
@@ -375,19 +409,19 @@ def qll_q4_0_repacked_gated_bytes(n, k):
 
 def qll_q4_0_repack_gated(wg, wu, wp, n, k, stream=None):
     """Load-time repack of a gate and up pair into the matrix-core operand form."""
-    need = qll_q4_0_repacked_gated_bytes(n, k)
+    d = _device(wp, "wp")
     nb = n * (k // 32) * Q4_0_BLOCK_BYTES
-    _call("qll_q4_0_repack_gated", _ptr(wg, nb, "wg"), _ptr(wu, nb, "wu"),
-          _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"), n, k, _on(stream, wg, wu, wp))
+    _call("qll_q4_0_repack_gated", _arg(wg, nb, "wg", d), _arg(wu, nb, "wu", d),
+          _arg(wp, _repacked_need(n, k, True), "wp", d), n, k, _on(d, stream))
 
 
 def qll_q4_0_repacked_q8_0_gated(wp, xq, act, y, m, n, k, ws=None, stream=None):
     """qll_q4_0_q8_0_gated on a pair repacked by qll_q4_0_repack_gated."""
-    wsp, wsb = _op_ws(ws, QLL_OP_Q4_0_REPACKED_GATED, m, n, k)
-    need = qll_q4_0_repacked_gated_bytes(n, k)
-    _call("qll_q4_0_repacked_q8_0_gated", _ptr(wp, need if need != 2 ** 64 - 1 else 0, "wp"),
-          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), int(act), _ptr(y, m * n * 4, "y"), m, n, k, wsp, wsb,
-          _on(stream, wp, xq, y, ws))
+    d = _device(y, "y")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_q4_0_repacked_q8_0_gated", _arg(wp, _repacked_need(n, k, True), "wp", d),
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb,
+          _on(d, stream))
 
 
 # ----------------------------------------------------------------- norms into activations
@@ -399,19 +433,20 @@ def _esize(dtype):
 def qll_rmsnorm_q8_0(x, dtype, residual, weight, eps, h, xq, m, k, stream=None):
     """xq = Q8_0(rmsnorm(x + residual) * weight), h = x + residual; residual
     and h may be None, h may be x or residual."""
+    d = _device(x, "x")
     nb = m * k * _esize(dtype)
-    _call("qll_rmsnorm_q8_0", _ptr(x, nb, "x"), int(dtype), _ptr(residual, nb, "residual"),
-          _ptr(weight, k * 4, "weight"), float(eps), _ptr(h, nb, "h"),
-          _ptr(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq"), m, k, _on(stream, x, residual, weight, h, xq))
+    _call("qll_rmsnorm_q8_0", _arg(x, nb, "x", d), dtype, _arg(residual, nb, "residual", d),
+          _arg(weight, k * 4, "weight", d), eps, _arg(h, nb, "h", d),
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), m, k, _on(d, stream))
 
 
 def qll_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_sum, m, k, stream=None):
     """As qll_rmsnorm_q8_0, into int8 rows with act_scale and act_sum."""
+    d = _device(x, "x")
     nb = m * k * _esize(dtype)
-    _call("qll_rmsnorm_i8_rows", _ptr(x, nb, "x"), int(dtype), _ptr(residual, nb, "residual"),
-          _ptr(weight, k * 4, "weight"), float(eps), _ptr(h, nb, "h"), _ptr(xq, m * k, "xq"),
-          _ptr(act_scale, m * 4, "act_scale"), _ptr(act_sum, m * 4, "act_sum"), m, k,
-          _on(stream, x, residual, weight, h, xq, act_scale, act_sum))
+    _call("qll_rmsnorm_i8_rows", _arg(x, nb, "x", d), dtype, _arg(residual, nb, "residual", d),
+          _arg(weight, k * 4, "weight", d), eps, _arg(h, nb, "h", d), _arg(xq, m * k, "xq", d),
+          _arg(act_scale, m * 4, "act_scale", d), _arg(act_sum, m * 4, "act_sum", d), m, k, _on(d, stream))
 
 
 # ----------------------------------------------------------------- token log probabilities
@@ -421,8 +456,9 @@ def qll_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids,
     """Log probabilities of t given tokens a row (int32 ids), entropy, and the
     top largest; tokens and logprob may be None at t = 0, top_ids and
     top_logprob at top = 0, entropy always."""
-    wsp, wsb = _op_ws(ws, QLL_OP_TOKEN_LOGPROBS, m, v, top)
-    _call("qll_token_logprobs", _ptr(logits, m * v * _esize(dtype), "logits"), int(dtype),
-          _ptr(tokens, m * t * 4, "tokens"), t, _ptr(logprob, m * t * 4, "logprob"), _ptr(entropy, m * 4, "entropy"),
-          top, _ptr(top_ids, m * top * 4, "top_ids"), _ptr(top_logprob, m * top * 4, "top_logprob"), m, v, wsp, wsb,
-          _on(stream, logits, tokens, logprob, entropy, top_ids, top_logprob, ws))
+    d = _device(logits, "logits")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_token_logprobs", _arg(logits, m * v * _esize(dtype), "logits", d), dtype,
+          _arg(tokens, m * t * 4, "tokens", d), t, _arg(logprob, m * t * 4, "logprob", d),
+          _arg(entropy, m * 4, "entropy", d), top, _arg(top_ids, m * top * 4, "top_ids", d),
+          _arg(top_logprob, m * top * 4, "top_logprob", d), m, v, wsp, wsb, _on(d, stream))

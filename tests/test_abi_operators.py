@@ -164,3 +164,16 @@ def test_logprobs(L):
     assert W(qll.QLL_OP_TOKEN_LOGPROBS, 1, 2 ** 20, 64) < SIZE_MAX
     for m, v, top in ((0, 10, 1), (1, 0, 0), (1, 10, 11), (1, 100, 65), (1, 2 ** 20 + 1, 1), (1, 10, -1)):
         assert W(qll.QLL_OP_TOKEN_LOGPROBS, m, v, top) == SIZE_MAX
+
+
+def test_binding_refuses_host_tensors_of_every_operator():
+    import torch
+    t = torch.zeros(4096)
+    for call in (lambda: qll.qll_q4_0_q8_0_linear(t, t, None, 0, None, t, 1, 8, 32),
+                 lambda: qll.qll_q4_0_repacked_q8_0_linear(t, t, None, 0, None, t, 1, 8, 32),
+                 lambda: qll.qll_q4_0_q8_0_gated(t, t, t, 0, t, 1, 8, 32),
+                 lambda: qll.qll_q4_0_repack_gated(t, t, t, 8, 32),
+                 lambda: qll.qll_q4_0_repacked_q8_0_gated(t, t, 0, t, 1, 8, 32),
+                 lambda: qll.qll_token_logprobs(t, 0, None, 0, None, t, 0, None, None, 1, 8)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
