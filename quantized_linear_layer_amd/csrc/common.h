@@ -151,20 +151,21 @@ __device__ __forceinline__ void activate16(V16 &v, int act)
 // argument, so that the plain entries keep their kernels.
 struct PlainEpilogue { // y = v
     static constexpr bool kLinear = false, kGated = false;
-    PlainEpilogue rows(int64_t, int64_t) const { return *this; }
+    __host__ __device__ PlainEpilogue rows(int64_t, int64_t) const { return *this; }
 };
 struct LinearEpilogue { // y = act(v + bias[j]) + res[i][j]; bias and res may be null, res may be y
     static constexpr bool kLinear = true, kGated = false;
     const float *bias, *res;
     int act;
     // the same for rows i0, i0 + 1, ... as rows 0, 1, ...
-    LinearEpilogue rows(int64_t i0, int64_t n) const { return {bias, res ? res + i0 * n : nullptr, act}; }
+    __host__ __device__ LinearEpilogue rows(int64_t i0, int64_t n) const { return {bias, res ? res + i0 * n : nullptr, act}; }
 };
 struct GatedEpilogue { // y = act(v of w) * (v of wu); raw: both products as planes (a k-split's partials)
     static constexpr bool kLinear = false, kGated = true;
     const uint8_t *wu; // null where the weights are interleaved at load time
     int act;
     bool raw;
+    __host__ __device__ GatedEpilogue rows(int64_t, int64_t) const { return *this; }
 };
 
 template <class EP>
