@@ -215,31 +215,38 @@ struct WaveTop {
         }
     }
 
-    // Where a step has more candidates than the list has room for, those that fit
-    // give a tighter bound and the step is gone through again (this keeps the
-    // search for a bound, which is long, in one place of the code).
+    // Where a step has more candidates than the list has room for, the list is
+    // first cut to its k best, then those that fit give a tighter bound, and the
+    // step is gone through again (this keeps the search for a bound, which is long,
+    // in one place of the code).  With k entries before the step, 192 - k of its
+    // candidates fit and at most k of them stay above the bound, so every time
+    // through at least 64 fewer are left.  (With 128 entries before it and k = 64,
+    // the 64 that fit could all stay, and the search went on forever.)
     template <int V, int E, class IDX>
     __device__ __forceinline__ void add(const float (&x)[E], const float (&pm)[E / V], float ts, bool ties,
                                         const IDX &idx)
     {
-        bool again;
+        bool over;
         do {
             const int n0 = n;
             if (ties)
                 append<true, V>(x, pm, ts, idx);
             else
                 append<false, V>(x, pm, ts, idx);
-            again = n > kLpCap;
-            if (n > kLpCap - 64)
-                cut(!again);
-            if (again) {
+            over = n > kLpCap;
+            const bool shorten = over && n0 > k;
+            if (shorten)
                 n = n0;
+            if (shorten || n > kLpCap - 64)
+                cut(!over || shorten);
+            if (over) {
+                n = shorten ? n : n0;
                 // the bound lies among this step's elements now: values equal to
                 // it are told apart by index
                 ts = fmaxf(ts, below(tv));
                 ties = true;
             }
-        } while (again);
+        } while (over);
     }
 
     // The bound at the k-th best of the list, n > k (of its first kLpCap, if it

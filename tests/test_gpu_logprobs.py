@@ -163,3 +163,39 @@ def test_row_does_not_depend_on_its_batch_in_what_it_chooses(qll_gpu):
     x, tokens = logits(9, 300, 9000, torch.float16)
     many, one = call(x, tokens, 64), call(x[7:8].clone(), tokens[7:8], 64)
     assert np.array_equal(many[2][7], one[2][0])
+
+
+@pytest.mark.parametrize("count", [65, 127, 128, 129])
+@pytest.mark.parametrize("m", [200, 256])  # in segments of a row, and whole rows
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_full_list_then_only_better_logits(qll_gpu, dtype, m, count):
+    """`count` entries in a wave's list (it holds 192), then a step whose every
+    logit is better than all of them, worst first: a search for a bound that
+    took the first 64 of the step again and again would not end."""
+    v, piece = 16384, 16 // torch.empty(0, dtype=dtype).element_size()
+    threads = 256 if m < 256 else 512
+    pieces = 8 // piece if m < 256 else 2
+    step = threads * pieces * piece
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(m, v, generator=g) * 0.1 - 8
+    own = (torch.arange(v) // piece) % threads < 64  # the first wave's logits
+    first = torch.nonzero(own[:step])[:, 0]
+    x[:, first] = -40.0
+    # (a lane's logits of a step lie piece by piece: all of the first lanes')
+    lane = (first // piece) % threads
+    few = first[torch.argsort(lane, stable=True)][:count]
+    x[:, few] = -2.0 + 0.01 * torch.rand(m, count, generator=g)
+    second = step + first
+    place = (first // (piece * threads)) * piece + first % piece
+    x[:, second] = 4.0 + (place * 64 + lane).float() / 256
+    check(x.to(dtype), np.full((m, 1), 7), 64)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("m", [2, 256])
+@pytest.mark.parametrize("top", [1, 20, 64])
+def test_rising_rows(qll_gpu, dtype, m, top):
+    v = 20000
+    x = torch.linspace(-30, 30, v).repeat(m, 1) + torch.arange(m)[:, None] / 64
+    x[1] = x[1].flip(0)
+    check(x.to(dtype), np.full((m, 1), 3), top)
