@@ -461,6 +461,18 @@ struct LpOut {
     int32_t *top_ids;
     float *top_logprob;
     int top, v;
+
+    // The same for rows r0, r0 + 1, ... as rows 0, 1, ...
+    LpOut rows(int64_t r0) const
+    {
+        LpOut o = *this;
+        o.tokens = nt > 0 ? tokens + r0 * nt : nullptr;
+        o.logprob = nt > 0 ? logprob + r0 * nt : nullptr;
+        o.entropy = entropy ? entropy + r0 : nullptr;
+        o.top_ids = top > 0 ? top_ids + r0 * top : nullptr;
+        o.top_logprob = top > 0 ? top_logprob + r0 * top : nullptr;
+        return o;
+    }
 };
 
 // log p from a row's reference and sums; NaN in a row with nothing left (m is
@@ -839,6 +851,7 @@ __global__ __launch_bounds__(64 * kLpWaves) void logprob_join_kernel(const T *__
 // it takes for about 1024 workgroups (512 measured 0 to 10% slower, workgroups of
 // eight waves up to 40%).
 constexpr int kLpGroups = 1024;
+constexpr int64_t kLpMaxRows = (int64_t)1 << 22; // whole rows of one launch: a grid has fewer than 2^32 threads
 struct LpPlan {
     bool row;
     int segments, steps;
@@ -878,22 +891,28 @@ size_t token_logprobs_workspace(int64_t m, int64_t v, int64_t top)
 template <typename T>
 static hipError_t launch_logprobs(const T *x, const LpOut &o, int64_t m, void *wsp, hipStream_t s)
 {
-    if (o.v < LpPiece<T>::V) {
-        hipLaunchKernelGGL(logprob_tiny_kernel<T>, dim3((unsigned)((m + 63) / 64)), dim3(64), 0, s, x, o, m);
-        return hipGetLastError();
-    }
     const LpPlan p = lp_plan<T>(m, o.v);
     LpWs ws;
     ws.stat = static_cast<LpStat *>(wsp);
     ws.key = reinterpret_cast<uint64_t *>(ws.stat + m * p.segments * kLpWaves);
-    if (m * p.segments > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(m * p.segments));
     if (p.row) {
-        const dim3 block(64 * kLpRowWaves);
-        hipLaunchKernelGGL((logprob_kernel<T, kLpRowWaves, true>), grid, block, 0, s, x, ws, o, 1, p.steps);
-        return hipGetLastError();
+        for (int64_t r0 = 0; r0 < m; r0 += kLpMaxRows) {
+            const int64_t rows = m - r0 < kLpMaxRows ? m - r0 : kLpMaxRows;
+            const T *xr = x + r0 * o.v;
+            const LpOut part = o.rows(r0);
+            if (o.v < LpPiece<T>::V)
+                hipLaunchKernelGGL(logprob_tiny_kernel<T>, dim3((unsigned)((rows + 63) / 64)), dim3(64), 0, s, xr, part,
+                                   rows);
+            else
+                hipLaunchKernelGGL((logprob_kernel<T, kLpRowWaves, true>), dim3((unsigned)rows),
+                                   dim3(64 * kLpRowWaves), 0, s, xr, ws, part, 1, p.steps);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
+        return hipSuccess;
     }
+    const dim3 grid((unsigned)(m * p.segments)); // m < 256
     const dim3 block(64 * kLpWaves);
     hipLaunchKernelGGL((logprob_kernel<T, kLpWaves, false>), grid, block, 0, s, x, ws, o, p.segments, p.steps);
     const hipError_t e = hipGetLastError();

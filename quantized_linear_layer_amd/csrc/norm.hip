@@ -556,12 +556,35 @@ static hipError_t launch_norm_v(const NormArgs &a, hipStream_t s)
     return launch_norm_long<T, RES, V>(a, s);
 }
 
+// Rows of one launch: a grid has fewer than 2^32 threads.
+constexpr int64_t kNormMaxRows = (int64_t)1 << 21;
+
 template <typename T>
-static hipError_t launch_norm_t(const NormArgs &a, hipStream_t s)
+static hipError_t launch_norm_t(const NormArgs &all, hipStream_t s)
 {
-    if (a.k % 4 == 0)
-        return a.res ? launch_norm_v<T, true, 4>(a, s) : launch_norm_v<T, false, 4>(a, s);
-    return a.res ? launch_norm_v<T, true, 1>(a, s) : launch_norm_v<T, false, 1>(a, s);
+    for (int64_t r0 = 0; r0 < all.m; r0 += kNormMaxRows) {
+        NormArgs a = all;
+        const int64_t at = r0 * all.k;
+        a.m = all.m - r0 < kNormMaxRows ? all.m - r0 : kNormMaxRows;
+        a.x = static_cast<const T *>(all.x) + at;
+        a.res = all.res ? static_cast<const T *>(all.res) + at : nullptr;
+        a.h = all.h ? static_cast<T *>(all.h) + at : nullptr;
+        if (all.act_scale) {
+            a.xq += at;
+            a.act_scale += r0;
+            a.act_sum += r0;
+        } else {
+            a.xq += at / 32 * 34;
+        }
+        hipError_t e;
+        if (a.k % 4 == 0)
+            e = a.res ? launch_norm_v<T, true, 4>(a, s) : launch_norm_v<T, false, 4>(a, s);
+        else
+            e = a.res ? launch_norm_v<T, true, 1>(a, s) : launch_norm_v<T, false, 1>(a, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 static hipError_t launch_norm_any(int dtype, const NormArgs &a, hipStream_t s)

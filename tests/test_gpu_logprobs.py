@@ -199,3 +199,48 @@ def test_rising_rows(qll_gpu, dtype, m, top):
     x = torch.linspace(-30, 30, v).repeat(m, 1) + torch.arange(m)[:, None] / 64
     x[1] = x[1].flip(0)
     check(x.to(dtype), np.full((m, 1), 3), top)
+
+
+@pytest.mark.parametrize("v", [3, 8])  # a thread per row, and a workgroup per row
+def test_more_rows_than_one_grid_holds(qll_gpu, v):
+    """Workgroups of 512 threads for 2^23 + 3 rows: 2^32 threads and more."""
+    m = (1 << 23) + 3
+    x = torch.zeros(m, v, dtype=torch.bfloat16, device="cuda")
+    x[1 << 22, 1], x[m - 1, 2] = 2.0, 1.0
+    tokens = torch.zeros(m, dtype=torch.int32, device="cuda")
+    tokens[m - 1] = 2
+    lp, en = torch.full((m + 8,), 9.0, device="cuda"), torch.full((m + 8,), 9.0, device="cuda")
+    ids = torch.full((m + 8,), -9, dtype=torch.int32, device="cuda")
+    tl = torch.full((m + 8,), 9.0, device="cuda")
+    ws = empty(qll.qll_workspace_bytes(qll.QLL_OP_TOKEN_LOGPROBS, m, v, 1))
+    qll.qll_token_logprobs(x, qll.QLL_DTYPE_BF16, tokens, 1, lp, en, 1, ids, tl, m, v, ws=ws)
+    torch.cuda.synchronize()
+    rows = [0, (1 << 22) - 1, 1 << 22, m - 2, m - 1]
+    want = R.reference(x[rows].float().cpu().numpy(), tokens[rows].cpu().numpy()[:, None], 1)
+    R.assert_close(lp[rows].cpu().numpy()[:, None], want[0], want[4], "given tokens")
+    R.assert_close(en[rows].cpu().numpy(), want[1], want[5], "entropy")
+    R.assert_close(tl[rows].cpu().numpy()[:, None], want[3], want[4], "chosen tokens")
+    assert np.array_equal(ids[rows].cpu().numpy()[:, None], want[2])
+    even = torch.ones(m, dtype=torch.bool, device="cuda")
+    even[[1 << 22, m - 1]] = False
+    assert (lp[:m][even] == lp[0]).all() and (en[:m][even] == en[0]).all() and (ids[:m][even] == 0).all()
+    assert (lp[m:] == 9).all() and (en[m:] == 9).all() and (ids[m:] == -9).all() and (tl[m:] == 9).all()
+
+
+def test_offsets_past_32_bits(qll_gpu):
+    m, v = 4099, 1 << 20
+    x = torch.zeros(m, v, dtype=torch.float16, device="cuda")
+    tail, tokens = logits(15, 3, v, torch.float16)
+    x[-3:] = tail.cuda()
+    given = torch.zeros(m, 3, dtype=torch.int32, device="cuda")
+    given[-3:] = torch.from_numpy(tokens.astype(np.int32)).cuda()
+    lp, en = torch.empty(m * 3, device="cuda"), torch.empty(m, device="cuda")
+    ids, tl = torch.empty(m * 5, dtype=torch.int32, device="cuda"), torch.empty(m * 5, device="cuda")
+    ws = empty(qll.qll_workspace_bytes(qll.QLL_OP_TOKEN_LOGPROBS, m, v, 5))
+    qll.qll_token_logprobs(x, qll.QLL_DTYPE_F16, given, 3, lp, en, 5, ids, tl, m, v, ws=ws)
+    torch.cuda.synchronize()
+    want = R.reference(tail.float().numpy(), tokens, 5)
+    R.assert_close(lp[-9:].cpu().numpy().reshape(3, 3), want[0], want[4], "given tokens")
+    R.assert_close(en[-3:].cpu().numpy(), want[1], want[5], "entropy")
+    assert np.array_equal(ids[-15:].cpu().numpy().reshape(3, 5), want[2])
+    R.assert_close(tl[-15:].cpu().numpy().reshape(3, 5), want[3], want[4], "chosen tokens")

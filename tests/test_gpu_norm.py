@@ -68,9 +68,9 @@ def call(form, x, res, w, eps, h, stream=None, guard=0):
         assert (raw[m * k:] == 0x5A).all() and (s[m:] == -7).all() and (t[m:] == -7).all(), "wrote past the rows"
         scale, total, codes = s[:m], t[:m], raw[:m * k].reshape(m, k).astype(np.int64)
     if res is not None and h != "res":
-        assert torch.equal(rd.cpu(), res)
+        assert torch.equal(rd.cpu().view(torch.uint8), res.view(torch.uint8))
     if h != "x":
-        assert torch.equal(xd.cpu(), x)
+        assert torch.equal(xd.cpu().view(torch.uint8), x.view(torch.uint8))
     return None if hd is None else hd.cpu(), codes, scale, total
 
 
@@ -198,3 +198,63 @@ def test_codes_of_a_row_do_not_depend_on_its_batch(qll_gpu):
     many = call("q8_0", x, r, w, 1e-5, "new")
     one = call("q8_0", x[17:18].clone(), r[17:18].clone(), w, 1e-5, "new")
     assert np.array_equal(many[1][17], one[1][0]) and np.array_equal(many[2][17], one[2][0])
+
+
+@pytest.mark.parametrize("form", ["q8_0", "i8"])
+@pytest.mark.parametrize("h", ["new", "x"])
+@pytest.mark.parametrize("k", [64, 4096, 16416])
+def test_stream_added_to_itself(qll_gpu, form, h, k):
+    x, _, w = stream_rows(13, 3, k, torch.bfloat16)
+    xd, wd = x.to(DEV), w.to(DEV)
+    hd = xd if h == "x" else torch.empty_like(xd)
+    want = definition(x, x, w, 1e-5, form == "q8_0")
+    if form == "q8_0":
+        xq = torch.empty(3 * (k // 32) * 34, dtype=torch.uint8, device=DEV)
+        qll.qll_rmsnorm_q8_0(xd, qll.QLL_DTYPE_BF16, xd, wd, 1e-5, hd, xq, 3, k)
+        codes = xq.cpu().numpy().reshape(3, k // 32, 34)[..., 2:].copy().view(np.int8).reshape(3, k)
+    else:
+        xq = torch.empty(3 * k, dtype=torch.int8, device=DEV)
+        s, t = torch.empty(3, device=DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+        qll.qll_rmsnorm_i8_rows(xd, qll.QLL_DTYPE_BF16, xd, wd, 1e-5, hd, xq, s, t, 3, k)
+        codes = xq.cpu().numpy().reshape(3, k)
+        assert np.array_equal(s.cpu().numpy(), want[2]) and np.array_equal(t.cpu().numpy(), want[3])
+    assert torch.equal(hd.cpu(), want[0]) and np.array_equal(codes, want[1])
+
+
+def test_more_rows_than_one_grid_holds(qll_gpu):
+    """2^26 + 3 rows of one wave each: 2^32 threads and more."""
+    m, k = (1 << 26) + 3, 1
+    x = torch.zeros(m, k, dtype=torch.float16, device=DEV)
+    x[0], x[(1 << 21) - 1], x[1 << 21], x[m - 1] = 1.0, -2.0, 3.0, -4.0
+    w = torch.full((k,), 0.5, device=DEV)
+    xq = torch.full((m + 4,), 7, dtype=torch.int8, device=DEV)
+    s, t = torch.full((m + 4,), -7.0, device=DEV), torch.full((m + 4,), -7, dtype=torch.int32, device=DEV)
+    qll.qll_rmsnorm_i8_rows(x, qll.QLL_DTYPE_F16, None, w, 0.0, None, xq, s, t, m, k)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, (1 << 21) - 1, 1 << 21, m - 1], device=DEV)
+    want = torch.tensor([127, -127, 127, -127], device=DEV)
+    assert torch.equal(xq[at].int(), want.int()) and torch.equal(t[at], want.int())
+    assert torch.equal(s[at], torch.full((4,), 254.0, device=DEV))
+    assert int((xq[:m] != 0).sum()) == 4 and int((t[:m] != 0).sum()) == 4 and int((s[:m] != 0).sum()) == 4
+    assert (xq[m:] == 7).all() and (s[m:] == -7).all() and (t[m:] == -7).all()
+
+
+@pytest.mark.parametrize("form", ["q8_0", "i8"])
+def test_offsets_past_32_bits(qll_gpu, form):
+    m, k = (1 << 20) + 5, 4096
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    tail, _, w = stream_rows(14, 5, k, torch.bfloat16)
+    x[-5:] = tail.to(DEV)
+    xt, wd = x[-5:].cpu(), w.to(DEV)
+    want = definition(xt, None, w, 1e-5, form == "q8_0")
+    if form == "q8_0":
+        xq = torch.empty(m * (k // 32) * 34, dtype=torch.uint8, device=DEV)
+        qll.qll_rmsnorm_q8_0(x, qll.QLL_DTYPE_BF16, None, wd, 1e-5, x, xq, m, k)
+        codes = xq[-5 * (k // 32) * 34:].cpu().numpy().reshape(5, k // 32, 34)[..., 2:].copy().view(np.int8)
+    else:
+        xq = torch.empty(m * k, dtype=torch.int8, device=DEV)
+        s, t = torch.empty(m, device=DEV), torch.empty(m, dtype=torch.int32, device=DEV)
+        qll.qll_rmsnorm_i8_rows(x, qll.QLL_DTYPE_BF16, None, wd, 1e-5, x, xq, s, t, m, k)
+        codes = xq[-5 * k:].cpu().numpy()
+        assert np.array_equal(s[-5:].cpu().numpy(), want[2]) and np.array_equal(t[-5:].cpu().numpy(), want[3])
+    assert np.array_equal(codes.reshape(5, k), want[1]) and torch.equal(x[-5:].cpu(), xt)
