@@ -411,7 +411,7 @@ int qll_q4_0_repacked_q8_0_gated(const void *wp, const void *xq, int act, float 
  * rounded to it once, to nearest even, and the norm is taken of the rounded
  * sum).  h, where not NULL, receives the sum; it may be x or residual itself
  * (the update in place) and must not overlap an input otherwise.  x,
- * residual, h: [m][k] of type T; weight: float[k]; eps >= 0 and finite (else
+ * residual, h: [m][k] of type T; weight: float[k], finite; eps >= 0 and finite (else
  * QLL_ERR_VALUE, like an unknown dtype).  k < 2^24 (else QLL_ERR_SHAPE, as in
  * the GEMMs that take the result).
  *
@@ -423,13 +423,15 @@ int qll_q4_0_repacked_q8_0_gated(const void *wp, const void *xq, int act, float 
  * values within f32 rounding of a border. */
 
 /* Q8_0 blocks: d = binary16(f32(A / (127 rms))) per 32-block.  xq:
- * block_q8_0[m][k/32].  k % 32 == 0. */
+ * block_q8_0[m][k/32].  k % 32 == 0.  In a row whose h has NaN or an infinity in
+ * it, d is NaN in every block whose products are not all zero, and the codes
+ * are unspecified. */
 int qll_rmsnorm_q8_0(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
                      void *xq, int64_t m, int64_t k, void *stream);
 
 /* int8 rows: act_scale = f32(127 rms / A) and act_sum = sum_t q_t per row; a
- * row with A = 0, or whose act_scale is not finite, gets q = 0, act_scale = 0
- * and act_sum = 0.  xq: int8[m][k], act_scale: float[m], act_sum: int32[m].
+ * row with A = 0, or whose act_scale is not finite (one with NaN or an infinity
+ * in its h among them), gets q = 0, act_scale = 0 and act_sum = 0.  xq: int8[m][k], act_scale: float[m], act_sum: int32[m].
  * Any k >= 1. */
 int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
                         int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m, int64_t k, void *stream);

@@ -238,10 +238,11 @@ __device__ __forceinline__ void store_codes(uint8_t *blk, int sub, uint32_t c)
 }
 
 // d of a block with maximum a; scale = 1 / (127 rms).  A block of zeros has
-// d = 0, also where eps = 0 makes the row's factor infinite.
+// d = 0, also where eps = 0 makes the row's factor infinite; in a row with NaN or
+// an infinity in it scale is NaN, and a where a block has nothing else.
 __device__ __forceinline__ void store_scale(uint8_t *blk, double a, double scale)
 {
-    float d = a > 0.0 ? (float)(a * scale) : 0.0f;
+    float d = a == 0.0 ? 0.0f : (float)(a * scale);
     // two roundings, as the quantizer's: the compiler would otherwise convert
     // f64 to binary16 in one (and in a long sequence of integer operations)
     asm volatile("" : "+v"(d));

@@ -200,6 +200,29 @@ def test_codes_of_a_row_do_not_depend_on_its_batch(qll_gpu):
     assert np.array_equal(many[1][17], one[1][0]) and np.array_equal(many[2][17], one[2][0])
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("form", ["q8_0", "i8"])
+@pytest.mark.parametrize("m,k", [(7, 96), (7, 4096), (260, 4096), (7, 16416)])
+def test_rows_with_nan_or_infinity(qll_gpu, form, m, k, dtype):
+    x, r, w = stream_rows(12, m, k, dtype)
+    bad = [1, 2, 4, 5]
+    x[1, 40] = float("nan")
+    r[2] = float("nan")
+    x[4, 3] = float("inf")
+    x[5, 7] = r[5, 7] = torch.finfo(dtype).max  # a sum that overflows
+    got = call(form, x, r, w, 1e-5, "new")
+    h, codes, scale, total = definition(x, r, w, 1e-5, form == "q8_0")
+    good = [i for i in range(m) if i not in bad]
+    assert np.array_equal(got[1][good], codes[good]) and np.array_equal(got[2][good], scale[good])
+    same = (got[0] == h) | (torch.isnan(got[0]) & torch.isnan(h))
+    assert same.all()
+    if form == "q8_0":
+        assert np.isnan(got[2][bad]).all()
+    else:
+        assert np.array_equal(got[3][good], total[good])
+        assert (got[1][bad] == 0).all() and (got[2][bad] == 0).all() and (got[3][bad] == 0).all()
+
+
 @pytest.mark.parametrize("form", ["q8_0", "i8"])
 @pytest.mark.parametrize("h", ["new", "x"])
 @pytest.mark.parametrize("k", [64, 4096, 16416])
