@@ -98,7 +98,7 @@ __device__ __forceinline__ float times_sigmoid(float x, float t)
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * t));
 }
 
-__device__ __forceinline__ float act_relu(float x) { return x > 0.0f ? x : 0.0f; }
+__device__ __forceinline__ float act_relu(float x) { return x < 0.0f ? 0.0f : x; } // NaN stays
 __device__ __forceinline__ float act_gelu(float x) { return 0.5f * x * erfcf(-0.70710678f * x); }
 // 0.5 (1 + tanh(u)) = sigmoid(2 u)
 __device__ __forceinline__ float act_gelu_tanh(float x)

@@ -220,3 +220,50 @@ def test_another_stream_and_determinism(qll_gpu):
     third = run_linear(layer, False, True, "gelu", True, stream=torch.cuda.current_stream())
     assert np.array_equal(first.view(np.uint32), second.view(np.uint32))
     assert np.array_equal(first.view(np.uint32), third.view(np.uint32))
+
+
+@pytest.mark.parametrize("repacked", [False, True])
+@pytest.mark.parametrize("m", [1, 2, 40, 70])
+@pytest.mark.parametrize("act", list(E.ACTS))
+def test_nan_and_infinity_reach_the_output(qll_gpu, act, m, repacked):
+    layer = Layer(31, m, 70, 256)
+    clean = run_linear(layer, repacked, True, act, True)
+    layer.bias[3], layer.bias[40] = np.nan, np.inf
+    layer.residual[m - 1, 5], layer.residual[0, 6] = np.nan, -np.inf
+    got = run_linear(layer, repacked, True, act, True)
+    assert np.isnan(got[:, 3]).all() and (got[:, 40] == np.inf).all()
+    assert np.isnan(got[m - 1, 5]) and got[0, 6] == -np.inf
+    got[:, [3, 40]] = clean[:, [3, 40]]
+    got[m - 1, 5], got[0, 6] = clean[m - 1, 5], clean[0, 6]
+    assert np.array_equal(got.view(np.uint32), clean.view(np.uint32)), "other outputs changed"
+
+
+@pytest.mark.parametrize("m", [1, 7, 40, 70])
+def test_gate_and_up_the_same_matrix(qll_gpu, m):
+    layer = Layer(32, m, 70, 256)
+    layer.raw, layer.w, layer.products = layer.raw * 2, layer.w * 2, layer.products * 2
+    (g, eg), (u, eu) = layer.products
+    for repacked in (False, True):
+        E.assert_bound(run_gated(layer, repacked, "relu"), *E.gated(g, eg, u, eu, "relu"), "relu")
+
+
+def test_outputs_past_32_bits(qll_gpu):
+    """65600 x 33000 outputs, the residual in place: the last rows are those of
+    a small call."""
+    m, n, k, last = 65600, 33000, 32, 70
+    rng = np.random.default_rng(33)
+    w = [pack_q4_0(*synth.q4_0_weights(rng, n, k)) for _ in range(2)]
+    xq = quantize_q8_0(synth.normal_f32(rng, (m, k)))
+    tail = xq.reshape(m, -1)[-last:].clone().reshape(-1)  # (the slice itself is not 16-byte aligned)
+    y, ys = torch.ones(m * n, device="cuda"), torch.ones(last * n, device="cuda")
+    b = dev(synth.normal_f32(rng, (n,)))
+    for rows, q, out in ((m, xq, y), (last, tail, ys)):
+        ws = workspace(qll.QLL_OP_Q4_0_LINEAR, rows, n, k)
+        qll.qll_q4_0_q8_0_linear(w[0], q, b, qll.QLL_ACT_GELU, out, out, rows, n, k, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-last * n:], ys)
+    for rows, q, out in ((m, xq, y), (last, tail, ys)):
+        ws = workspace(qll.QLL_OP_Q4_0_GATED, rows, n, k)
+        qll.qll_q4_0_q8_0_gated(*w, q, qll.QLL_ACT_SILU, out, rows, n, k, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-last * n:], ys)
