@@ -361,8 +361,8 @@ int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const f
  * it is stored: bias float[n] or NULL, act a QLL_ACT_* value, residual
  * float[m][n] or NULL.  residual may be y itself (an accumulation in place);
  * otherwise y must not overlap an input.  Without bias, activation and
- * residual the result is that of qll_q4_0_q8_0_gemm bit for bit, but at 33 <= m
- * <= 64 on small matrices (n * k < 2^24), where the order of the f32 sum differs.
+ * residual the result is that of qll_q4_0_q8_0_gemm bit for bit, but at 17 <= m
+ * <= 64, where the order of the f32 sum can differ.
  * QLL_ERR_VALUE for an unknown act. */
 int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int act, const float *residual, float *y,
                          int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);

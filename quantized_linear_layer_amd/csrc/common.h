@@ -228,6 +228,17 @@ hipError_t launch_q4_0_q8_0_gemv_f32(const uint8_t *w, const float *x, float *y,
 size_t q4_0_gemv_f32_workspace(int64_t m, int64_t n, int64_t k);
 size_t q4_0_q8_0_gemm_workspace(int64_t m, int64_t n, int64_t k);
 // The same products with an epilogue, on the same kernels and workspaces.
+//
+// 17 <= m <= 64: groups of 16 rows in one launch instead of one of 32 rows after
+// another.  More and smaller workgroups count for more than reading the weights
+// again (m = 37 in us, 1440 -> 4099 9.4 -> 8.0, 4096 -> 4096 13.2 -> 10.5, 8192 -> 8192
+// 38.3 -> 32.3; m = 64, 4096 -> 6144 29.0 -> 18.1), but on tall and large matrices, which
+// fill the CUs with 32 rows (14336 x 4096: m = 32 19.0 -> 19.9, m = 37 28.8 -> 31.8).
+inline bool q4_row_groups(int64_t m, int64_t n, int64_t k)
+{
+    return m > 16 && m <= 64 && k >= kMinKMfma && k < kMaxKMfma &&
+           (n < 12288 || (n < 32768 && n * k < ((int64_t)1 << 25)));
+}
 hipError_t launch_sum_splits_linear(const float *parts, float *y, int64_t m, int64_t n, int splits,
                                     const LinearEpilogue &ep, hipStream_t s);
 hipError_t launch_q4_0_q8_0_gemv_linear(const uint8_t *w, const uint8_t *xq, float *y, int64_t n, int64_t k,

@@ -1310,11 +1310,7 @@ static hipError_t launch_small(const uint8_t *w, const uint8_t *xq, float *y, in
 {
     if (m == 1 && k <= kMaxKQ4Gemv)
         return gemv_one(w, xq, y, n, k, ep, s);
-    // 33 <= m <= 64 on small matrices: a linear epilogue's groups of 32 rows in
-    // one launch, where the second launch would cost more than reading the
-    // weights apart saves (m = 37: 1440 -> 4099 13.5 -> 9.7 us, 4096 -> 2048 12.7
-    // -> 8.4; 4096 -> 4096 13.6 -> 15.0)
-    if (EP::kLinear && m > kMaxMMfma && k >= kMinKMfma && n < 32768 && n * k < ((int64_t)1 << 24))
+    if (EP::kLinear && q4_row_groups(m, n, k))
         return small_m(w, xq, y, m, n, k, ep, s);
     if (m > kMaxMMfma) {
         // groups of at most 32 activation rows (a last group of one row: the

@@ -320,11 +320,11 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row0 = (int64_t)blockIdx.x * OR;
-    if constexpr (EP::kGated || EP::kLinear) { // a group of at most 32 rows per blockIdx.y
-        const int64_t a0 = (int64_t)blockIdx.y * kMaxMMfma;
+    if constexpr (EP::kGated || EP::kLinear) { // a group of at most MP rows per blockIdx.y
+        const int64_t a0 = (int64_t)blockIdx.y * MP;
         xq += a0 * nb * 34;
         y += a0 * n;
-        m = m - a0 < kMaxMMfma ? m - a0 : kMaxMMfma;
+        m = m - a0 < MP ? m - a0 : MP;
         ep = ep.rows(a0, n);
     }
     const uint8_t *wt = w + row0 * ((int64_t)nb * 18), *wt2 = nullptr;
@@ -346,6 +346,19 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
 #pragma unroll
         for (int i = 0; i < 4; i++)
             acc[t][i] = 0.0f;
+    // a linear epilogue's values are requested before the first stage, so that
+    // the store does not wait for a second trip to memory
+    constexpr int OUT = (16 * MT * OR + 64 * KS - 1) / (64 * KS); // outputs of a thread
+    float bias[OUT], res[OUT];
+    if constexpr (EP::kLinear) {
+#pragma unroll
+        for (int i = 0; i < OUT; i++) {
+            const int oi = threadIdx.x + 64 * KS * i, col = oi / OR, row = oi % OR;
+            const int64_t r = row0 + row < n ? row0 + row : n - 1, c = col < m ? col : m - 1;
+            bias[i] = ep.bias ? ep.bias[r] : 0.0f;
+            res[i] = ep.res ? ep.res[c * n + r] : 0.0f;
+        }
+    }
     // kSmNS stage buffers in a ring: stage s in buffer s % kSmNS, the
     // kSmNS - 1 stages after it in flight while it is computed
 #pragma unroll
@@ -389,9 +402,12 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
             v += (*reinterpret_cast<const Part *>(&stage[q][0][0]))[reg][ln];
         return v * 0.0625f;
     };
-    for (int oi = threadIdx.x; oi < 16 * MT * OR; oi += 64 * KS) {
+#pragma unroll
+    for (int i = 0; i < OUT; i++) {
         // activation row col and weight row row of the workgroup's tile
-        const int col = oi / OR, row = oi % OR;
+        const int oi = threadIdx.x + 64 * KS * i, col = oi / OR, row = oi % OR;
+        if (16 * MT * OR % (64 * KS) != 0 && oi >= 16 * MT * OR)
+            break;
         const int u = row >> 4, t = col >> 4;
         const int reg = 4 * (u * MT + t) + (row & 3), ln = 16 * ((row & 15) >> 2) + (col & 15);
         if constexpr (GATED) {
@@ -399,9 +415,13 @@ __global__ __launch_bounds__(64 * KS) void q4_0_small_m_mfma_kernel(const uint8_
             if (col < m && row0 + row < n)
                 y[(int64_t)col * n + row0 + row] = activate(g, ep.act) * up;
         } else {
-            const float v = total(reg, ln);
+            float v = total(reg, ln);
+            if constexpr (EP::kLinear) {
+                v = activate(v + bias[i], ep.act);
+                v = ep.res ? v + res[i] : v;
+            }
             if (col < m && row0 + row < n)
-                y[(int64_t)col * n + row0 + row] = epilogue(ep, v, col, row0 + row, n);
+                y[(int64_t)col * n + row0 + row] = v;
         }
     }
 }
@@ -545,7 +565,7 @@ static void launch_sm(const SmArgs<EP> &a)
     if constexpr (sm_per_cu<T, MP, EP::kGated>(KS) >= 1) {
         const int rows = EP::kGated ? 16 : 16 * T;
         const unsigned tiles = (unsigned)((a.n + rows - 1) / rows);
-        const unsigned groups = (unsigned)((a.m + kMaxMMfma - 1) / kMaxMMfma); // 1 for the plain products
+        const unsigned groups = (unsigned)((a.m + MP - 1) / MP); // 1 for the plain products
         hipLaunchKernelGGL((q4_0_small_m_mfma_kernel<T, MP, KS, EP>), dim3(tiles, groups), dim3(64 * KS), 0, a.s, a.w,
                            a.xq, a.y, a.m, a.n, a.nb, a.ep);
     }
@@ -620,16 +640,35 @@ static void launch_sh(const SmArgs<EP> &a)
                        a.xq, a.y, a.m, a.n, a.nb, a.ep);
 }
 
+// Waves per 16 columns where one launch holds groups of 16 rows (q4_row_groups):
+// the rule above on all the workgroups, but down to one stage a wave (m = 32,
+// 1024 -> 1024: 3.6 us with four waves of one, 4.1 with two of two).
+template <int T, bool GATED>
+static int small_m_groups_split(int64_t m, int64_t n, int nb)
+{
+    const int64_t wgs = (n + 15) / 16 * ((m + 15) / 16), nst = (nb + kSmSB - 1) / kSmSB;
+    int ks = 8;
+    while (ks > 1 && (nst < ks || wgs > 256 * sm_per_cu<T, 16, GATED>(ks)))
+        ks /= 2;
+    return ks;
+}
+
 template <class EP>
 static hipError_t launch_small_m(const uint8_t *w, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,
                                  const EP &ep, hipStream_t s)
 {
-    if (m < 1 || m > (EP::kLinear ? 2 * kMaxMMfma : kMaxMMfma) || k < kMinKMfma || k >= kMaxKMfma)
+    const bool groups = EP::kLinear && q4_row_groups(m, n, k);
+    if (m < 1 || (m > kMaxMMfma && !groups) || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
     if ((n + 15) / 16 > 0x7fffffff)
         return hipErrorInvalidConfiguration;
     const int mp = sm_rows(m);
     const SmArgs<EP> a{w, xq, y, m, n, (int)(k / 32), ep, s};
+    if (groups) {
+        if constexpr (EP::kLinear)
+            launch_sm_ks<1, 16>(small_m_groups_split<1, false>(m, n, a.nb), a);
+        return hipGetLastError();
+    }
     if (small_m_mfma_shared(m, n, k)) { // m > 4: 8, 16 or 32 staged rows
         if (mp == 8)
             launch_sh<8>(a);
@@ -669,39 +708,39 @@ hipError_t launch_q4_0_q8_0_small_m_mfma_linear(const uint8_t *w, const uint8_t 
 // Gated products: waves per 16 output columns by the rule above (the largest
 // split whose workgroups are resident at once, two stages a wave at least).
 template <int MP>
-static void launch_gated_mp(const SmArgs<GatedEpilogue> &a)
+static int gated_split(int64_t m, int64_t n, int nb)
 {
-    const int64_t tiles = (a.n + 15) / 16, nst = (a.nb + kSmSB - 1) / kSmSB;
+    const int64_t wgs = (n + 15) / 16 * ((m + MP - 1) / MP), nst = (nb + kSmSB - 1) / kSmSB;
     int ks = 8;
-    while (ks > 1 && (nst < 2 * ks || tiles > 256 * sm_per_cu<2, MP, true>(ks)))
+    while (ks > 1 && (nst < 2 * ks || wgs > 256 * sm_per_cu<2, MP, true>(ks)))
         ks /= 2;
-    launch_sm_ks<2, MP>(ks, a);
+    return ks;
 }
 
 hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
                                      int64_t m, int64_t n, int64_t k, hipStream_t s)
 {
-    if (k < kMinKMfma || k >= kMaxKMfma)
+    if (m < 1 || m > 2 * kMaxMMfma || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
     if ((n + 15) / 16 > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    // above 32 rows, groups of 32: in one launch on small matrices (m = 37, 2048 ->
-    // 2048: 10.9 -> 6.9 us; 4096 -> 4096 17.7 -> 19.5), one after another else
-    const int64_t step = n * k < ((int64_t)1 << 23) ? m : kMaxMMfma;
-    for (int64_t a0 = 0; a0 < m; a0 += step) {
-        const SmArgs<GatedEpilogue> a{wg, xq + a0 * (k / 32) * 34, y + a0 * n, m - a0 < step ? m - a0 : step, n,
-                                      (int)(k / 32), GatedEpilogue{wu, act, false}, s};
-        switch (sm_rows(a.m)) {
-        case 4: launch_gated_mp<4>(a); break;
-        case 8: launch_gated_mp<8>(a); break;
-        case 16: launch_gated_mp<16>(a); break;
-        default: launch_gated_mp<32>(a); break;
-        }
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-    }
-    return hipSuccess;
+    const SmArgs<GatedEpilogue> a{wg, xq, y, m, n, (int)(k / 32), GatedEpilogue{wu, act, false}, s};
+    // Groups of 16 rows where all their workgroups have a CU of their own (m = 32,
+    // 2048 -> 2048: 6.6 -> 5.2 us; 4096 -> 2048 7.8 -> 8.9), and above 32 rows on
+    // large matrices, where groups of 32 leave CUs idle (m = 48, 4096 -> 4096: 18.6 ->
+    // 15.6 us; 2048 -> 2048 6.8 -> 8.1).
+    const bool few = (n + 15) / 16 * ((m + 15) / 16) <= 256;
+    if (m > 16 && (few || (m > kMaxMMfma && n * k >= ((int64_t)1 << 23))))
+        launch_sm_ks<2, 16>(small_m_groups_split<2, true>(m, n, a.nb), a);
+    else if (m <= 4)
+        launch_sm_ks<2, 4>(gated_split<4>(m, n, a.nb), a);
+    else if (m <= 8)
+        launch_sm_ks<2, 8>(gated_split<8>(m, n, a.nb), a);
+    else if (m <= 16)
+        launch_sm_ks<2, 16>(gated_split<16>(m, n, a.nb), a);
+    else
+        launch_sm_ks<2, 32>(gated_split<32>(m, n, a.nb), a);
+    return hipGetLastError();
 }
 
 } // namespace qll
