@@ -244,3 +244,28 @@ def test_offsets_past_32_bits(qll_gpu):
     R.assert_close(en[-3:].cpu().numpy(), want[1], want[5], "entropy")
     assert np.array_equal(ids[-15:].cpu().numpy().reshape(3, 5), want[2])
     R.assert_close(tl[-15:].cpu().numpy().reshape(3, 5), want[3], want[4], "chosen tokens")
+
+
+@pytest.mark.parametrize("m,v,top", [(1, 128256, 20), (1, 128256, 33), (3, 200000, 64), (1, 262144, 7), (40, 50257, 64),
+                                     (200, 9000, 64), (1, 5000, 64), (1, 300000, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_joined_lists(qll_gpu, dtype, m, v, top):
+    """Few to many segments and alternatives; the best in one segment, spread over
+    all, and tied."""
+    x, tokens = logits(m * v, m, v, dtype)
+    x[0] = torch.linspace(-9, 9, v).to(dtype)
+    check(x, tokens, top)
+    x[:, :100] += 40.0
+    x[0] = 1.0
+    check(x, tokens, top)
+
+
+@pytest.mark.parametrize("left", [1, 20, 64, 65, 300])
+@pytest.mark.parametrize("m", [1, 256])
+def test_few_logits_left_by_a_mask(qll_gpu, m, left):
+    v = 30000
+    x, tokens = logits(left, m, v, torch.float32)
+    keep = torch.zeros(v, dtype=torch.bool)
+    keep[torch.randperm(v, generator=torch.Generator().manual_seed(left))[:left]] = True
+    x[:, ~keep] = -float("inf")
+    check(x, tokens, 64)
