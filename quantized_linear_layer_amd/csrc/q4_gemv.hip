@@ -1183,6 +1183,13 @@ __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *
     constexpr int CB = GmLds<M, U, PAIR>::CB;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane / kGmL, r = lane % kGmL;
+    if constexpr (EP::kLinear) { // a group of at most eight activation rows per blockIdx.y
+        const int64_t a0 = (int64_t)blockIdx.y * kMaxMSmall;
+        xin = static_cast<const uint8_t *>(xin) + a0 * nb * 34;
+        y += a0 * n;
+        m = m - a0 < M ? m - a0 : M;
+        ep = ep.rows(a0, n);
+    }
     const int nu = PAIR ? nb / 2 : nb;
     const int chunks = (nb + CB - 1) / CB;
     const int64_t row_bytes = (int64_t)nb * 18;
@@ -1220,16 +1227,23 @@ __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *
             cur[q] = nxt[q];
     }
 #pragma unroll
-    for (int q = 0; q < RW; q++)
+    for (int q = 0; q < RW; q++) {
+        float mine = 0.0f; // a linear epilogue: lane a of the 16 takes activation row a
 #pragma unroll
         for (int a = 0; a < M; a++) {
             float v = acc[q][a];
 #pragma unroll
             for (int off = kGmL / 2; off > 0; off >>= 1)
                 v += __shfl_xor(v, off);
-            if (r == 0 && row0 + q < n && a < m)
-                y[(int64_t)a * n + row0 + q] = epilogue(ep, v, a, row0 + q, n);
+            if constexpr (EP::kLinear)
+                mine = r == a ? v : mine;
+            else if (r == 0 && row0 + q < n && a < m)
+                y[(int64_t)a * n + row0 + q] = v;
         }
+        if constexpr (EP::kLinear)
+            if (r < m && row0 + q < n)
+                y[(int64_t)r * n + row0 + q] = epilogue(ep, mine, r, row0 + q, n);
+    }
 }
 
 template <int RW, int U, bool F32, class EP>
@@ -1241,7 +1255,7 @@ static hipError_t launch_gm_l(const uint8_t *w, const void *xin, float *y, int64
     const int64_t grid = (groups + kGmThreads / 64 - 1) / (kGmThreads / 64);
     if (grid > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    const dim3 gd((unsigned)grid), bd(kGmThreads);
+    const dim3 gd((unsigned)grid, EP::kLinear ? (unsigned)((m + kMaxMSmall - 1) / kMaxMSmall) : 1u), bd(kGmThreads);
 #define QLL_GM(MM)                                                                                                    \
     do {                                                                                                              \
         if (nb % 2 == 0)                                                                                              \
@@ -1312,6 +1326,10 @@ static hipError_t launch_small(const uint8_t *w, const uint8_t *xq, float *y, in
         return gemv_one(w, xq, y, n, k, ep, s);
     if (EP::kLinear && q4_row_groups(m, n, k))
         return small_m(w, xq, y, m, n, k, ep, s);
+    // rows of fewer than eight blocks: all groups of eight activation rows in one
+    // launch (m = 46, 32 -> 2979: 7.9 us, 41.6 one after another)
+    if (EP::kLinear && k < kMinKMfma)
+        return launch_gm<false>(w, xq, y, m, n, k, s, ep);
     if (m > kMaxMMfma) {
         // groups of at most 32 activation rows (a last group of one row: the
         // GEMV); each group's outputs are its own rows of y

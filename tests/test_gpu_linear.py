@@ -77,6 +77,7 @@ EPILOGUES = [("none", False, False), ("relu", True, False), ("gelu", True, True)
 # without a split k
 BLOCKS = [(1, 1, 32), (1, 67, 96), (1, 300, 4096), (1, 129, 14368), (1, 20000, 320), (1, 5, 49152),
           (2, 8200, 512), (4, 32770, 256), (5, 64, 96), (40, 70, 224),
+          (9, 8200, 224), (13, 33000, 32), (64, 130, 64), (33, 8192, 96), (16, 50, 192),
           (3, 200, 1024), (8, 33, 256), (16, 300, 2048), (27, 77, 288), (20, 8200, 256), (33, 96, 512), (64, 40, 1056), (37, 4100, 4096), (64, 65600, 256), (50, 33, 288), (17, 2048, 2048),
           (48, 8200, 1056), (33, 300, 16416), (49, 14336, 2560), (64, 6144, 288),
           (7, 32800, 256), (12, 32770, 288),
