@@ -15,8 +15,10 @@
 // rounded as f64 has it, so a code depends on nothing but its own block's
 // values: not on how the sum of squares was split, nor on the launch shape.
 // Vector f64 runs at the rate of f32 here (without packed f32), so this costs
-// little: 18 or so operations an element against the 39 that 5 bytes an element
-// leave at 5 TB/s.
+// little: 25 instructions an element, counted, against the 47 that the 7 bytes of a
+// bf16 stream with residual leave at 5.8 TB/s (20 for the 3 bytes of one without).
+// Measured: 8192 x 4096 f32 with residual to Q8_0 75 us (438 MB, 5.8 TB/s), 4096 x 6912
+// bf16 with residual to int8 46 us (198 MB, 4.3 TB/s); one row of 4096 3.0 us.
 #include "common.h"
 
 namespace qll {

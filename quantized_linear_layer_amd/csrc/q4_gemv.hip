@@ -513,7 +513,8 @@ hipError_t launch_q4_0_q8_0_gemv_linear(const uint8_t *w, const uint8_t *xq, flo
 // group holding the same units of row j of both matrices, so the product is
 // formed where the two sums are.  One launch and one staging of the activation
 // row for both matrices; the weight stream (twice 18/32 bytes a weight) bounds
-// it.  Two units per lane and matrix: four loads in flight, as in the GEMV.
+// it: 2 x 14336 x 4096 (66 MB) 10.5 to 12.3 us.  Two units per lane and matrix: four
+// loads in flight, as in the GEMV.
 template <int L, bool PAIR>
 __global__ __launch_bounds__(kGemvThreads) void q4_0_gated_gemv_kernel(const uint8_t *__restrict__ wg,
                                                                        const uint8_t *__restrict__ wu,
