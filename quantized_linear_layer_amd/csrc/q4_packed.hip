@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256) void q4p_prep_kernel(const uint8_t *__restrict
     }
     uint8_t *chunk = p.x + c * kPXChunk;
     store_planes6(chunk, r, hd);
-    store_planes6(chunk + 3072, r, ld);
+    store_planes6(chunk + kPWChunk, r, ld);
     p.dx[c * PBM + r] = (uint16_t)d;
 }
 
@@ -449,8 +449,8 @@ __device__ __forceinline__ void q4p_read_b(const QLL_LDS char *base, const Q4pLa
     const u32x2 w1 = q4p_lds<u32x2>(base, o.w1[j] + kb * WC);
     b.m = i32x8{(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], 0, 0};
     if (Q8W) { // the l half of the weight codes, 3072 bytes further
-        const u32x4 v0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + 3072 + 16 * STEP * j);
-        const u32x2 v1 = q4p_lds<u32x2>(base, o.w1[j] + kb * WC + 3072);
+        const u32x4 v0 = q4p_lds<u32x4>(base, o.w0 + kb * WC + kPWChunk + 16 * STEP * j);
+        const u32x2 v1 = q4p_lds<u32x2>(base, o.w1[j] + kb * WC + kPWChunk);
         b.l = i32x8{(int)v0[0], (int)v0[1], (int)v0[2], (int)v0[3], (int)v1[0], (int)v1[1], 0, 0};
     }
     const uint32_t d = q4p_lds<uint16_t>(base, o.dw + kb * 2 * PBN + 2 * STEP * j);
