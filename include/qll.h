@@ -361,8 +361,8 @@ int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const f
  * it is stored: bias float[n] or NULL, act a QLL_ACT_* value, residual
  * float[m][n] or NULL.  residual may be y itself (an accumulation in place);
  * otherwise y must not overlap an input.  Without bias, activation and
- * residual the result is that of qll_q4_0_q8_0_gemm bit for bit, but at 17 <= m
- * <= 64, where the order of the f32 sum can differ.
+ * residual the result is that of qll_q4_0_q8_0_gemm bit for bit up to m = 16;
+ * above, the order of the f32 sum can differ.
  * QLL_ERR_VALUE for an unknown act. */
 int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int act, const float *residual, float *y,
                          int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);
@@ -380,8 +380,8 @@ int qll_q4_0_repacked_q8_0_linear(const void *wp, const void *xq, const float *b
  * y: float[m][n]; each product with the arithmetic of qll_q4_0_q8_0_gemm
  * (exact int32 block sums, f32 scaling).  k % 32 == 0 and k < 2^24.
  * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4_0_GATED, m, n, k) bytes
- * (0 for m <= 64 with k >= 256, and for m == 1); contents on return are
- * unspecified. */
+ * (0 for m <= 64 with k >= 256, for m == 1 and for other small products);
+ * contents on return are unspecified. */
 int qll_q4_0_q8_0_gated(const void *wg, const void *wu, const void *xq, int act, float *y, int64_t m, int64_t n,
                         int64_t k, void *ws, size_t ws_bytes, void *stream);
 

@@ -139,7 +139,9 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
     case QLL_OP_Q4_0_LINEAR:
         if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || (m > kMaxMSmall && k >= kMaxGemmK))
             return SIZE_MAX;
-        return q4_small_m_path(m, n, k) ? 0 : q4_0_q8_0_gemm_workspace(m, n, k);
+        return (op == QLL_OP_Q4_0_LINEAR ? q4_linear_small(m, n, k) : q4_small_m_path(m, n, k))
+                   ? 0
+                   : q4_0_q8_0_gemm_workspace(m, n, k);
     case QLL_OP_TERNARY_GEMM:
         if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 16 != 0)
             return SIZE_MAX;
@@ -170,7 +172,7 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
             return SIZE_MAX;
         if (op == QLL_OP_Q4_0_REPACKED_GATED)
             return q4_0_packed_gated_workspace(m, n, k);
-        return q4_gated_small(m, k) ? 0 : q4_0_gated_gemm_workspace(m, n, k);
+        return q4_gated_small(m, n, k) ? 0 : q4_0_gated_gemm_workspace(m, n, k);
     case QLL_OP_TOKEN_LOGPROBS:
         if (!logprob_dims_ok(m, n, k))
             return SIZE_MAX;
@@ -551,7 +553,7 @@ int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int a
         return QLL_ERR_ALIGN;
     const uint8_t *wb = static_cast<const uint8_t *>(w), *xb = static_cast<const uint8_t *>(xq);
     const LinearEpilogue ep{bias, residual, act};
-    if (q4_small_m_path(m, n, k)) {
+    if (q4_linear_small(m, n, k)) {
         if (int rc = check_device())
             return rc;
         return launched(launch_q4_0_q8_0_gemv_m_linear(wb, xb, y, m, n, k, ep, as_stream(stream)));
@@ -599,7 +601,7 @@ int qll_q4_0_q8_0_gated(const void *wg, const void *wu, const void *xq, int act,
         return QLL_ERR_ALIGN;
     const uint8_t *g = static_cast<const uint8_t *>(wg), *u = static_cast<const uint8_t *>(wu),
                   *x = static_cast<const uint8_t *>(xq);
-    if (q4_gated_small(m, k)) {
+    if (q4_gated_small(m, n, k)) {
         if (int rc = check_device())
             return rc;
         if (m == 1 && k <= kMaxKQ4Gemv)

@@ -229,15 +229,37 @@ size_t q4_0_gemv_f32_workspace(int64_t m, int64_t n, int64_t k);
 size_t q4_0_q8_0_gemm_workspace(int64_t m, int64_t n, int64_t k);
 // The same products with an epilogue, on the same kernels and workspaces.
 //
-// 17 <= m <= 64: groups of 16 rows in one launch instead of one of 32 rows after
-// another.  More and smaller workgroups count for more than reading the weights
-// again (m = 37 in us, 1440 -> 4099 9.4 -> 8.0, 4096 -> 4096 13.2 -> 10.5, 8192 -> 8192
-// 38.3 -> 32.3; m = 64, 4096 -> 6144 29.0 -> 18.1), but on tall and large matrices, which
-// fill the CUs with 32 rows (14336 x 4096: m = 32 19.0 -> 19.9, m = 37 28.8 -> 31.8).
+// From 17 rows: groups of 16 rows in one launch.  Up to 64 rows, instead of one
+// group of 32 rows after another: more and smaller workgroups count for more than
+// reading the weights again (m = 37 in us, 1440 -> 4099 9.4 -> 8.0, 4096 -> 4096 13.2 ->
+// 10.5, 8192 -> 8192 38.3 -> 32.3; m = 64, 4096 -> 6144 29.0 -> 18.1), but on tall and large
+// matrices, which fill the CUs with 32 rows (14336 x 4096: m = 32 19.0 -> 19.9, m = 37
+// 28.8 -> 31.8).  Above 64 rows, instead of the GEMM and its activation prepass and
+// split sum, while the work is small (m = 128, 1024 -> 1024 19.5 -> 4.3, 2048 -> 2048 22.2
+// -> 7.9, 4096 -> 4096 29.7 -> 20.7; 3.2e9 products are even: m = 192, 4096 -> 4096 34.3
+// and 34.2; m = 256 35.9 -> 40.5), and so are the outputs, many of which favour the
+// GEMM where k is short (512 -> 4096: m = 512 27.4 -> 19.3, m = 1024 30.1 -> 33.1).
+inline bool q4_small_work(int64_t m, int64_t n, int64_t k)
+{
+    return m <= 4096 && n < 32768 && m * n <= ((int64_t)1 << 21) && m * n <= (((int64_t)3 << 30) - 1) / k;
+}
 inline bool q4_row_groups(int64_t m, int64_t n, int64_t k)
 {
-    return m > 16 && m <= 64 && k >= kMinKMfma && k < kMaxKMfma &&
-           (n < 12288 || (n < 32768 && n * k < ((int64_t)1 << 25)));
+    if (m <= 16 || k < kMinKMfma || k >= kMaxKMfma)
+        return false;
+    return m <= 64 ? n < 12288 || (n < 32768 && n * k < ((int64_t)1 << 25)) : q4_small_work(m, n, k);
+}
+// The linear entry without a workspace: those groups, the kernels of the plain
+// product up to 64 rows, and groups of eight rows where rows have fewer than eight
+// blocks and, above 16 rows, the outputs are few (m = 128, 64 -> 1024 19.3 -> 11.3 us, m = 256 19.6 ->
+// 20.4).
+inline bool q4_linear_small(int64_t m, int64_t n, int64_t k)
+{
+    if (m <= kMaxMSmall)
+        return true;
+    if (k < kMinKMfma)
+        return m <= 16 || m * n <= ((int64_t)1 << 18);
+    return (m <= 64 && k < kMaxKMfma) || q4_row_groups(m, n, k);
 }
 hipError_t launch_sum_splits_linear(const float *parts, float *y, int64_t m, int64_t n, int splits,
                                     const LinearEpilogue &ep, hipStream_t s);
@@ -253,8 +275,12 @@ hipError_t launch_q4_0_packed_gemm_linear(const uint8_t *wp, const uint8_t *xq, 
                                           int64_t k, const LinearEpilogue &ep, void *ws, hipStream_t s);
 // Gated products y = act(X.Wg^T) * (X.Wu^T): the GEMV at m = 1 up to
 // kMaxKQ4Gemv, the small-m matrix-core kernel where q4_gated_small holds
-// (groups of at most 32 rows), the 128-row GEMM otherwise.
-inline bool q4_gated_small(int64_t m, int64_t k) { return m == 1 || (m <= 64 && k >= kMinKMfma); }
+// (groups of at most 32 rows; above 64 rows m = 128, 1024 -> 2 x 1024 19.2 -> 4.9 us, 4096 ->
+// 2 x 4096 34.7 -> 29.2; m = 192 44.8 -> 47.4), the 128-row GEMM otherwise.
+inline bool q4_gated_small(int64_t m, int64_t n, int64_t k)
+{
+    return m == 1 || (k >= kMinKMfma && (m <= 64 || q4_small_work(m, n, k)));
+}
 hipError_t launch_q4_0_gated_gemv(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
                                   int64_t n, int64_t k, hipStream_t s);
 hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,

@@ -738,7 +738,7 @@ static int gated_split(int64_t m, int64_t n, int nb)
 hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
                                      int64_t m, int64_t n, int64_t k, hipStream_t s)
 {
-    if (m < 1 || m > 2 * kMaxMMfma || k < kMinKMfma || k >= kMaxKMfma)
+    if (!q4_gated_small(m, n, k) || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
     if ((n + 15) / 16 > 0x7fffffff)
         return hipErrorInvalidConfiguration;
@@ -746,9 +746,9 @@ hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const
     // Groups of 16 rows where all their workgroups have a CU of their own (m = 32,
     // 2048 -> 2048: 6.6 -> 5.2 us; 4096 -> 2048 7.8 -> 8.9), and above 32 rows on
     // large matrices, where groups of 32 leave CUs idle (m = 48, 4096 -> 4096: 18.6 ->
-    // 15.6 us; 2048 -> 2048 6.8 -> 8.1).
+    // 15.6 us; 2048 -> 2048 6.8 -> 8.1), or above 64 rows.
     const bool few = (n + 15) / 16 * ((m + 15) / 16) <= 256;
-    if (m > 16 && (few || (m > kMaxMMfma && n * k >= ((int64_t)1 << 23))))
+    if (m > 16 && (few || m > 64 || (m > kMaxMMfma && n * k >= ((int64_t)1 << 23))))
         launch_sm_ks<2, 16>(small_m_groups_split<2, true>(m, n, a.nb), a);
     else if (m <= 4)
         launch_sm_ks<2, 4>(gated_split<4>(m, n, a.nb), a);

@@ -80,7 +80,7 @@ def refusals(f, ok, at, expect):
 
 def test_linear(L):
     big = 2 ** 40
-    ok = [GOOD, GOOD, GOOD, 2, GOOD, GOOD, 100, 8, 256, GOOD, big, None]
+    ok = [GOOD, GOOD, GOOD, 2, GOOD, GOOD, 512, 8192, 1024, GOOD, big, None]  # large enough for the 128-row GEMM
     for f, ws_null in ((L.qll_q4_0_q8_0_linear, WORKSPACE), (L.qll_q4_0_repacked_q8_0_linear, NULL)):
         for i in (0, 1, 5):
             refusals(f, ok, {i: NUL}, NULL)
@@ -94,15 +94,19 @@ def test_linear(L):
         refusals(f, ok, {10: 16}, WORKSPACE)
     # one row: the GEMV's limit on k
     refusals(L.qll_q4_0_q8_0_linear, ok, {6: 1, 8: 49152 + 32}, SHAPE)
-    for m, n, k in ((1, 4096, 4096), (64, 4096, 4096), (65, 257, 1024), (512, 4096, 14336)):
+    for m, n, k in ((1, 4096, 4096), (64, 4096, 4096), (512, 8192, 1024), (512, 4096, 14336)):
         assert qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k) == \
             qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_Q8_0_GEMM, m, n, k)
     assert qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, 2, 8, 40) == SIZE_MAX
+    for m, n, k in ((65, 257, 1024), (4096, 20, 256), (16, 2 ** 20, 96), (512, 512, 64), (191, 4096, 4096)):
+        assert qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k) == 0
+    for m, n, k in ((4097, 20, 256), (192, 4096, 4096), (65, 32768, 256), (65, 32767, 256), (513, 512, 64), (2 ** 31 - 1, 2, 2 ** 23)):
+        assert 0 < qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k)
 
 
 def test_gated(L):
     big = 2 ** 40
-    ok = [GOOD, GOOD, GOOD, 4, GOOD, 100, 8, 256, GOOD, big, None]
+    ok = [GOOD, GOOD, GOOD, 4, GOOD, 512, 8192, 1024, GOOD, big, None]
     f = L.qll_q4_0_q8_0_gated
     for i in (0, 1, 2, 4):
         refusals(f, ok, {i: NUL}, NULL)

@@ -81,7 +81,8 @@ BLOCKS = [(1, 1, 32), (1, 67, 96), (1, 300, 4096), (1, 129, 14368), (1, 20000, 3
           (3, 200, 1024), (8, 33, 256), (16, 300, 2048), (27, 77, 288), (20, 8200, 256), (33, 96, 512), (64, 40, 1056), (37, 4100, 4096), (64, 65600, 256), (50, 33, 288), (17, 2048, 2048),
           (48, 8200, 1056), (33, 300, 16416), (49, 14336, 2560), (64, 6144, 288),
           (7, 32800, 256), (12, 32770, 288),
-          (65, 257, 1024), (130, 129, 96), (128, 128, 4096), (257, 132, 544)]
+          (65, 257, 1024), (130, 129, 96), (128, 128, 4096), (257, 132, 544), (512, 300, 256), (1000, 17, 288),
+          (4096, 20, 256), (4097, 20, 256), (130, 2100, 96), (64, 4100, 224), (70, 32800, 256), (2000, 130, 64)]
 
 
 @pytest.mark.parametrize("m,n,k", BLOCKS)
@@ -92,7 +93,7 @@ def test_linear(qll_gpu, m, n, k):
         got = run_linear(layer, False, bias, act, residual)
         want, bound = E.linear(v, ev, layer.bias if bias else None, act, layer.residual if residual else None)
         E.assert_bound(got, want, bound, f"{act} bias={bias} residual={residual}")
-        if act == "none" and not 16 < m <= 64:
+        if act == "none" and (m <= 16 or (m > 64 and qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k))):  # the same kernels
             plain = q4_gemm(layer.w[0], layer.xq, m, n, k)
             torch.cuda.synchronize()
             assert np.array_equal(got.view(np.uint32), plain.cpu().numpy().reshape(m, n).view(np.uint32)), \
@@ -153,7 +154,8 @@ GATED = [(1, 1, 32), (1, 67, 96), (1, 300, 4096), (1, 33, 14368), (1, 20000, 320
          (2, 200, 1024), (4, 33, 256), (6, 16, 4096), (8, 300, 2048), (12, 4100, 256), (16, 15, 8192), (27, 77, 288),
          (32, 5000, 512), (33, 96, 512), (64, 40, 1056), (9, 16500, 256), (37, 2100, 4096), (64, 33000, 256), (20, 1024, 1024),
          (64, 500, 2080), (48, 4100, 2080), (61, 300, 512), (17, 4096, 1024),
-         (2, 64, 96), (40, 70, 224), (65, 257, 1024), (130, 129, 96), (257, 132, 544), (128, 64, 4096)]
+         (2, 64, 96), (40, 70, 224), (65, 257, 1024), (130, 129, 96), (257, 132, 544), (128, 64, 4096),
+         (500, 33, 1056), (4096, 20, 256), (4097, 20, 256), (70, 33000, 256), (4100, 40, 4096)]
 
 
 @pytest.mark.parametrize("m,n,k", GATED)

@@ -28,7 +28,7 @@ def test_short_strided_and_host_tensors(qll_gpu):
 
 def test_workspaces_and_shapes(qll_gpu):
     f = torch.float32
-    m, n, k = 65, 8, 32
+    m, n, k = 65, 4100, 32
     w, xq, y = empty(n * 18), empty(m * 34), empty(m * n, f)
     need = qll.qll_workspace_bytes(qll.QLL_OP_Q4_0_LINEAR, m, n, k)
     for ws in (None, empty(need - 1)):
