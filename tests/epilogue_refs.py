@@ -7,7 +7,7 @@ term, the conversion, the scale product and the fma).  An activation has slope
 at most 1.13; its own evaluation, x / (1 + exp(-t)), has a relative error of
 a few steps plus exp's argument rounding |t| 2^-22 (t a cubic of x with four
 roundings); the erf form's argument rounding moves erfc(z) by 2 z^2 2^-23
-relative, and the library function is good to 16 steps with room."""
+relative, and a fit of erfc and its evaluation are good to 16 steps with room."""
 import numpy as np
 from scipy import special
 
