@@ -164,18 +164,22 @@ struct WaveTop {
         publish<NW>(x, mx, (k + NW - 1) / NW, idx, shared);
         __syncthreads();
         const uint32_t none = order_bits(-INFINITY);
-        uint64_t b = ~0ull;
+        uint64_t b = ~0ull, most = 0;
         int some = 0; // waves with enough logits that are not masked
 #pragma unroll
         for (int w = 0; w < NW; w++) {
             const uint64_t o = shared_load(shared + w);
             some += (uint32_t)(o >> 32) != none;
             b = o < b ? o : b;
+            most = o > most ? o : most;
         }
-        if ((uint32_t)(b >> 32) == none) {
-            // the others find k among themselves, if they can (a row's last
-            // segment, masked rows)
-            const int j = some ? (k + some - 1) / some : k;
+        const bool masked = some < NW && some > 0, equal = (uint32_t)(b >> 32) == (uint32_t)(most >> 32);
+        if (masked || equal) {
+            // A row's last segment, or masked logits: the waves that have enough of
+            // them find k among themselves, if they can.  Equal logits in all waves
+            // (or nothing left): the least index is the last wave's, so one wave's own k
+            // are the better bound.
+            const int j = masked ? (k + some - 1) / some : k;
             __syncthreads();
             publish<NW>(x, mx, j, idx, shared);
             __syncthreads();
@@ -188,8 +192,9 @@ struct WaveTop {
                     found += j;
                     least = o < least ? o : least;
                 }
+                b = j >= k && o > b ? o : b;
             }
-            b = found >= k ? least : b;
+            b = masked && found >= k && least > b ? least : b;
         }
         tv = order_value(__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)));
         tlo = __builtin_amdgcn_readfirstlane((uint32_t)b);
