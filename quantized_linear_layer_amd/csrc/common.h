@@ -47,6 +47,31 @@ __device__ __forceinline__ u32x4 load4_a4(const uint8_t *p)
     return *reinterpret_cast<const u32x4_a4 *>(p);
 }
 
+// One wave-wide global -> LDS load: lane l reads 16 bytes at base + off (base
+// uniform, in scalar registers; the address need only be 2-byte aligned) and the
+// wave writes them to LDS at lds + 16 l.  Inline assembly keeps these loads out of
+// the compiler's wait bookkeeping, and so out of its hazard bookkeeping too: a load
+// that takes its LDS address from M0 has to come one wait state or more after the
+// scalar write of M0, which the s_nop is for.
+__device__ __forceinline__ void lds_dma16(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma16(const void *base, uint32_t off,
+                                          const __attribute__((address_space(3))) void *lds)
+{
+    lds_dma16(base, off, (uint32_t)(uintptr_t)lds);
+}
+// The same with two bytes a lane, zero-extended to lds + 4 l.
+__device__ __forceinline__ void lds_dma2(const void *base, uint32_t off,
+                                         const __attribute__((address_space(3))) void *lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_ushort %0, %1" ::"v"(off), "s"(base),
+                 "s"((uint32_t)(uintptr_t)lds)
+                 : "memory", "m0");
+}
+
 // Q8_0 code of x for the block scale d (IEEE f32 division, ties away from
 // zero, clamped to +-127; d = 0 gives 0).
 __device__ __forceinline__ int quant_code(float x, float d)

@@ -287,13 +287,6 @@ struct NbLds {
     uint8_t w[NW][NbCfg<NJ, NW>::WChunk];
 };
 
-__device__ __forceinline__ void nb_dma16(const void *base, uint32_t off, const QLL_LDS_NT void *lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
-                 "s"((uint32_t)(uintptr_t)lds)
-                 : "memory", "m0");
-}
-
 // K step kt into buffer s: the activation chunk (12 KB, three 1 KB loads per
 // wave) and the weight rows of each plane (32 bytes each, two lanes per row,
 // 32 rows per load; rows past n load row n - 1, whose outputs are dropped).
@@ -308,7 +301,7 @@ __device__ __forceinline__ void nb_load(const uint8_t *__restrict__ w, int64_t p
 #pragma unroll
     for (int j = 0; j < 3; j++) {
         const int region = 3 * wave + j;
-        nb_dma16(ab + region * 1024, 16u * lane, as + region * 1024);
+        lds_dma16(ab + region * 1024, 16u * lane, as + region * 1024);
     }
 #pragma unroll
     for (int ww = 0; ww < NW; ww++)
@@ -318,7 +311,7 @@ __device__ __forceinline__ void nb_load(const uint8_t *__restrict__ w, int64_t p
             const int row = 32 * q + (lane >> 1);
             const int64_t grow = n0 + row < n ? n0 + row : n - 1;
             const uint32_t off = (uint32_t)((grow - n0) * k * 2 + kt * 32 + 16 * nb_half(row, lane & 1));
-            nb_dma16(w + ww * plane + n0 * k * 2, off, (const QLL_LDS_NT char *)&s.w[ww][0] + 1024 * q);
+            lds_dma16(w + ww * plane + n0 * k * 2, off, (const QLL_LDS_NT char *)&s.w[ww][0] + 1024 * q);
         }
 }
 

@@ -532,15 +532,6 @@ constexpr int kLpWaves = 4, kLpRowWaves = 8;
 template <typename T, bool ROW>
 constexpr int lp_elems() { return ROW ? 2 * LpPiece<T>::V : 8; }
 
-// One wave-wide global -> LDS load: lane l reads 16 bytes at base + off (which
-// need only be aligned to 2 bytes) and the wave writes them at lds + 16 l.
-// Inline assembly keeps these loads out of the compiler's wait bookkeeping.
-__device__ __forceinline__ void lp_dma16(const void *base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
-                 : "memory", "m0");
-}
-
 // Wait until at most N vector-memory operations of this wave are outstanding.
 template <int N>
 __device__ __forceinline__ void lp_wait()
@@ -572,8 +563,8 @@ struct LpStream {
     {
 #pragma unroll
         for (int p = 0; p < P; p++)
-            lp_dma16(row, (uint32_t)sizeof(T) * (uint32_t)min(place(st, p), end - V),
-                     lds + (uint32_t)((st % S) * P + p) * 1024u);
+            lds_dma16(row, (uint32_t)sizeof(T) * (uint32_t)min(place(st, p), end - V),
+                      lds + (uint32_t)((st % S) * P + p) * 1024u);
     }
 
     // Step st into x, after it has landed; then the step S ahead is requested

@@ -219,24 +219,6 @@ __device__ __forceinline__ Q4GemmSrc q4gemm_src(const Q4GemmPrep &p, int64_t n0,
     return c;
 }
 
-// One wave-wide global -> LDS load: lane l reads `size` bytes at base + off
-// (base uniform, in scalar registers) and the wave writes them to LDS at
-// lds + 4 l (size 2, zero-extended) or lds + 16 l (size 16).  Inline
-// assembly keeps these loads out of the compiler's wait bookkeeping.
-__device__ __forceinline__ void q4gemm_dma16(const void *base, uint32_t off, const QLL_LDS void *lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
-                 "s"((uint32_t)(uintptr_t)lds)
-                 : "memory", "m0");
-}
-
-__device__ __forceinline__ void q4gemm_dma2(const void *base, uint32_t off, const QLL_LDS void *lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ushort %0, %1" ::"v"(off), "s"(base),
-                 "s"((uint32_t)(uintptr_t)lds)
-                 : "memory", "m0");
-}
-
 // Row-tile and column-tile bases of the stage loads, set once per workgroup.
 struct Q4GemmBase {
     const uint8_t *x;  // prepared activations of row m0, block 0
@@ -263,19 +245,19 @@ __device__ __forceinline__ void q4gemm_load_wave(const Q4GemmBase &g, const Q4Ge
 #pragma unroll
     for (int j = 0; j < XL; j++) {
         constexpr int r0 = WAVE * XL;
-        q4gemm_dma16(xb, c.xo[j], (const QLL_LDS void *)&s.xs[(r0 + j) / RPB][((r0 + j) % RPB) * 16][0]);
+        lds_dma16(xb, c.xo[j], (const QLL_LDS void *)&s.xs[(r0 + j) / RPB][((r0 + j) % RPB) * 16][0]);
     }
     // every wave issues exactly one of these (C0: lanes past the data
     // masked), so the per-wave load count stays QDma
     if (WAVE < 2)
-        q4gemm_dma16(g.dx + (int64_t)(b + WAVE) * g.sblk, c.so, (const QLL_LDS void *)&s.dx[WAVE][0]);
+        lds_dma16(g.dx + (int64_t)(b + WAVE) * g.sblk, c.so, (const QLL_LDS void *)&s.dx[WAVE][0]);
     else if (lane < QBM / 4)
-        q4gemm_dma16(g.c0 + (int64_t)(b + WAVE - 2) * (g.sblk / 2), c.so, (const QLL_LDS void *)&s.c0[WAVE - 2][0]);
+        lds_dma16(g.c0 + (int64_t)(b + WAVE - 2) * (g.sblk / 2), c.so, (const QLL_LDS void *)&s.c0[WAVE - 2][0]);
     constexpr int kb = WAVE >> 1, rbase = (WAVE & 1) * 64;
     const int bw = (b + kb < nb) ? b + kb : nb - 1;
     const uint8_t *wb = g.w + 18u * (uint32_t)bw;
-    q4gemm_dma16(wb + 2, c.wo, (const QLL_LDS void *)&s.wq[kb][rbase]);
-    q4gemm_dma2(wb, c.wo, (const QLL_LDS void *)&s.dw[kb][rbase]);
+    lds_dma16(wb + 2, c.wo, (const QLL_LDS void *)&s.wq[kb][rbase]);
+    lds_dma2(wb, c.wo, (const QLL_LDS void *)&s.dw[kb][rbase]);
 }
 
 // The loads of a stage; `wave` is uniform (a scalar register).

@@ -276,16 +276,6 @@ struct Q4pLds {
     uint16_t dw[PKB][PBN];
 };
 
-// One wave-wide global -> LDS load of 16 bytes per lane: lane l reads
-// base + off and the wave writes LDS at lds + 16 l.  Inline assembly keeps
-// these loads out of the compiler's wait bookkeeping.
-__device__ __forceinline__ void q4p_dma16(const void *base, uint32_t off, const QLL_LDS void *lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
-                 "s"((uint32_t)(uintptr_t)lds)
-                 : "memory", "m0");
-}
-
 // Row-tile and column-tile bases of the stage loads, set once per workgroup.
 struct Q4pSrc {
     const uint8_t *x;  // activation chunks of the row tile
@@ -311,19 +301,19 @@ __device__ __forceinline__ void q4p_load_wave(const Q4pSrc &src, int nb, int b, 
 #pragma unroll
     for (int j = 0; j < 3; j++) {
         constexpr int r0 = 3 * WAVE;
-        q4p_dma16(xb + (r0 + j) * 1024, lo, xs + (r0 + j) * 1024);
+        lds_dma16(xb + (r0 + j) * 1024, lo, xs + (r0 + j) * 1024);
     }
     if (Q8W) {
 #pragma unroll
         for (int j = 0; j < 3; j++) {
             const int region = 3 * WAVE + j, kb = region / 6, part = region % 6;
-            q4p_dma16(src.w + wblock(kb) * (uint32_t)WC + part * 1024, lo, wq + kb * WC + part * 1024);
+            lds_dma16(src.w + wblock(kb) * (uint32_t)WC + part * 1024, lo, wq + kb * WC + part * 1024);
         }
         if (lane < 16) {
             if (WAVE < 2)
-                q4p_dma16(src.dx + (uint32_t)(b + WAVE) * (uint32_t)kPSChunk, lo, (const QLL_LDS void *)&s.dx[WAVE][0]);
+                lds_dma16(src.dx + (uint32_t)(b + WAVE) * (uint32_t)kPSChunk, lo, (const QLL_LDS void *)&s.dx[WAVE][0]);
             else
-                q4p_dma16(src.dw + wblock(WAVE - 2) * (uint32_t)kPSChunk, lo,
+                lds_dma16(src.dw + wblock(WAVE - 2) * (uint32_t)kPSChunk, lo,
                           (const QLL_LDS void *)&s.dw[WAVE - 2][0]);
         }
     } else {
@@ -332,13 +322,13 @@ __device__ __forceinline__ void q4p_load_wave(const Q4pSrc &src, int nb, int b, 
         for (int j = 0; j < nw; j++) {
             const int region = WAVE < 2 ? 2 * WAVE + j : 2 + WAVE;
             const int kb = region / 3, part = region % 3;
-            q4p_dma16(src.w + wblock(kb) * (uint32_t)WC + part * 1024, lo, wq + kb * WC + part * 1024);
+            lds_dma16(src.w + wblock(kb) * (uint32_t)WC + part * 1024, lo, wq + kb * WC + part * 1024);
         }
         if (WAVE == 2 && lane < 32) {
-            q4p_dma16(src.dx + (uint32_t)b * (uint32_t)kPSChunk, lo, (const QLL_LDS void *)&s.dx[0][0]);
+            lds_dma16(src.dx + (uint32_t)b * (uint32_t)kPSChunk, lo, (const QLL_LDS void *)&s.dx[0][0]);
         } else if (WAVE == 3 && lane < 32) {
             const int bb = b + (lane >> 4) < nb ? b + (lane >> 4) : nb - 1;
-            q4p_dma16(src.dw, (uint32_t)bb * kPSChunk + 16u * (uint32_t)(lane & 15),
+            lds_dma16(src.dw, (uint32_t)bb * kPSChunk + 16u * (uint32_t)(lane & 15),
                       (const QLL_LDS void *)&s.dw[0][0]);
         }
     }

@@ -111,22 +111,12 @@ __device__ __forceinline__ void sm_offsets(int64_t m, int64_t n, int nb, int64_t
     }
 }
 
-// One wave-wide global -> LDS load: lane l reads 16 bytes at base + off and
-// the wave writes them to LDS at lds + 16 l.  The addresses need only be
-// 2-byte aligned.  Inline assembly keeps these loads out of the compiler's
-// wait bookkeeping; the waits below count them.
-__device__ __forceinline__ void sm_dma16(const void *base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
-                 : "memory", "m0");
-}
-
-// The same for the pieces from `first` of a region of `pieces`, without padding
+// lds_dma16 for the pieces from `first` of a region of `pieces`, without padding
 // behind it.
 __device__ __forceinline__ void sm_dma16_exact(int first, int pieces, const void *base, uint32_t off, uint32_t lds)
 {
     if (pieces - first >= 64 || (int)(threadIdx.x & 63) < pieces - first)
-        sm_dma16(base, off, lds);
+        lds_dma16(base, off, lds);
 }
 
 // Wait until at most N of this wave's vector-memory operations are
@@ -160,7 +150,7 @@ __device__ __forceinline__ void sm_load(const uint8_t *wt, const uint8_t *wt2, c
         if (L::EXACT)
             sm_dma16_exact(64 * i, pieces, base, off, lds + at + 1024 * i);
         else
-            sm_dma16(base, off, lds + at + 1024 * i);
+            lds_dma16(base, off, lds + at + 1024 * i);
     };
 #pragma unroll
     for (int i = 0; i < L::NX; i++)
@@ -506,10 +496,10 @@ __global__ __launch_bounds__(64 * R) void q4_0_small_m_shared_kernel(const uint8
 #pragma unroll
         for (int i = 0; i < L::NX; i++)
             if (i % R == wave) // uniform
-                sm_dma16(xb, o.x[i], xl[j] + 1024 * i);
+                lds_dma16(xb, o.x[i], xl[j] + 1024 * i);
 #pragma unroll
         for (int i = 0; i < L::NW; i++)
-            sm_dma16(wb, o.w[i], wl[j] + 1024 * i);
+            lds_dma16(wb, o.w[i], wl[j] + 1024 * i);
     };
 
     const uint32_t width = lane < 16 ? 16u : 0u; // the scale operands live in lanes 0..15

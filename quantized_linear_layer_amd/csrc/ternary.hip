@@ -460,13 +460,6 @@ __global__ __launch_bounds__(kTerGemmThreads) void ternary_gemm_kernel(
 // Words past the end of a row (a partial last chunk) are loaded from
 // clamped addresses and their code word is zeroed: code 0 adds nothing to
 // sum c q, and act_sum counts the row's real words only.
-__device__ __forceinline__ void ter_dma16(const void *base, uint32_t off, const QLL_LDS_T void *lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
-                 "s"((uint32_t)(uintptr_t)lds)
-                 : "memory", "m0");
-}
-
 // Wait until at most N vector-memory operations of this wave are
 // outstanding (and all LDS operations have completed).
 template <int N>
@@ -525,23 +518,23 @@ __device__ __forceinline__ void ter_ks_load(const uint32_t *__restrict__ w, cons
 #pragma unroll
     for (int q = 0; q < 8; q++) {
         if (FULL) {
-            ter_dma16(xq + (int64_t)w0 * 16, o.x[q], xs + 1024 * q);
+            lds_dma16(xq + (int64_t)w0 * 16, o.x[q], xs + 1024 * q);
         } else {
             const int lam = (lane & 15) ^ ((4 * q + (lane >> 4)) & 15);
             const int rel = 16 * (lam >> 3) + (lam & 7); // word within the half's runs
             const int word = w0 + rel < nw ? w0 + rel : nw - 1;
-            ter_dma16(xq, o.x[q] - (uint32_t)rel * 16u + (uint32_t)word * 16u, xs + 1024 * q);
+            lds_dma16(xq, o.x[q] - (uint32_t)rel * 16u + (uint32_t)word * 16u, xs + 1024 * q);
         }
     }
 #pragma unroll
     for (int q = 0; q < 4; q++) {
         if (FULL) {
-            ter_dma16(w + w0, o.w[q], ws + 1024 * q);
+            lds_dma16(w + w0, o.w[q], ws + 1024 * q);
         } else {
             const int row = 16 * q + (lane >> 2), gam = (lane & 3) ^ ((row >> 2) & 3);
             const int rel = 16 * (gam >> 1) + 4 * (gam & 1);
             const int word = w0 + rel + 4 <= nw ? w0 + rel : nw - 4;
-            ter_dma16(w, o.w[q] - (uint32_t)rel * 4u + (uint32_t)word * 4u, ws + 1024 * q);
+            lds_dma16(w, o.w[q] - (uint32_t)rel * 4u + (uint32_t)word * 4u, ws + 1024 * q);
         }
     }
 }
@@ -777,14 +770,14 @@ __device__ __forceinline__ void tb_part(const uint32_t *__restrict__ w, const in
 #pragma unroll
     for (int i = 0; i < 2 * NQ; i++) {
         const int qg = qa + o.wq[i] < qb ? qa + o.wq[i] : qb - 1;
-        ter_dma16(w, o.w[i] + 32u * (uint32_t)qg, (const QLL_LDS_T char *)&s.w[0] + 1024 * i);
+        lds_dma16(w, o.w[i] + 32u * (uint32_t)qg, (const QLL_LDS_T char *)&s.w[0] + 1024 * i);
     }
 #pragma unroll
     for (int j = 0; j < NQ; j++) {
         const int qg = qa + j < qb ? qa + j : qb - 1;
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            ter_dma16(xq + 128 * (int64_t)qg, o.x[i], (const QLL_LDS_T char *)&s.x[j][0][0] + 1024 * i);
+            lds_dma16(xq + 128 * (int64_t)qg, o.x[i], (const QLL_LDS_T char *)&s.x[j][0][0] + 1024 * i);
     }
     if (qb - qa == NQ) { // uniform; no branch between the steps of a whole part
 #pragma unroll
