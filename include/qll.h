@@ -424,8 +424,7 @@ int qll_q4_0_repacked_q8_0_gated(const void *wp, const void *xq, int act, float 
 
 /* Q8_0 blocks: d = binary16(f32(A / (127 rms))) per 32-block.  xq:
  * block_q8_0[m][k/32].  k % 32 == 0.  In a row whose h has NaN or an infinity in
- * it, d is NaN in every block whose products are not all zero, and the codes
- * are unspecified. */
+ * it, d is NaN in every block, and the codes are unspecified. */
 int qll_rmsnorm_q8_0(const void *x, int dtype, const void *residual, const float *weight, float eps, void *h,
                      void *xq, int64_t m, int64_t k, void *stream);
 

@@ -239,12 +239,16 @@ __device__ __forceinline__ void store_codes(uint8_t *blk, int sub, uint32_t c)
     *reinterpret_cast<u32_a2 *>(blk + 2 + 4 * sub) = c;
 }
 
-// d of a block with maximum a; scale = 1 / (127 rms).  A block of zeros has
-// d = 0, also where eps = 0 makes the row's factor infinite; in a row with NaN or
-// an infinity in it scale is NaN, and a where a block has nothing else.
+// 1 / (127 rms), v = rms^2.  A row with NaN or an infinity in it (v is NaN or
+// infinite, and inverse_root takes 0 times it) has a factor of NaN, which reaches the
+// scale of every block: a block's maximum drops its NaN, and is 0 where the others
+// are zeros.  A row of zeros with eps = 0 has 0.
+__device__ __forceinline__ double block_factor(double v) { return v == 0.0 ? 0.0 : inverse_root(v) * (1.0 / 127.0); }
+
+// d of a block with maximum a; scale: block_factor of its row.
 __device__ __forceinline__ void store_scale(uint8_t *blk, double a, double scale)
 {
-    float d = a == 0.0 ? 0.0f : (float)(a * scale);
+    float d = (float)(a * scale);
     // two roundings, as the quantizer's: the compiler would otherwise convert
     // f64 to binary16 in one (and in a long sequence of integer operations)
     asm volatile("" : "+v"(d));
@@ -339,7 +343,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_q8_0_kernel(con
     }
     double unused = 0.0;
     row_reduce<TPR, false>(ss, unused, red);
-    const double scale = inverse_root(fma(ss, inv_k, eps)) * (1.0 / 127.0);
+    const double scale = block_factor(fma(ss, inv_k, eps));
 #pragma unroll
     for (int j = 0; j < P; j++) {
         const int i = t + TPR * j;
@@ -451,7 +455,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const T *x, const T 
                 mx = fmax(mx, fabs(p[e]));
     }
     row_reduce<1024, !Q8>(ss, mx, red);
-    const double scale = inverse_root(fma(ss, inv_k, eps)) * (1.0 / 127.0);
+    const double scale = block_factor(fma(ss, inv_k, eps));
     const float sc = Q8 ? 0.0f : row_scale(fma(ss, inv_k, eps), mx);
     const double a = sc > 0.0f ? mx : 0.0, f = code_factor(a);
     int sum = 0;
