@@ -279,8 +279,10 @@ __device__ __forceinline__ int store_i8(int8_t *q8, const double (&p)[V], double
     return sum;
 }
 
+// Sum of the row's codes; sc: its scale.  In a row without one (0) the codes of NaN are
+// the low bits of NaN: zero in the byte that is stored, but not in the 32 that are summed.
 template <int TPR>
-__device__ __forceinline__ int row_sum(int sum, int *red)
+__device__ __forceinline__ int row_sum(int sum, float sc, int *red)
 {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
@@ -294,7 +296,7 @@ __device__ __forceinline__ int row_sum(int sum, int *red)
         for (int i = 0; i < TPR / 64; i++)
             sum += red[i];
     }
-    return sum;
+    return sc > 0.0f ? sum : 0;
 }
 
 // Q8_0 output.  TPR threads per row (64: four rows share a workgroup), thread
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_i8_rows_kernel(
             sum += store_i8<V>(xq + base + V * i, p, a, f);
         }
     }
-    sum = row_sum<TPR>(sum, red_i);
+    sum = row_sum<TPR>(sum, sc, red_i);
     if (t == 0) {
         act_scale[row] = sc;
         act_sum[row] = sum;
@@ -480,7 +482,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const T *x, const T 
         }
     }
     if constexpr (!Q8) {
-        sum = row_sum<1024>(sum, red_i);
+        sum = row_sum<1024>(sum, sc, red_i);
         if (threadIdx.x == 0) {
             act_scale[row] = sc;
             act_sum[row] = sum;

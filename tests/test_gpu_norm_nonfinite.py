@@ -43,3 +43,21 @@ def test_q8_0_scales_show_a_lone_nan_or_infinity(qll_gpu, m, k, dtype, eps):
         assert np.isnan(scale[bad]).all(), f"finite scales in rows {np.argwhere(~np.isnan(scale[bad]))[:4].tolist()}"
         assert np.array_equal(codes[good], want[good]) and np.array_equal(scale[good], d[good])
         assert (codes[5] == 0).all() and (scale[5] == 0).all()
+
+
+@pytest.mark.parametrize("m,k", [(3, 60), (3, 63), (3, 1000), (3, 1001), (3, 4096), (260, 4096), (3, 16381),
+                                 (258, 16384), (3, 16387), (3, 20000)])
+@pytest.mark.parametrize("where", ["x", "x alone", "residual"])
+def test_i8_rows_with_nan_of_any_bits_are_zero(qll_gpu, m, k, where):
+    x, r, w = stream_rows(m + k, m, k, torch.float32)
+    bits = torch.tensor([0x7fffffff, -1, 0x7fc00007], dtype=torch.int32)  # 0xff bytes among them
+    at = [3, k // 2, k - 1]
+    (r if where == "residual" else x)[0, at] = bits.view(torch.float32)
+    (r if where == "residual" else x)[1] = bits[1:2].view(torch.float32)  # a row filled with 0xff
+    res = None if where == "x alone" else r
+    for h in ("new", None):
+        _, codes, scale, total = call("i8", x, res, w, 1e-5, h)
+        _, want, s, t = definition(x[2:], None if res is None else res[2:], w, 1e-5, False)
+        assert (codes[:2] == 0).all() and (scale[:2] == 0).all()
+        assert (total[:2] == 0).all(), f"code sums {total[:2]}"
+        assert np.array_equal(codes[2:], want) and np.array_equal(scale[2:], s) and np.array_equal(total[2:], t)
