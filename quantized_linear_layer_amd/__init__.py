@@ -144,8 +144,10 @@ def _device(t, what):
         raise ValueError(f"{what} must be a CUDA tensor")
     if _raw_stream is None:
         import torch
-        # (the calls that torch.cuda.current_stream() and current_device() wrap, without the objects: 2.5 us a call)
-        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        # (the calls that torch.cuda.current_stream() and current_device() wrap, without the objects: 2.5 us a call;
+        # the one that is tested above comes last: another thread may be here too)
+        _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream
     if dev != _current_device():
         raise ValueError(f"{what} is on device {dev}, the current device is {_current_device()}")
     return dev
