@@ -133,12 +133,14 @@ def _stream(stream):
 
 _raw_stream = None  # torch's current stream of a device as a handle, and its current device
 _current_device = None
+_F32, _I32 = QLL_DTYPE_F32, "int32"
+_types = {}  # element types of an argument by its QLL_DTYPE_* value (or _I32): its own, or raw bits
 
 
 def _device(t, what):
     """The device that a call on `t` runs on: its own, which has to be the
     current one (a kernel is launched on the current device)."""
-    global _raw_stream, _current_device
+    global _raw_stream, _current_device, _types
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
@@ -146,6 +148,9 @@ def _device(t, what):
         import torch
         # (the calls that torch.cuda.current_stream() and current_device() wrap, without the objects: 2.5 us a call;
         # the one that is tested above comes last: another thread may be here too)
+        _types = {_F32: (torch.float32, torch.uint8), _I32: (torch.int32, torch.uint8),
+                  QLL_DTYPE_BF16: (torch.bfloat16, torch.int16, torch.uint8),
+                  QLL_DTYPE_F16: (torch.float16, torch.int16, torch.uint8)}
         _current_device = torch._C._cuda_getDevice
         _raw_stream = torch._C._cuda_getCurrentRawStream
     if dev != _current_device():
@@ -153,9 +158,11 @@ def _device(t, what):
     return dev
 
 
-def _arg(t, nbytes, what, dev):
+def _arg(t, nbytes, what, dev, type=None):
     """Device pointer of `t` (0 for None) after checking that it lies on `dev`,
-    is contiguous and can hold `nbytes` bytes."""
+    is contiguous and can hold `nbytes` bytes, and that its elements are of
+    `type`, a key of _types (int64 ids have bytes enough, and are other tokens).
+    A type that is no key is the library's to refuse."""
     if t is None:
         return None
     if t.get_device() != dev:
@@ -164,6 +171,8 @@ def _arg(t, nbytes, what, dev):
         raise ValueError(f"{what} must be contiguous")
     if t.nbytes < nbytes:
         raise ValueError(f"{what} holds {t.nbytes} bytes, the call needs {nbytes}")
+    if type in _types and nbytes > 0 and t.dtype not in _types[type]:
+        raise ValueError(f"{what} is of type {t.dtype}, the call takes {_types[type][0]}")
     return t.data_ptr()
 
 
@@ -382,8 +391,9 @@ def qll_q4_0_q8_0_linear(w, xq, bias, act, residual, y, m, n, k, ws=None, stream
     d = _device(y, "y")
     wsp, wsb = _scratch(ws, d)
     _call("qll_q4_0_q8_0_linear", _arg(w, n * (k // 32) * Q4_0_BLOCK_BYTES, "w", d),
-          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d), act,
-          _arg(residual, m * n * 4, "residual", d), _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb, _on(d, stream))
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d, _F32), act,
+          _arg(residual, m * n * 4, "residual", d, _F32), _arg(y, m * n * 4, "y", d, _F32), m, n, k, wsp, wsb,
+          _on(d, stream))
 
 
 def qll_q4_0_repacked_q8_0_linear(wp, xq, bias, act, residual, y, m, n, k, ws=None, stream=None):
@@ -391,8 +401,9 @@ def qll_q4_0_repacked_q8_0_linear(wp, xq, bias, act, residual, y, m, n, k, ws=No
     d = _device(y, "y")
     wsp, wsb = _scratch(ws, d)
     _call("qll_q4_0_repacked_q8_0_linear", _arg(wp, _repacked_need(n, k, False), "wp", d),
-          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d), act,
-          _arg(residual, m * n * 4, "residual", d), _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb, _on(d, stream))
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), _arg(bias, n * 4, "bias", d, _F32), act,
+          _arg(residual, m * n * 4, "residual", d, _F32), _arg(y, m * n * 4, "y", d, _F32), m, n, k, wsp, wsb,
+          _on(d, stream))
 
 
 def qll_q4_0_q8_0_gated(wg, wu, xq, act, y, m, n, k, ws=None, stream=None):
@@ -401,7 +412,7 @@ def qll_q4_0_q8_0_gated(wg, wu, xq, act, y, m, n, k, ws=None, stream=None):
     wsp, wsb = _scratch(ws, d)
     nb = n * (k // 32) * Q4_0_BLOCK_BYTES
     _call("qll_q4_0_q8_0_gated", _arg(wg, nb, "wg", d), _arg(wu, nb, "wu", d),
-          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb,
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d, _F32), m, n, k, wsp, wsb,
           _on(d, stream))
 
 
@@ -422,7 +433,7 @@ def qll_q4_0_repacked_q8_0_gated(wp, xq, act, y, m, n, k, ws=None, stream=None):
     d = _device(y, "y")
     wsp, wsb = _scratch(ws, d)
     _call("qll_q4_0_repacked_q8_0_gated", _arg(wp, _repacked_need(n, k, True), "wp", d),
-          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d), m, n, k, wsp, wsb,
+          _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), act, _arg(y, m * n * 4, "y", d, _F32), m, n, k, wsp, wsb,
           _on(d, stream))
 
 
@@ -437,8 +448,8 @@ def qll_rmsnorm_q8_0(x, dtype, residual, weight, eps, h, xq, m, k, stream=None):
     and h may be None, h may be x or residual."""
     d = _device(x, "x")
     nb = m * k * _esize(dtype)
-    _call("qll_rmsnorm_q8_0", _arg(x, nb, "x", d), dtype, _arg(residual, nb, "residual", d),
-          _arg(weight, k * 4, "weight", d), eps, _arg(h, nb, "h", d),
+    _call("qll_rmsnorm_q8_0", _arg(x, nb, "x", d, dtype), dtype, _arg(residual, nb, "residual", d, dtype),
+          _arg(weight, k * 4, "weight", d, _F32), eps, _arg(h, nb, "h", d, dtype),
           _arg(xq, m * (k // 32) * Q8_0_BLOCK_BYTES, "xq", d), m, k, _on(d, stream))
 
 
@@ -446,9 +457,9 @@ def qll_rmsnorm_i8_rows(x, dtype, residual, weight, eps, h, xq, act_scale, act_s
     """As qll_rmsnorm_q8_0, into int8 rows with act_scale and act_sum."""
     d = _device(x, "x")
     nb = m * k * _esize(dtype)
-    _call("qll_rmsnorm_i8_rows", _arg(x, nb, "x", d), dtype, _arg(residual, nb, "residual", d),
-          _arg(weight, k * 4, "weight", d), eps, _arg(h, nb, "h", d), _arg(xq, m * k, "xq", d),
-          _arg(act_scale, m * 4, "act_scale", d), _arg(act_sum, m * 4, "act_sum", d), m, k, _on(d, stream))
+    _call("qll_rmsnorm_i8_rows", _arg(x, nb, "x", d, dtype), dtype, _arg(residual, nb, "residual", d, dtype),
+          _arg(weight, k * 4, "weight", d, _F32), eps, _arg(h, nb, "h", d, dtype), _arg(xq, m * k, "xq", d),
+          _arg(act_scale, m * 4, "act_scale", d, _F32), _arg(act_sum, m * 4, "act_sum", d, _I32), m, k, _on(d, stream))
 
 
 # ----------------------------------------------------------------- token log probabilities
@@ -460,7 +471,7 @@ def qll_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids,
     top_logprob at top = 0, entropy always."""
     d = _device(logits, "logits")
     wsp, wsb = _scratch(ws, d)
-    _call("qll_token_logprobs", _arg(logits, m * v * _esize(dtype), "logits", d), dtype,
-          _arg(tokens, m * t * 4, "tokens", d), t, _arg(logprob, m * t * 4, "logprob", d),
-          _arg(entropy, m * 4, "entropy", d), top, _arg(top_ids, m * top * 4, "top_ids", d),
-          _arg(top_logprob, m * top * 4, "top_logprob", d), m, v, wsp, wsb, _on(d, stream))
+    _call("qll_token_logprobs", _arg(logits, m * v * _esize(dtype), "logits", d, dtype), dtype,
+          _arg(tokens, m * t * 4, "tokens", d, _I32), t, _arg(logprob, m * t * 4, "logprob", d, _F32),
+          _arg(entropy, m * 4, "entropy", d, _F32), top, _arg(top_ids, m * top * 4, "top_ids", d, _I32),
+          _arg(top_logprob, m * top * 4, "top_logprob", d, _F32), m, v, wsp, wsb, _on(d, stream))
