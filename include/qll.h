@@ -293,8 +293,8 @@ int qll_q8_0_repacked_q8_0_gemm(const void *wp, const void *xq, float *y, int64_
 /* C[m][n] = A[m][k] . B[k][n], all f32 row-major (the plain orientation of
  * [FAST] 6.4), accumulated in f32 (tolerance 1e-5 * sum_p |a*b| against an
  * f64 sum).  m == 1 runs a split-k GEMV whose partial sums go to ws in a
- * fixed order (results are bit-identical from run to run); ws: at least
- * qll_workspace_bytes(QLL_OP_SGEMM, 1, n, k) bytes.  m > 1 runs on the bf16
+ * fixed order (results are bit-identical from run to run) and takes n < 2^30; ws: at
+ * least qll_workspace_bytes(QLL_OP_SGEMM, 1, n, k) bytes.  m > 1 runs on the bf16
  * matrix core when ws holds at least qll_workspace_bytes(QLL_OP_SGEMM_BF16, m,
  * n, k) bytes and k % 16 == 0 (the workspace size selects the algorithm, as
  * in BLAS libraries): A and B (transposed on the way) are each split exactly

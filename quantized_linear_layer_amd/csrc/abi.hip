@@ -26,6 +26,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;    // every dimension below 2^31
 constexpr int64_t kMaxElems = (int64_t)1 << 40;  // and every tensor below 2^40 elements
+constexpr int64_t kMaxSgemvN = (int64_t)1 << 30; // the f32 GEMV: four threads a column in one grid
 constexpr int64_t kMaxGemmK = (int64_t)1 << 24;  // Q4_0/Q8_0 GEMMs (m > 8, repacked): 32-bit load offsets
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -132,7 +133,7 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
 {
     switch (op) {
     case QLL_OP_SGEMM:
-        if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n))
+        if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || (m == 1 && n >= kMaxSgemvN))
             return SIZE_MAX;
         return m == 1 ? sgemv_workspace(n, k) : 0;
     case QLL_OP_Q4_0_Q8_0_GEMM:
@@ -467,7 +468,7 @@ int qll_sgemm(const float *a, const float *b, float *c, int64_t m, int64_t n, in
 {
     if (!a || !b || !c)
         return QLL_ERR_NULL;
-    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n))
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || (m == 1 && n >= kMaxSgemvN))
         return QLL_ERR_SHAPE;
     if (!aligned16(a) || !aligned16(b) || !aligned16(c))
         return QLL_ERR_ALIGN;

@@ -223,6 +223,26 @@ __device__ __forceinline__ float epilogue(const EP &ep, float v, int64_t i, int6
     return v;
 }
 
+// ------------------------------------------------------------ grids
+
+// A grid has fewer than 2^32 threads in each dimension.  More wrap around without
+// an error, and the launch leaves the rest undone.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t)1 << 32; }
+
+// `count` units (rows, blocks) in launches of at most `part`: launch(first, number).
+template <class F>
+inline hipError_t launch_parts(int64_t count, int64_t part, const F &launch)
+{
+    for (int64_t first = 0; first < count; first += part) {
+        launch(first, count - first < part ? count - first : part);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+constexpr int64_t kPartThreads = (int64_t)1 << 31; // threads of such a launch
+
 // ------------------------------------------------------------ launchers
 // Each returns a hipError_t of the launch; arguments are already validated.
 

@@ -136,13 +136,11 @@ template <int WFMT, int L, int U, bool VEC>
 static hipError_t launch_nt_l(const float *x, const uint8_t *w, float *y, int64_t n, int64_t k, hipStream_t s)
 {
     constexpr int R = 64 / L;
-    const int64_t rows_per_wg = R * (kGemvNtThreads / 64);
-    const int64_t grid = (n + rows_per_wg - 1) / rows_per_wg;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((gemv_nt_kernel<WFMT, L, U, VEC>), dim3((unsigned)grid), dim3(kGemvNtThreads), 0, s, x, w, y,
-                       n, k);
-    return hipGetLastError();
+    const int64_t rows_per_wg = R * (kGemvNtThreads / 64), row_bytes = k * (WFMT == QLL_W_F32 ? 4 : 2);
+    return launch_parts(n, kPartThreads / L, [&](int64_t r0, int64_t rows) {
+        hipLaunchKernelGGL((gemv_nt_kernel<WFMT, L, U, VEC>), dim3((unsigned)((rows + rows_per_wg - 1) / rows_per_wg)),
+                           dim3(kGemvNtThreads), 0, s, x, w + r0 * row_bytes, y + r0, rows, k);
+    });
 }
 
 // Lanes per row: one pass of 4 vectors per lane for short rows, 64 lanes
@@ -593,8 +591,9 @@ hipError_t launch_gemm_nt_bf16_mfma(const float *x, const void *w, int wfmt, flo
     p.kp = k;
     const int64_t chunks = (p.mp / kNbM) * (k / kNbK);
     const int64_t count8 = n * k / 8;
-    if (chunks > 0x7fffffff || plan.tiles > 0x7fffffff || (count8 + 255) / 256 > 0x7fffffff ||
-        (b_kn && ((n + 63) / 64 > 0x7fffffff || (k + 63) / 64 > 65535)))
+    if (!grid_fits(chunks, 256) || !grid_fits(plan.tiles, kNbThreads) ||
+        (plan.nw > 1 && !b_kn && !grid_fits((count8 + 255) / 256, 256)) ||
+        (b_kn && (!grid_fits((n + 63) / 64, 256) || (k + 63) / 64 > 65535)))
         return hipErrorInvalidConfiguration;
     if (m % kNbM == 0 && k % (2 * kNbK) == 0)
         hipLaunchKernelGGL(nt_bf16_prep_full_kernel, dim3((unsigned)(chunks / 2)), dim3(256), 0, s, x, p, k);

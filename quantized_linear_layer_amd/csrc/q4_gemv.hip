@@ -438,6 +438,7 @@ __global__ __launch_bounds__(kGemvThreads) void q4_0_q8_0_gemv_kernel(const uint
 size_t q4_gemv_lds_bytes(int nb) { return (size_t)nb * 40; }
 
 constexpr int64_t kF32GemvGrid = 512;
+constexpr int64_t kMaxGemvGrid = kPartThreads / kGemvThreads;
 
 // One work item per wave: the dispatcher starts new workgroups as others
 // finish, which measured faster on the 296 MB vocabulary projection than
@@ -456,8 +457,8 @@ static hipError_t launch_l(const uint8_t *w, const void *xin, float *y, int64_t 
     // on the 296 MB vocabulary projection)
     if (F32 && grid > kF32GemvGrid)
         grid = kF32GemvGrid;
-    if (grid > 0x7fffffff)
-        grid = 0x7fffffff;
+    if (grid > kMaxGemvGrid)
+        grid = kMaxGemvGrid;
     hipLaunchKernelGGL((q4_0_q8_0_gemv_kernel<L, U, PAIR, F32, EP>), dim3((unsigned)grid), dim3(kGemvThreads),
                        q4_gemv_lds_bytes(nb), s, w, xin, y, n, nb, ep);
     return hipGetLastError();
@@ -565,17 +566,16 @@ static hipError_t launch_gated_l(const uint8_t *wg, const uint8_t *wu, const uin
                                  int64_t n, int nb, hipStream_t s)
 {
     constexpr int rows = 64 / L * (kGemvThreads / 64);
-    const int64_t grid = (n + rows - 1) / rows;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    const dim3 gd((unsigned)grid), bd(kGemvThreads);
-    if (nb % 2 == 0)
-        hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, true>), gd, bd, q4_gemv_lds_bytes(nb), s, wg, wu, xq, act, y,
-                           n, nb);
-    else
-        hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, false>), gd, bd, q4_gemv_lds_bytes(nb), s, wg, wu, xq, act, y,
-                           n, nb);
-    return hipGetLastError();
+    return launch_parts(n, kPartThreads / L, [&](int64_t r0, int64_t part) {
+        const dim3 gd((unsigned)((part + rows - 1) / rows)), bd(kGemvThreads);
+        const int64_t at = r0 * nb * 18;
+        if (nb % 2 == 0)
+            hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, true>), gd, bd, q4_gemv_lds_bytes(nb), s, wg + at, wu + at,
+                               xq, act, y + r0, part, nb);
+        else
+            hipLaunchKernelGGL((q4_0_gated_gemv_kernel<L, false>), gd, bd, q4_gemv_lds_bytes(nb), s, wg + at, wu + at,
+                               xq, act, y + r0, part, nb);
+    });
 }
 
 hipError_t launch_q4_0_gated_gemv(const uint8_t *wg, const uint8_t *wu, const uint8_t *xq, int act, float *y,
@@ -707,8 +707,8 @@ static hipError_t launch_q4p_l(const uint8_t *w, const uint8_t *xq, float *y, in
     constexpr int R = 64 / L;
     const int64_t groups = (n + R - 1) / R;
     int64_t grid = (groups + kGemvThreads / 64 - 1) / (kGemvThreads / 64);
-    if (grid > 0x7fffffff)
-        grid = 0x7fffffff;
+    if (grid > kMaxGemvGrid)
+        grid = kMaxGemvGrid;
     hipLaunchKernelGGL((q4_0_packed_gemv_kernel<L, U>), dim3((unsigned)grid), dim3(kGemvThreads),
                        q4_gemv_lds_bytes(nb), s, w, xq, y, n, nb);
     return hipGetLastError();
@@ -773,12 +773,11 @@ __global__ __launch_bounds__(256) void q4_0_pack_decode_kernel(const uint8_t *__
 hipError_t launch_q4_0_pack_decode(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
 {
     const int nb = (int)(k / 32);
-    const int64_t pieces = n * (nb + (nb + 7) / 8);
-    const int64_t grid = (pieces + 255) / 256;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(q4_0_pack_decode_kernel, dim3((unsigned)grid), dim3(256), 0, s, w, wp, n, nb);
-    return hipGetLastError();
+    const int64_t per_row = nb + (nb + 7) / 8; // pieces, fewer than 2^27
+    return launch_parts(n, kPartThreads / per_row, [&](int64_t r0, int64_t rows) {
+        hipLaunchKernelGGL(q4_0_pack_decode_kernel, dim3((unsigned)((rows * per_row + 255) / 256)), dim3(256), 0, s,
+                           w + r0 * nb * 18, wp + r0 * per_row * 16, rows, nb);
+    });
 }
 
 // ------------------------------------------------------------------ Q8_0 weights
@@ -950,8 +949,8 @@ static hipError_t launch_q8w_l(const uint8_t *w, const uint8_t *xq, float *y, in
     constexpr int R = 64 / L;
     const int64_t groups = (n + R - 1) / R;
     int64_t grid = (groups + kGemvThreads / 64 - 1) / (kGemvThreads / 64);
-    if (grid > 0x7fffffff)
-        grid = 0x7fffffff;
+    if (grid > kMaxGemvGrid)
+        grid = kMaxGemvGrid;
     hipLaunchKernelGGL((q8_0_q8_0_gemv_kernel<L, U, PAIR>), dim3((unsigned)grid), dim3(kGemvThreads),
                        q4_gemv_lds_bytes(nb), s, w, xq, y, n, nb);
     return hipGetLastError();
@@ -1178,7 +1177,7 @@ __device__ __forceinline__ void gm_compute(const GemvRaw<U> raw[RW], int64_t row
 template <int M, int RW, int U, bool PAIR, bool F32, class EP>
 __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *__restrict__ w, const void *xin,
                                                                   float *__restrict__ y, int64_t m, int64_t n, int nb,
-                                                                  EP ep)
+                                                                  int64_t first, EP ep)
 {
     __shared__ GmLds<M, U, PAIR> s;
     constexpr int CB = GmLds<M, U, PAIR>::CB;
@@ -1194,8 +1193,9 @@ __global__ __launch_bounds__(kGmThreads) void q4_0_gemv_m_kernel(const uint8_t *
     const int nu = PAIR ? nb / 2 : nb;
     const int chunks = (nb + CB - 1) / CB;
     const int64_t row_bytes = (int64_t)nb * 18;
-    // rows row0 .. row0 + RW - 1 (some may be >= n: loaded as row 0, masked)
-    const int64_t row0 = (((int64_t)blockIdx.x * (kGmThreads / 64) + wave) * (64 / kGmL) + g) * RW;
+    // rows row0 .. row0 + RW - 1 (some may be >= n: loaded as row 0, masked); first:
+    // of the launch
+    const int64_t row0 = first + (((int64_t)blockIdx.x * (kGmThreads / 64) + wave) * (64 / kGmL) + g) * RW;
 
     float acc[RW][M];
 #pragma unroll
@@ -1251,30 +1251,29 @@ template <int RW, int U, bool F32, class EP>
 static hipError_t launch_gm_l(const uint8_t *w, const void *xin, float *y, int64_t m, int64_t n, int nb,
                               const EP &ep, hipStream_t s)
 {
-    constexpr int R = 64 / kGmL * RW; // weight rows per wave
-    const int64_t groups = (n + R - 1) / R;
-    const int64_t grid = (groups + kGmThreads / 64 - 1) / (kGmThreads / 64);
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    const dim3 gd((unsigned)grid, EP::kLinear ? (unsigned)((m + kMaxMSmall - 1) / kMaxMSmall) : 1u), bd(kGmThreads);
+    constexpr int R = kGmThreads / kGmL * RW; // weight rows per workgroup
+    return launch_parts(n, kPartThreads / kGmL * RW, [&](int64_t first, int64_t rows) {
+        const dim3 gd((unsigned)((rows + R - 1) / R), EP::kLinear ? (unsigned)((m + kMaxMSmall - 1) / kMaxMSmall) : 1u);
+        const dim3 bd(kGmThreads);
 #define QLL_GM(MM)                                                                                                    \
     do {                                                                                                              \
         if (nb % 2 == 0)                                                                                              \
-            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, true, F32, EP>), gd, bd, 0, s, w, xin, y, m, n, nb, ep); \
+            hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, true, F32, EP>), gd, bd, 0, s, w, xin, y, m, n, nb,      \
+                               first, ep);                                                                            \
         else                                                                                                          \
             hipLaunchKernelGGL((q4_0_gemv_m_kernel<MM, RW, U, false, F32, EP>), gd, bd, 0, s, w, xin, y, m, n, nb,     \
-                               ep);                                                                                   \
+                               first, ep);                                                                            \
     } while (0)
-    if (m <= 1)
-        QLL_GM(1);
-    else if (m <= 2)
-        QLL_GM(2);
-    else if (m <= 4)
-        QLL_GM(4);
-    else
-        QLL_GM(8);
+        if (m <= 1)
+            QLL_GM(1);
+        else if (m <= 2)
+            QLL_GM(2);
+        else if (m <= 4)
+            QLL_GM(4);
+        else
+            QLL_GM(8);
 #undef QLL_GM
-    return hipGetLastError();
+    });
 }
 
 // 64-row workgroups (4 rows per lane group) once they number at least 512,

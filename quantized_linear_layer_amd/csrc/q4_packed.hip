@@ -149,14 +149,16 @@ template <bool GATED>
 static hipError_t launch_repack(const uint8_t *w, const uint8_t *wu, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
 {
     const int nb = (int)(k / 32);
-    const int64_t rows = GATED ? PBN / 2 : PBN, nt = (n + rows - 1) / rows;
-    const int64_t total = nt * nb * PBN;
+    const int64_t rows = GATED ? PBN / 2 : PBN, nt = (n + rows - 1) / rows, tile = (int64_t)nb * PBN;
     uint16_t *dws = reinterpret_cast<uint16_t *>(wp + (size_t)nt * nb * kPWChunk);
-    const int64_t grid = (total + 255) / 256;
-    if (grid > 0x7fffffff)
+    if (tile > kPartThreads)
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(q4p_repack_kernel<GATED>, dim3((unsigned)grid), dim3(256), 0, s, w, wu, wp, dws, n, nb, total);
-    return hipGetLastError();
+    return launch_parts(nt, kPartThreads / tile, [&](int64_t t0, int64_t tiles) {
+        const int64_t at = t0 * rows * nb * 18, total = tiles * tile;
+        hipLaunchKernelGGL(q4p_repack_kernel<GATED>, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, w + at,
+                           GATED ? wu + at : nullptr, wp + (size_t)t0 * nb * kPWChunk, dws + t0 * tile, n - t0 * rows,
+                           nb, total);
+    });
 }
 
 hipError_t launch_q4_0_repack(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s)
@@ -255,6 +257,18 @@ __global__ __launch_bounds__(256) void q4p_prep_kernel(const uint8_t *__restrict
     store_planes6(chunk, r, hd);
     store_planes6(chunk + kPWChunk, r, ld);
     p.dx[c * PBM + r] = (uint16_t)d;
+}
+
+static hipError_t launch_q4p_prep(const uint8_t *xq, const Q4pPrep &p, int64_t m, int nb, hipStream_t s)
+{
+    const int64_t tile = p.nbp * PBM;
+    if (tile > kPartThreads)
+        return hipErrorInvalidConfiguration;
+    return launch_parts(p.mp / PBM, kPartThreads / tile, [&](int64_t t0, int64_t tiles) {
+        const Q4pPrep part{p.x + t0 * p.nbp * kPXChunk, p.dx + t0 * tile, tiles * PBM, p.nbp};
+        hipLaunchKernelGGL(q4p_prep_kernel, dim3((unsigned)((tiles * tile + 255) / 256)), dim3(256), 0, s,
+                           xq + t0 * PBM * nb * 34, part, m - t0 * PBM, nb, tiles * tile);
+    });
 }
 
 // ------------------------------------------------------------------ GEMM
@@ -669,10 +683,7 @@ static hipError_t launch_packed_kernel(const uint8_t *wp, const uint8_t *xq, flo
     prep.mp = plan.mp;
     prep.nbp = plan.nbp;
     const int nb = (int)(k / 32);
-    const int64_t prep_threads = plan.mp * plan.nbp;
-    hipLaunchKernelGGL(q4p_prep_kernel, dim3((unsigned)((prep_threads + 255) / 256)), dim3(256), 0, s, xq, prep, m,
-                       nb, prep_threads);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = launch_q4p_prep(xq, prep, m, nb, s);
     if (e != hipSuccess)
         return e;
     const int64_t nt = (n + Q4pCols<EP>::kOut - 1) / Q4pCols<EP>::kOut;
@@ -749,12 +760,7 @@ hipError_t launch_q8_0_repack(const uint8_t *w, uint8_t *wp, int64_t n, int64_t 
     p.dx = reinterpret_cast<uint16_t *>(wp + (size_t)nt * nb * (2 * kPWChunk));
     p.mp = nt * PBN;
     p.nbp = nb;
-    const int64_t total = p.mp * nb;
-    const int64_t grid = (total + 255) / 256;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(q4p_prep_kernel, dim3((unsigned)grid), dim3(256), 0, s, w, p, n, nb, total);
-    return hipGetLastError();
+    return launch_q4p_prep(w, p, n, nb, s);
 }
 
 hipError_t launch_q8_0_packed_gemm(const uint8_t *wp, const uint8_t *xq, float *y, int64_t m, int64_t n, int64_t k,

@@ -668,7 +668,7 @@ static hipError_t launch_small_m(const uint8_t *w, const uint8_t *xq, float *y, 
     const bool groups = EP::kLinear && q4_row_groups(m, n, k);
     if (m < 1 || (m > kMaxMMfma && !groups) || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
-    if ((n + 15) / 16 > 0x7fffffff)
+    if (!grid_fits((n + 15) / 16, 64)) // (so many columns are not split over waves)
         return hipErrorInvalidConfiguration;
     const int mp = sm_rows(m);
     const SmArgs<EP> a{w, xq, y, m, n, (int)(k / 32), ep, s};
@@ -730,7 +730,7 @@ hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const
 {
     if (!q4_gated_small(m, n, k) || k < kMinKMfma || k >= kMaxKMfma)
         return hipErrorInvalidValue;
-    if ((n + 15) / 16 > 0x7fffffff)
+    if (!grid_fits((n + 15) / 16, 64)) // (so many columns are not split over waves)
         return hipErrorInvalidConfiguration;
     const SmArgs<GatedEpilogue> a{wg, xq, y, m, n, (int)(k / 32), GatedEpilogue{wu, act, false}, s};
     // Groups of 16 rows where all their workgroups have a CU of their own (m = 32,

@@ -59,18 +59,18 @@ __global__ __launch_bounds__(256) void pack_ternary_kernel(const uint8_t *__rest
 hipError_t launch_pack_q4_0(const uint8_t *codes, const uint16_t *d_bits, uint8_t *w, int64_t n, int64_t k,
                             hipStream_t s)
 {
-    int64_t nblocks = n * (k / 32);
-    int64_t grid = (nblocks + 255) / 256;
-    hipLaunchKernelGGL(pack_q4_0_kernel, dim3((unsigned)grid), dim3(256), 0, s, codes, d_bits, w, nblocks);
-    return hipGetLastError();
+    return launch_parts(n * (k / 32), kPartThreads, [&](int64_t b0, int64_t nblocks) {
+        hipLaunchKernelGGL(pack_q4_0_kernel, dim3((unsigned)((nblocks + 255) / 256)), dim3(256), 0, s, codes + b0 * 32,
+                           d_bits + b0, w + b0 * 18, nblocks);
+    });
 }
 
 hipError_t launch_pack_ternary(const uint8_t *codes, uint32_t *w, int64_t n, int64_t k, hipStream_t s)
 {
-    int64_t nwords = n * (k / 16);
-    int64_t grid = (nwords + 255) / 256;
-    hipLaunchKernelGGL(pack_ternary_kernel, dim3((unsigned)grid), dim3(256), 0, s, codes, w, nwords);
-    return hipGetLastError();
+    return launch_parts(n * (k / 16), kPartThreads, [&](int64_t w0, int64_t nwords) {
+        hipLaunchKernelGGL(pack_ternary_kernel, dim3((unsigned)((nwords + 255) / 256)), dim3(256), 0, s,
+                           codes + w0 * 16, w + w0, nwords);
+    });
 }
 
 // ------------------------------------------------------------------ Q8_0
@@ -121,9 +121,10 @@ hipError_t launch_quantize_q8_0(const float *x, uint8_t *xq, int64_t nblocks, hi
         hipLaunchKernelGGL(quantize_q8_0_kernel<64>, dim3((unsigned)((nblocks + 7) / 8)), dim3(64), 0, s, x, xq, nblocks);
         return hipGetLastError();
     }
-    int64_t grid = (nblocks + 31) / 32;
-    hipLaunchKernelGGL(quantize_q8_0_kernel<256>, dim3((unsigned)grid), dim3(256), 0, s, x, xq, nblocks);
-    return hipGetLastError();
+    return launch_parts(nblocks, kPartThreads / 8, [&](int64_t b0, int64_t part) {
+        hipLaunchKernelGGL(quantize_q8_0_kernel<256>, dim3((unsigned)((part + 31) / 32)), dim3(256), 0, s, x + b0 * 32,
+                           xq + b0 * 34, part);
+    });
 }
 
 // ------------------------------------------------------------------ int8 rows
@@ -231,13 +232,14 @@ __global__ __launch_bounds__(256) void quantize_i8_rows_kernel(const float *__re
 hipError_t launch_quantize_i8_rows(const float *x, int8_t *xq, float *act_scale, int32_t *act_sum, int64_t m,
                                    int64_t k, hipStream_t s)
 {
-    if (k % 4 == 0)
-        hipLaunchKernelGGL(quantize_i8_rows_kernel<4>, dim3((unsigned)m), dim3(256), 0, s, x, xq, act_scale,
-                           act_sum, k);
-    else
-        hipLaunchKernelGGL(quantize_i8_rows_kernel<1>, dim3((unsigned)m), dim3(256), 0, s, x, xq, act_scale,
-                           act_sum, k);
-    return hipGetLastError();
+    return launch_parts(m, kPartThreads / 256, [&](int64_t r0, int64_t rows) {
+        if (k % 4 == 0)
+            hipLaunchKernelGGL(quantize_i8_rows_kernel<4>, dim3((unsigned)rows), dim3(256), 0, s, x + r0 * k,
+                               xq + r0 * k, act_scale + r0, act_sum + r0, k);
+        else
+            hipLaunchKernelGGL(quantize_i8_rows_kernel<1>, dim3((unsigned)rows), dim3(256), 0, s, x + r0 * k,
+                               xq + r0 * k, act_scale + r0, act_sum + r0, k);
+    });
 }
 
 } // namespace qll

@@ -267,12 +267,10 @@ static hipError_t launch_tg2(const uint32_t *w, float w_scale, const int8_t *xq,
                              const int32_t *act_sum, float *y, int64_t n, int nw, hipStream_t st)
 {
     constexpr int R = 64 / L, RPW = R * (kTg2Threads / 64);
-    const int64_t grid = (n + RPW - 1) / RPW;
-    if (grid > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ternary_gemv2_kernel<L, U>), dim3((unsigned)grid), dim3(kTg2Threads), (size_t)nw * 16, st, w,
-                       w_scale, xq, act_scale, act_sum, y, n, nw);
-    return hipGetLastError();
+    return launch_parts(n, kPartThreads / L, [&](int64_t r0, int64_t rows) {
+        hipLaunchKernelGGL((ternary_gemv2_kernel<L, U>), dim3((unsigned)((rows + RPW - 1) / RPW)), dim3(kTg2Threads),
+                           (size_t)nw * 16, st, w + r0 * nw, w_scale, xq, act_scale, act_sum, y + r0, rows, nw);
+    });
 }
 
 template <int VEC>
@@ -909,6 +907,8 @@ hipError_t launch_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *x
         return hipGetLastError();
     }
     dim3 grid((unsigned)((n + TBN - 1) / TBN), (unsigned)((m + TBM - 1) / TBM));
+    if (!grid_fits(grid.x, kTerGemmThreads))
+        return hipErrorInvalidConfiguration;
     if (nw % 4 == 0)
         hipLaunchKernelGGL(ternary_gemm_kernel<true>, grid, dim3(kTerGemmThreads), 0, st, w, w_scale, xq, act_scale,
                            act_sum, y, m, n, nw);
