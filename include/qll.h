@@ -362,7 +362,9 @@ int qll_ternary_gemm(const uint32_t *w, float w_scale, const int8_t *xq, const f
  * float[m][n] or NULL.  residual may be y itself (an accumulation in place);
  * otherwise y must not overlap an input.  Without bias, activation and
  * residual the result is that of qll_q4_0_q8_0_gemm bit for bit up to m = 16;
- * above, the order of the f32 sum can differ.
+ * above, the order of the f32 sum can differ, and from m = 17 on small and
+ * middle-sized matrices this entry is the faster one (m = 128, 1024 -> 1024: 4.3
+ * against 19.5 us), since the plain one keeps its bits.
  * QLL_ERR_VALUE for an unknown act. */
 int qll_q4_0_q8_0_linear(const void *w, const void *xq, const float *bias, int act, const float *residual, float *y,
                          int64_t m, int64_t n, int64_t k, void *ws, size_t ws_bytes, void *stream);

@@ -126,10 +126,13 @@ __device__ __forceinline__ float times_sigmoid(float x, float t)
 __device__ __forceinline__ float act_relu(float x) { return x < 0.0f ? 0.0f : x; } // NaN stays
 // x Phi(x) = x - h for x >= 0 and h for x < 0, h = x erfc(|x| / sqrt(2)) / 2, with
 // erfc(|x| / sqrt(2)) = t 2^(G(t) - x^2 log2(e) / 2), t = 1 / (1 + 0.4 |x|).  G is a
-// polynomial fitted to that definition in f64 on |x| <= 14 (1e-7 relative; beyond,
-// h is below 1e-36), so the tail keeps its relative precision too.  About 20
-// instructions; with the library's erfcf a kernel of 128 x 128 tiles took 4 us longer
-// (14.2 against 10.2 us for one tile of five blocks).
+// polynomial fitted to that definition in f64 on |x| <= 14 (beyond, h is below
+// 1e-36); with its coefficients in f32 it gives erfc within 2.7e-7 relative, most at
+// |x| = 0.05, and within 1e-7 from 1 on.  In f32 the value is within 10 half steps
+// (2^-24 relative) from -2 on.  Below, the exponent's rounding counts, up to 0.85 x^2
+// of them: 21 down to -5, 83 (5e-6) down to -10.  About 20 instructions; with the
+// library's erfcf a kernel of 128 x 128 tiles took 4 us longer (14.2 against 10.2 us
+// for one tile of five blocks).
 __device__ __forceinline__ float act_gelu(float x)
 {
     const float xc = fminf(fmaxf(x, -14.0f), 14.0f), t = __builtin_amdgcn_rcpf(fmaf(0.4f, fabsf(xc), 1.0f));

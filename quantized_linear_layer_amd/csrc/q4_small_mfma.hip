@@ -733,10 +733,13 @@ hipError_t launch_q4_0_gated_small_m(const uint8_t *wg, const uint8_t *wu, const
     if (!grid_fits((n + 15) / 16, 64)) // (so many columns are not split over waves)
         return hipErrorInvalidConfiguration;
     const SmArgs<GatedEpilogue> a{wg, xq, y, m, n, (int)(k / 32), GatedEpilogue{wu, act, false}, s};
-    // Groups of 16 rows where all their workgroups have a CU of their own (m = 32,
-    // 2048 -> 2048: 6.6 -> 5.2 us; 4096 -> 2048 7.8 -> 8.9), and above 32 rows on
-    // large matrices, where groups of 32 leave CUs idle (m = 48, 4096 -> 4096: 18.6 ->
-    // 15.6 us; 2048 -> 2048 6.8 -> 8.1), or above 64 rows.
+    // Groups of 16 rows where all their workgroups have a CU of their own (m = 32 in
+    // us, groups of 32 -> of 16: 2048 -> 2 x 2048 7.5 -> 5.6, 4096 -> 2 x 2048 10.6 -> 7.9;
+    // 8192 -> 2 x 4096, over the limit, 17.6 -> 19.2), and above 32 rows on large
+    // matrices, where groups of 32 leave CUs idle (m = 48: 4096 -> 2 x 4096 16.7 -> 15.6,
+    // 2048 -> 2 x 8192 16.7 -> 15.3, 4096 -> 2 x 14336 59.9 -> 46.8; m = 64: 16.7 and 16.7, 16.9 ->
+    // 16.4, 60.8 -> 55.5, at worst 8192 -> 2 x 8192 50.4 -> 51.6; on small ones even: 2048 -> 2 x
+    // 2048 7.7 and 7.6), or above 64 rows.
     const bool few = (n + 15) / 16 * ((m + 15) / 16) <= 256;
     if (m > 16 && (few || m > 64 || (m > kMaxMMfma && n * k >= ((int64_t)1 << 23))))
         launch_sm_ks<2, 16>(small_m_groups_split<2, true>(m, n, a.nb), a);
