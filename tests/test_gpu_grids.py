@@ -99,12 +99,13 @@ def test_repacked_pair(qll_gpu):
     wp = torch.empty(need, dtype=torch.uint8, device=DEV)
     wp[-256 * nb:] = 0xA5
     qll.qll_q4_0_repack_gated(w, w, wp, n, k)
-    codes, scales = wp[:tiles * nb * 3072].view(tiles, -1), wp[tiles * nb * 3072:].view(tiles, -1)
+    chunk = nb * 128 * 24  # a tile's codes: 128 rows of 32 six-bit ones a block
+    codes, scales = wp[:tiles * chunk].view(tiles, -1), wp[tiles * chunk:].view(tiles, -1)
     one = torch.empty(qll.qll_q4_0_repacked_gated_bytes(64, k), dtype=torch.uint8, device=DEV)
     for t in some:
         part = w[t * 64 * nb * 18:(t + 1) * 64 * nb * 18].clone()
         qll.qll_q4_0_repack_gated(part, part, one, 64, k)
-        assert torch.equal(codes[t], one[:nb * 3072]) and torch.equal(scales[t], one[nb * 3072:]), t
+        assert torch.equal(codes[t], one[:chunk]) and torch.equal(scales[t], one[chunk:]), t
     assert int(scales[1].max()) == 0 and int(scales[tiles - 3].max()) == 0
 
 
