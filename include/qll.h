@@ -83,7 +83,10 @@ enum {
     QLL_OP_Q4_0_LINEAR = 11,         /* qll_q4_0_q8_0_linear (the repacked form: QLL_OP_Q4_0_REPACKED_GEMM) */
     QLL_OP_Q4_0_GATED = 12,          /* qll_q4_0_q8_0_gated */
     QLL_OP_Q4_0_REPACKED_GATED = 13, /* qll_q4_0_repacked_q8_0_gated */
-    QLL_OP_TOKEN_LOGPROBS = 14       /* qll_token_logprobs: n is its v, k its top */
+    QLL_OP_TOKEN_LOGPROBS = 14,      /* qll_token_logprobs: n is its v, k its top */
+    QLL_OP_Q4G_LINEAR = 15,          /* qll_q4g_linear */
+    QLL_OP_MOE_ROUTE = 16,           /* qll_moe_route: n is its e, k its top */
+    QLL_OP_Q4G_MOE = 17              /* qll_q4g_moe: k is its top; qll_q4g_moe_layer: this and QLL_OP_MOE_ROUTE's, added */
 };
 
 /* Bytes of device workspace `op` needs at this shape (0 if none); SIZE_MAX if
@@ -461,6 +464,87 @@ int qll_rmsnorm_i8_rows(const void *x, int dtype, const void *residual, const fl
 int qll_token_logprobs(const void *logits, int dtype, const int32_t *tokens, int64_t t, float *logprob,
                        float *entropy, int64_t top, int32_t *top_ids, float *top_logprob, int64_t m, int64_t v,
                        void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------- 4-bit weights with group scales */
+
+/* Weights w[j][t] = s[j][t / g] * (c[j][t] - z[j][t / g]): 4-bit codes c with
+ * one 16-bit scale s and, where wanted, one 4-bit zero point z for every g = `group`
+ * weights of a row, g 32, 64 or 128 (without zero points z = 8; groups of 32 with f16
+ * scales are then Q4_0's values).  Other than in the Q4_0 entries the activations are not
+ * quantized: they are f32, bf16 or f16 and every one of their bits counts.
+ *
+ * fmt is a sum of these bits: scales are bf16 (else f16), zero points are present. */
+enum { QLL_Q4G_BF16 = 1, QLL_Q4G_ZEROS = 2 };
+
+/* Bytes of the packed form of weights W[n][k] (a multiple of 256; SIZE_MAX if the
+ * shape, group or fmt is invalid): for tiles of 16 rows and 128 weights, both padded, 1024
+ * bytes a tile, then 1024 / group bytes of scales and 256 / group of zero points for each
+ * row and 512 weights. */
+size_t qll_q4g_packed_bytes(int64_t n, int64_t k, int64_t group, int fmt);
+
+/* Load-time packing.  codes: uint8[n][k] (0..15; the low bits are used), scales:
+ * uint16[n][k / group] (bits of f16 or bf16, finite), zeros: uint8[n][k / group] (0..15),
+ * used only with QLL_Q4G_ZEROS.  wp: qll_q4g_packed_bytes(n, k, group, fmt) bytes, written in
+ * full.  k % group == 0.  QLL_ERR_VALUE for another group or fmt. */
+int qll_q4g_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int64_t group, int fmt, void *wp,
+                 int64_t n, int64_t k, void *stream);
+
+/* The packed form (group 32, fmt 0) of Q4_0 weights w: block_q4_0[n][k/32]; lossless. */
+int qll_q4g_from_q4_0(const void *w, void *wp, int64_t n, int64_t k, void *stream);
+
+/* Y[m][n] = T(act(X.W^T + bias) + residual).  wp: packed weights; x: [m][k] of type dtype
+ * (QLL_DTYPE_*); bias: float[n] or NULL; act a QLL_ACT_* value; residual: [m][n] of
+ * type y_dtype or NULL, may be y itself; y: [m][n] of type T = y_dtype, rounded once, to
+ * nearest even.  Sums are f32: without an epilogue, before that rounding, within
+ * 1e-4 * sum_t |x s| (|c - z| + 16) of the exact sum.  |x| < 2^120.  A row of x with
+ * NaN or an infinity in it has unspecified outputs, other rows do not change.  k % group == 0,
+ * k < 2^24 (else QLL_ERR_SHAPE).  ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_LINEAR,
+ * m, n, k) bytes (0 so far: ws may be NULL).  QLL_ERR_VALUE for another group, fmt, dtype or act. */
+int qll_q4g_linear(const void *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias, int act,
+                   const void *residual, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------- mixture of experts, few tokens */
+
+enum { QLL_SCORE_SOFTMAX = 0, QLL_SCORE_SIGMOID = 1 };
+
+/* The experts of each token.  Logits l = X.Wr^T, summed in f64; scores p = softmax(l) over the
+ * e experts, or the sigmoid of each l.  ids[m][top]: the `top` experts with the largest
+ * p + bias[expert] (the largest l where bias is NULL), largest first, the lower index first among
+ * equal ones.  weights[m][top]: their p, divided by its sum over them where renorm is not 0,
+ * times scale.  Scores are f64, so the choice does not depend on the order of a sum; f32 only on
+ * return.  x: [m][k] of type dtype, wr: [e][k] of type wr_dtype, bias: float[e] or
+ * NULL, scale finite.  1 <= e <= 1024, 1 <= top <= min(32, e), any k >= 1 below 2^24 (else
+ * QLL_ERR_SHAPE); QLL_ERR_VALUE for an unknown dtype or score.  In a row with NaN or an infinity
+ * among its logits the ids are unspecified, different and below e, and the weights unspecified.  ws/ws_bytes: at least
+ * qll_workspace_bytes(QLL_OP_MOE_ROUTE, m, e, top) bytes; contents on return unspecified. */
+int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const float *bias, int score, int renorm,
+                  float scale, int32_t *ids, float *weights, int64_t top, int64_t m, int64_t e, int64_t k, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* The experts of a feed-forward block on the tokens that chose them, two kernels:
+ *     Y[i] = T(sum_j weights[i][j] * Wd_e.(act(Wg_e.x_i) * (Wu_e.x_i)) + residual[i]),  e = ids[i][j].
+ * wg, wu: e packed matrices [n][k], one every qll_q4g_packed_bytes(n, k, group, fmt) bytes; wd: e
+ * packed matrices [k][n] likewise; x, residual (or NULL; may be y), y: [m][k] of type T = dtype;
+ * ids: int32[m][top], weights: float[m][top].  An id outside [0, e) (padding) adds nothing, and
+ * its weight is not read; a row of such ids gets its residual, or 0.  An expert that a token names
+ * twice counts with the sum of its weights.  The gated products are f32 between the two
+ * kernels.  Made for few tokens: up to 64 read each chosen expert's weights once, more go in
+ * groups of 64.  n % group == 0, k % group == 0, both below 2^24; e and top as in
+ * qll_moe_route.  NaN and infinities in x, and its size: as in qll_q4g_linear.  The result does
+ * not depend on what other tokens are in the call beyond the order of f32 sums.
+ * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_MOE, m, n, top) bytes; contents on
+ * return unspecified. */
+int qll_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top, const void *wg,
+                const void *wu, const void *wd, int64_t group, int fmt, int act, const void *residual, void *y,
+                int64_t m, int64_t n, int64_t k, int64_t e, void *ws, size_t ws_bytes, void *stream);
+
+/* The whole layer: qll_moe_route into ids and weights, then qll_q4g_moe on them.  ws/ws_bytes: at
+ * least the sum of both workspaces. */
+int qll_q4g_moe_layer(const void *x, int dtype, const void *wr, int wr_dtype, const float *bias, int score, int renorm,
+                      float scale, int32_t *ids, float *weights, int64_t top, const void *wg, const void *wu,
+                      const void *wd, int64_t group, int fmt, int act, const void *residual, void *y, int64_t m,
+                      int64_t n, int64_t k, int64_t e, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

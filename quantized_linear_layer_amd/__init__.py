@@ -30,8 +30,13 @@ QLL_OP_Q4_0_LINEAR = 11
 QLL_OP_Q4_0_GATED = 12
 QLL_OP_Q4_0_REPACKED_GATED = 13
 QLL_OP_TOKEN_LOGPROBS = 14
+QLL_OP_Q4G_LINEAR = 15
+QLL_OP_MOE_ROUTE = 16
+QLL_OP_Q4G_MOE = 17
 QLL_ACT_NONE, QLL_ACT_RELU, QLL_ACT_GELU, QLL_ACT_GELU_TANH, QLL_ACT_SILU = 0, 1, 2, 3, 4
 QLL_DTYPE_F32, QLL_DTYPE_BF16, QLL_DTYPE_F16 = 0, 1, 2
+QLL_Q4G_BF16, QLL_Q4G_ZEROS = 1, 2
+QLL_SCORE_SOFTMAX, QLL_SCORE_SIGMOID = 0, 1
 
 Q4_0_BLOCK_BYTES = 18
 Q8_0_BLOCK_BYTES = 34
@@ -54,6 +59,7 @@ def load(path=LIB_PATH):
         raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
     L = ctypes.CDLL(path)
     P, I, S, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    C = ctypes.c_int
     sig = {
         "qll_pack_q4_0": [P, P, P, I, I, P],
         "qll_pack_ternary": [P, P, I, I, P],
@@ -80,6 +86,12 @@ def load(path=LIB_PATH):
         "qll_q4_0_repack_gated": [P, P, P, I, I, P],
         "qll_q4_0_repacked_q8_0_gated": [P, P, ctypes.c_int, P, I, I, I, P, S, P],
         "qll_token_logprobs": [P, ctypes.c_int, P, I, P, P, I, P, P, I, I, P, S, P],
+        "qll_q4g_pack": [P, P, P, I, C, P, I, I, P],
+        "qll_q4g_from_q4_0": [P, P, I, I, P],
+        "qll_q4g_linear": [P, I, C, P, C, P, C, P, P, C, I, I, I, P, S, P],
+        "qll_moe_route": [P, C, P, C, P, C, C, F, P, P, I, I, I, I, P, S, P],
+        "qll_q4g_moe": [P, C, P, P, I, P, P, P, I, C, C, P, P, I, I, I, I, P, S, P],
+        "qll_q4g_moe_layer": [P, C, P, C, P, C, C, F, P, P, I, P, P, P, I, C, C, P, P, I, I, I, I, P, S, P],
         "qll_rmsnorm_q8_0": [P, ctypes.c_int, P, P, F, P, P, I, I, P],
         "qll_rmsnorm_i8_rows": [P, ctypes.c_int, P, P, F, P, P, P, P, I, I, P],
     }
@@ -97,6 +109,8 @@ def load(path=LIB_PATH):
     L.qll_q4_0_decode_packed_bytes.restype = ctypes.c_size_t
     L.qll_q8_0_repacked_bytes.argtypes = [I, I]
     L.qll_q8_0_repacked_bytes.restype = ctypes.c_size_t
+    L.qll_q4g_packed_bytes.argtypes = [I, I, I, C]
+    L.qll_q4g_packed_bytes.restype = ctypes.c_size_t
     L.qll_status_string.argtypes = [ctypes.c_int]
     L.qll_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -475,3 +489,91 @@ def qll_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids,
           _arg(tokens, m * t * 4, "tokens", d, _I32), t, _arg(logprob, m * t * 4, "logprob", d, _F32),
           _arg(entropy, m * 4, "entropy", d, _F32), top, _arg(top_ids, m * top * 4, "top_ids", d, _I32),
           _arg(top_logprob, m * top * 4, "top_logprob", d, _F32), m, v, wsp, wsb, _on(d, stream))
+
+
+# ----------------------------------------------------------------- 4-bit weights with group scales
+
+def qll_q4g_packed_bytes(n, k, group, fmt):
+    return int(load().qll_q4g_packed_bytes(int(n), int(k), int(group), int(fmt)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _q4g_need(n, k, group, fmt):
+    need = qll_q4g_packed_bytes(n, k, group, fmt)
+    return need if need != 2 ** 64 - 1 else 0
+
+
+def qll_q4g_pack(codes, scales, zeros, group, fmt, wp, n, k, stream=None):
+    """Load-time packing of 4-bit codes with their group scales and, with
+    QLL_Q4G_ZEROS in fmt, zero points (else unused)."""
+    d = _device(wp, "wp")
+    groups = n * (k // group) if group else 0
+    zeros = zeros if fmt & QLL_Q4G_ZEROS else None
+    _call("qll_q4g_pack", _arg(codes, n * k, "codes", d),
+          _arg(scales, groups * 2, "scales", d, QLL_DTYPE_BF16 if fmt & QLL_Q4G_BF16 else QLL_DTYPE_F16),
+          _arg(zeros, groups, "zeros", d), group, fmt, _arg(wp, _q4g_need(n, k, group, fmt), "wp", d), n, k,
+          _on(d, stream))
+
+
+def qll_q4g_from_q4_0(w, wp, n, k, stream=None):
+    """The packed form (group 32, fmt 0) of Q4_0 blocks."""
+    d = _device(wp, "wp")
+    _call("qll_q4g_from_q4_0", _arg(w, n * (k // 32) * Q4_0_BLOCK_BYTES, "w", d),
+          _arg(wp, _q4g_need(n, k, 32, 0), "wp", d), n, k, _on(d, stream))
+
+
+def qll_q4g_linear(wp, group, fmt, x, dtype, bias, act, residual, y, y_dtype, m, n, k, ws=None, stream=None):
+    """y = act(x.W^T + bias) + residual; bias and residual may be None, residual
+    may be y."""
+    d = _device(y, "y")
+    wsp, wsb = _scratch(ws, d)
+    nb = m * n * _esize(y_dtype)
+    _call("qll_q4g_linear", _arg(wp, _q4g_need(n, k, group, fmt), "wp", d), group, fmt,
+          _arg(x, m * k * _esize(dtype), "x", d, dtype), dtype, _arg(bias, n * 4, "bias", d, _F32), act,
+          _arg(residual, nb, "residual", d, y_dtype), _arg(y, nb, "y", d, y_dtype), y_dtype, m, n, k, wsp, wsb,
+          _on(d, stream))
+
+
+# ----------------------------------------------------------------- mixture of experts, few tokens
+
+def _route_args(x, dtype, wr, wr_dtype, bias, score, renorm, scale, ids, weights, top, m, e, k, d):
+    return (_arg(x, m * k * _esize(dtype), "x", d, dtype), dtype, _arg(wr, e * k * _esize(wr_dtype), "wr", d, wr_dtype),
+            wr_dtype, _arg(bias, e * 4, "bias", d, _F32), score, int(renorm), scale,
+            _arg(ids, m * top * 4, "ids", d, _I32), _arg(weights, m * top * 4, "weights", d, _F32), top)
+
+
+def _expert_args(wg, wu, wd, group, fmt, act, residual, y, dtype, m, n, k, e, d):
+    gu, nb = e * _q4g_need(n, k, group, fmt), m * k * _esize(dtype)
+    return (_arg(wg, gu, "wg", d), _arg(wu, gu, "wu", d), _arg(wd, e * _q4g_need(k, n, group, fmt), "wd", d), group,
+            fmt, act, _arg(residual, nb, "residual", d, dtype), _arg(y, nb, "y", d, dtype), m, n, k, e)
+
+
+def qll_moe_route(x, dtype, wr, wr_dtype, bias, score, renorm, scale, ids, weights, top, m, e, k, ws=None,
+                  stream=None):
+    """ids (int32) and weights of the `top` experts of each row of x; bias may be
+    None."""
+    d = _device(x, "x")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_moe_route", *_route_args(x, dtype, wr, wr_dtype, bias, score, renorm, scale, ids, weights, top, m, e, k,
+                                        d), m, e, k, wsp, wsb, _on(d, stream))
+
+
+def qll_q4g_moe(x, dtype, ids, weights, top, wg, wu, wd, group, fmt, act, residual, y, m, n, k, e, ws=None,
+                stream=None):
+    """The experts that ids (int32) name, weighted and added up; residual may be
+    None or y."""
+    d = _device(x, "x")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_q4g_moe", _arg(x, m * k * _esize(dtype), "x", d, dtype), dtype, _arg(ids, m * top * 4, "ids", d, _I32),
+          _arg(weights, m * top * 4, "weights", d, _F32), top,
+          *_expert_args(wg, wu, wd, group, fmt, act, residual, y, dtype, m, n, k, e, d), wsp, wsb, _on(d, stream))
+
+
+def qll_q4g_moe_layer(x, dtype, wr, wr_dtype, bias, score, renorm, scale, ids, weights, top, wg, wu, wd, group, fmt,
+                      act, residual, y, m, n, k, e, ws=None, stream=None):
+    """qll_moe_route and qll_q4g_moe in one call."""
+    d = _device(x, "x")
+    wsp, wsb = _scratch(ws, d)
+    _call("qll_q4g_moe_layer", *_route_args(x, dtype, wr, wr_dtype, bias, score, renorm, scale, ids, weights, top, m, e,
+                                            k, d),
+          *_expert_args(wg, wu, wd, group, fmt, act, residual, y, dtype, m, n, k, e, d), wsp, wsb, _on(d, stream))

@@ -28,7 +28,7 @@ FLAGS = ["-std=c++17", "-O3", f"--offload-arch={ARCH}", "-fPIC", "-Wall", "-Wno-
 # fmas that apply the scales read them without a v_accvgpr_read each.
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA = {"q4_gemm.hip": _VGPR_FORM, "q4_packed.hip": _VGPR_FORM, "q4_small_mfma.hip": _VGPR_FORM,
-         "ternary.hip": _VGPR_FORM}
+         "ternary.hip": _VGPR_FORM, "q4g.hip": _VGPR_FORM, "moe.hip": _VGPR_FORM}
 
 
 def _compile(src):

@@ -97,6 +97,20 @@ bool logprob_dims_ok(int64_t m, int64_t v, int64_t top)
     return dims_ok(m, v) && v <= kMaxLpVocab && top >= 0 && top <= kMaxLpTop && top <= v;
 }
 
+static_assert((int)QLL_Q4G_BF16 == 1 && (int)QLL_Q4G_ZEROS == 2, "the bits q4g.h tests");
+
+bool dtype_ok(int dtype) { return dtype >= QLL_DTYPE_F32 && dtype <= QLL_DTYPE_F16; }
+
+bool q4g_format_ok(int64_t group, int fmt)
+{
+    return (group == 32 || group == 64 || group == 128) && fmt >= 0 && fmt <= (QLL_Q4G_BF16 | QLL_Q4G_ZEROS);
+}
+
+bool route_dims_ok(int64_t m, int64_t e, int64_t top)
+{
+    return dims_ok(m, e) && e <= kMaxExperts && top >= 1 && top <= kMaxTop && top <= e;
+}
+
 hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
 } // namespace
@@ -178,6 +192,18 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (!logprob_dims_ok(m, n, k))
             return SIZE_MAX;
         return token_logprobs_workspace(m, n, k);
+    case QLL_OP_Q4G_LINEAR:
+        if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
+            return SIZE_MAX;
+        return 0;
+    case QLL_OP_MOE_ROUTE:
+        if (!route_dims_ok(m, n, k))
+            return SIZE_MAX;
+        return moe_route_workspace(m, n);
+    case QLL_OP_Q4G_MOE:
+        if (!dims_ok(m, n) || n % 32 != 0 || n >= kMaxGemmK || k < 1 || k > kMaxTop)
+            return SIZE_MAX;
+        return q4g_moe_workspace(m, n, k);
     default:
         return SIZE_MAX;
     }
@@ -722,6 +748,149 @@ int qll_token_logprobs(const void *logits, int dtype, const int32_t *tokens, int
         return rc;
     return launched(launch_token_logprobs(logits, dtype, tokens, t, logprob, entropy, top, top_ids, top_logprob, m, v,
                                           ws, as_stream(stream)));
+}
+
+size_t qll_q4g_packed_bytes(int64_t n, int64_t k, int64_t group, int fmt)
+{
+    if (!q4g_format_ok(group, fmt) || !dims_ok(n, k) || k % group != 0)
+        return SIZE_MAX;
+    return q4g_packed_bytes(n, k, group, fmt);
+}
+
+int qll_q4g_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int64_t group, int fmt, void *wp,
+                 int64_t n, int64_t k, void *stream)
+{
+    if (!q4g_format_ok(group, fmt))
+        return QLL_ERR_VALUE;
+    if (!codes || !scales || !wp || ((fmt & QLL_Q4G_ZEROS) && !zeros))
+        return QLL_ERR_NULL;
+    if (!dims_ok(n, k) || k % group != 0)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(codes) || !aligned16(scales) || ((fmt & QLL_Q4G_ZEROS) && !aligned16(zeros)) || !aligned16(wp))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4g_pack(codes, scales, zeros, group, fmt, static_cast<uint8_t *>(wp), n, k,
+                                    as_stream(stream)));
+}
+
+int qll_q4g_from_q4_0(const void *w, void *wp, int64_t n, int64_t k, void *stream)
+{
+    if (!w || !wp)
+        return QLL_ERR_NULL;
+    if (!dims_ok(n, k) || k % 32 != 0)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(w) || !aligned16(wp))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4g_from_q4_0(static_cast<const uint8_t *>(w), static_cast<uint8_t *>(wp), n, k,
+                                         as_stream(stream)));
+}
+
+int qll_q4g_linear(const void *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias, int act,
+                   const void *residual, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
+                   size_t ws_bytes, void *stream)
+{
+    (void)ws_bytes;
+    if (!wp || !x || !y)
+        return QLL_ERR_NULL;
+    if (!q4g_format_ok(group, fmt) || !dtype_ok(dtype) || !dtype_ok(y_dtype) || !act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % group != 0 || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(wp) || !aligned16(x) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) || !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4g_linear(static_cast<const uint8_t *>(wp), group, fmt, x, dtype, bias, act, residual, y,
+                                      y_dtype, m, n, k, as_stream(stream)));
+}
+
+// What the router's arguments have to be; QLL_OK or the status to return.
+static int route_args(const void *x, int dtype, const void *wr, int wr_dtype, const float *bias, int score, float scale,
+                      const int32_t *ids, const float *weights, int64_t top, int64_t m, int64_t e, int64_t k,
+                      const void *ws)
+{
+    if (!x || !wr || !ids || !weights || !ws)
+        return QLL_ERR_NULL;
+    if (!dtype_ok(dtype) || !dtype_ok(wr_dtype) || (score != QLL_SCORE_SOFTMAX && score != QLL_SCORE_SIGMOID) ||
+        !__builtin_isfinite(scale))
+        return QLL_ERR_VALUE;
+    if (!route_dims_ok(m, e, top) || !dims_ok(m, k) || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(wr) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights) || !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    return QLL_OK;
+}
+
+// The same of the experts' arguments.
+static int moe_args(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top, const void *wg,
+                    const void *wu, const void *wd, int64_t group, int fmt, int act, const void *residual,
+                    const void *y, int64_t m, int64_t n, int64_t k, int64_t e, const void *ws)
+{
+    if (!x || !ids || !weights || !wg || !wu || !wd || !y || !ws)
+        return QLL_ERR_NULL;
+    if (!q4g_format_ok(group, fmt) || !dtype_ok(dtype) || !act_ok(act))
+        return QLL_ERR_VALUE;
+    if (!route_dims_ok(m, e, top) || !dims_ok(m, k) || !dims_ok(m, n) || !dims_ok(n, k) || n % group != 0 ||
+        k % group != 0 || n >= kMaxGemmK || k >= kMaxGemmK)
+        return QLL_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(ids) || !aligned16(weights) || !aligned16(wg) || !aligned16(wu) ||
+        !aligned16(wd) || !aligned16(residual) || !aligned16(y) || !aligned16(ws))
+        return QLL_ERR_ALIGN;
+    return QLL_OK;
+}
+
+int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const float *bias, int score, int renorm,
+                  float scale, int32_t *ids, float *weights, int64_t top, int64_t m, int64_t e, int64_t k, void *ws,
+                  size_t ws_bytes, void *stream)
+{
+    if (int rc = route_args(x, dtype, wr, wr_dtype, bias, score, scale, ids, weights, top, m, e, k, ws))
+        return rc;
+    if (ws_bytes < moe_route_workspace(m, e))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_moe_route(x, dtype, wr, wr_dtype, bias, score == QLL_SCORE_SIGMOID, renorm != 0, scale, ids,
+                                     weights, top, m, e, k, ws, as_stream(stream)));
+}
+
+int qll_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top, const void *wg,
+                const void *wu, const void *wd, int64_t group, int fmt, int act, const void *residual, void *y,
+                int64_t m, int64_t n, int64_t k, int64_t e, void *ws, size_t ws_bytes, void *stream)
+{
+    if (int rc = moe_args(x, dtype, ids, weights, top, wg, wu, wd, group, fmt, act, residual, y, m, n, k, e, ws))
+        return rc;
+    if (ws_bytes < q4g_moe_workspace(m, n, top))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    return launched(launch_q4g_moe(x, dtype, ids, weights, top, static_cast<const uint8_t *>(wg),
+                                   static_cast<const uint8_t *>(wu), static_cast<const uint8_t *>(wd), group, fmt, act,
+                                   residual, y, m, n, k, e, ws, as_stream(stream)));
+}
+
+int qll_q4g_moe_layer(const void *x, int dtype, const void *wr, int wr_dtype, const float *bias, int score, int renorm,
+                      float scale, int32_t *ids, float *weights, int64_t top, const void *wg, const void *wu,
+                      const void *wd, int64_t group, int fmt, int act, const void *residual, void *y, int64_t m,
+                      int64_t n, int64_t k, int64_t e, void *ws, size_t ws_bytes, void *stream)
+{
+    if (int rc = route_args(x, dtype, wr, wr_dtype, bias, score, scale, ids, weights, top, m, e, k, ws))
+        return rc;
+    if (int rc = moe_args(x, dtype, ids, weights, top, wg, wu, wd, group, fmt, act, residual, y, m, n, k, e, ws))
+        return rc;
+    const size_t first = moe_route_workspace(m, e);
+    if (ws_bytes < first + q4g_moe_workspace(m, n, top))
+        return QLL_ERR_WORKSPACE;
+    if (int rc = check_device())
+        return rc;
+    if (int rc = launched(launch_moe_route(x, dtype, wr, wr_dtype, bias, score == QLL_SCORE_SIGMOID, renorm != 0,
+                                           scale, ids, weights, top, m, e, k, ws, as_stream(stream))))
+        return rc;
+    return launched(launch_q4g_moe(x, dtype, ids, weights, top, static_cast<const uint8_t *>(wg),
+                                   static_cast<const uint8_t *>(wu), static_cast<const uint8_t *>(wd), group, fmt, act,
+                                   residual, y, m, n, k, e, static_cast<uint8_t *>(ws) + first, as_stream(stream)));
 }
 
 } // extern "C"

@@ -413,6 +413,27 @@ hipError_t launch_token_logprobs(const void *logits, int dtype, const int32_t *t
                                  float *entropy, int64_t top, int32_t *top_ids, float *top_logprob, int64_t m,
                                  int64_t v, void *ws, hipStream_t s);
 
+// 4-bit weights with group scales (q4g.h has the packed form; fmt: the ABI's
+// QLL_Q4G_* bits; dtypes: QLL_W_* values): packing, the linear layer, and the
+// experts of a mixture-of-experts layer with the router that chooses them.
+size_t q4g_packed_bytes(int64_t n, int64_t k, int64_t group, int fmt);
+hipError_t launch_q4g_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int64_t group, int fmt,
+                           uint8_t *wp, int64_t n, int64_t k, hipStream_t s);
+hipError_t launch_q4g_from_q4_0(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s);
+hipError_t launch_q4g_linear(const uint8_t *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias,
+                             int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k,
+                             hipStream_t s);
+constexpr int64_t kMaxExperts = 1024, kMaxTop = 32;
+size_t moe_route_workspace(int64_t m, int64_t e);
+hipError_t launch_moe_route(const void *x, int dtype, const void *w, int w_dtype, const float *bias, int sigmoid,
+                            int renorm, float scale, int32_t *ids, float *weights, int64_t top, int64_t m, int64_t e,
+                            int64_t k, void *ws, hipStream_t s);
+size_t q4g_moe_workspace(int64_t m, int64_t n, int64_t top);
+hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top,
+                          const uint8_t *wg, const uint8_t *wu, const uint8_t *wd, int64_t group, int fmt, int act,
+                          const void *res, void *y, int64_t m, int64_t n, int64_t k, int64_t e, void *ws,
+                          hipStream_t s);
+
 // Largest k the LDS-staged decode kernels accept (the activation of one row
 // is kept whole in LDS).
 constexpr int64_t kMaxKQ4Gemv = 49152;
