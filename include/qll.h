@@ -528,9 +528,9 @@ int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const 
  * packed matrices [k][n] likewise; x, residual (or NULL; may be y), y: [m][k] of type T = dtype;
  * ids: int32[m][top], weights: float[m][top].  An id outside [0, e) (padding) adds nothing, and
  * its weight is not read; a row of such ids gets its residual, or 0.  An expert that a token names
- * twice counts with the sum of its weights.  The gated products are f32 between the two
- * kernels.  Made for few tokens: up to 64 read each chosen expert's weights once, more go in
- * groups of 64.  n % group == 0, k % group == 0, both below 2^24; e and top as in
+ * twice counts with the sum of its weights.  The gated products keep 16 bits of
+ * precision between the two kernels, 24 where x is f32.  Made for few tokens: up to 64 read each chosen expert's weights once, more go in
+ * groups of 64.  n % group == 0, k % group == 0, n < 2^20, k < 2^24; e and top as in
  * qll_moe_route.  NaN and infinities in x, and its size: as in qll_q4g_linear.  The result does
  * not depend on what other tokens are in the call beyond the order of f32 sums.
  * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_MOE, m, n, top) bytes; contents on

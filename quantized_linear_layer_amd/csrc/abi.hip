@@ -201,7 +201,7 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
             return SIZE_MAX;
         return moe_route_workspace(m, n);
     case QLL_OP_Q4G_MOE:
-        if (!dims_ok(m, n) || n % 32 != 0 || n >= kMaxGemmK || k < 1 || k > kMaxTop)
+        if (!dims_ok(m, n) || n % 32 != 0 || n >= kMaxMoeN || k < 1 || k > kMaxTop)
             return SIZE_MAX;
         return q4g_moe_workspace(m, n, k);
     default:
@@ -834,7 +834,7 @@ static int moe_args(const void *x, int dtype, const int32_t *ids, const float *w
     if (!q4g_format_ok(group, fmt) || !dtype_ok(dtype) || !act_ok(act))
         return QLL_ERR_VALUE;
     if (!route_dims_ok(m, e, top) || !dims_ok(m, k) || !dims_ok(m, n) || !dims_ok(n, k) || n % group != 0 ||
-        k % group != 0 || n >= kMaxGemmK || k >= kMaxGemmK)
+        k % group != 0 || n >= kMaxMoeN || k >= kMaxGemmK)
         return QLL_ERR_SHAPE;
     if (!aligned16(x) || !aligned16(ids) || !aligned16(weights) || !aligned16(wg) || !aligned16(wu) ||
         !aligned16(wd) || !aligned16(residual) || !aligned16(y) || !aligned16(ws))

@@ -424,6 +424,7 @@ hipError_t launch_q4g_linear(const uint8_t *wp, int64_t group, int fmt, const vo
                              int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k,
                              hipStream_t s);
 constexpr int64_t kMaxExperts = 1024, kMaxTop = 32;
+constexpr int64_t kMaxMoeN = (int64_t)1 << 20; // the experts' inner size: 32-bit offsets into the gated products
 size_t moe_route_workspace(int64_t m, int64_t e);
 hipError_t launch_moe_route(const void *x, int dtype, const void *w, int w_dtype, const float *bias, int sigmoid,
                             int renorm, float scale, int32_t *ids, float *weights, int64_t top, int64_t m, int64_t e,

@@ -128,86 +128,80 @@ struct Q4gLinear {
 // kw waves share RTN row tiles, each a part of k, and add up in LDS; rw such
 // sets a workgroup.  Workgroups eight apart land on the same XCD: those of one set of
 // rows follow each other there, so that its weights stay in that L2.
-template <int TX, int GRP, int RTN, int C, int I, int D>
+template <int TX, int GRP, int RTN, int C, int PK, int D>
 __global__ void __launch_bounds__(512) q4g_linear_kernel(Q4gLinear a)
 {
-    extern __shared__ f32x4 part[]; // [rw][kw][RTN * C][64]
+    using Wave = Q4gWave<TX, GRP, RTN, C, PK, D>;
+    constexpr int kTokens = 16 / PK; // of a column group
+    extern __shared__ float part[];  // [rw][kw][RTN * C * N][64]
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, kw = wave % a.kw, rw = wave / a.kw;
+    const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw, rw = wave / a.kw;
     const int64_t b = blockIdx.x, tg = b / 8 % a.tok_groups, rg = b / 8 / a.tok_groups * 8 + b % 8;
     const int64_t rt0 = (a.row0 + rg * a.rw + rw) * RTN;
-    const int64_t tok0 = a.tok0 + tg * 16 * C;
-    Q4gWave<TX, GRP, RTN, C, I, D> w;
+    const int64_t tok0 = a.tok0 + tg * kTokens * C;
+    Wave w;
     w.clear();
     if (rt0 < sh.rt) {
-        Q4gRows rows[RTN];
-        const uint8_t *x[C];
+        typename Wave::Rows rows;
 #pragma unroll
         for (int r = 0; r < RTN; r++) // past the last tile: the last one again, not stored
-            rows[r] = Q4gRows(a.wp, sh, rt0 + r < sh.rt ? rt0 + r : sh.rt - 1, GRP, a.fmt, lane);
+            rows.w[r] = Q4gRows(a.wp, sh, rt0 + r < sh.rt ? rt0 + r : sh.rt - 1, GRP, a.fmt);
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            const int row = lane % 16;
-            int64_t t = tok0 + 16 * c + row / 4 + 4 * (row & 3);
-            t = t < a.m ? t : a.m - 1; // rows past the last: its values again, not stored
-            x[c] = static_cast<const uint8_t *>(a.x) + (t * a.k + 8 * (lane / 16)) * (TX == Q4G_X_F32 ? 4 : 2);
+            int64_t t = kTokens * c + Wave::row_of(lane);
+            t = tok0 + t < a.m ? t : a.m - 1 - tok0; // rows past the last: its values again, not stored
+            rows.at[c] = (uint32_t)(t * a.k * q4g_x_size(TX)); // 32 rows of f32, 64 of 16 bits: below 2^32
         }
-        const int64_t per = (sh.kt + a.kw - 1) / a.kw, t0 = kw * per, t1 = t0 + per < sh.kt ? t0 + per : sh.kt;
-        w.run(rows, x, t0, t1, a.k);
+        rows.x = static_cast<const uint8_t *>(a.x) + tok0 * a.k * q4g_x_size(TX);
+        rows.part = 0, rows.last = (int)a.k - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
+        const int kt = (int)sh.kt, per = (kt + a.kw - 1) / a.kw, t0 = kw * per, t1 = t0 + per < kt ? t0 + per : kt;
+        w.run(rows, t0, t1);
     }
+    constexpr int kOuts = RTN * C * Wave::N;
     if (a.kw > 1) {
 #pragma unroll
-        for (int r = 0; r < RTN; r++)
-#pragma unroll
-            for (int c = 0; c < C; c++)
-                part[(wave * RTN * C + r * C + c) * 64 + lane] = w.y[r][c];
+        for (int o = 0; o < kOuts; o++)
+            part[(wave * kOuts + o) * 64 + lane] = w.y[o / (C * Wave::N)][o / Wave::N % C][o % Wave::N];
         __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < RTN; r++)
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            if ((r * C + c) % a.kw != kw) // the set's waves take turns
-                continue;
-            f32x4 v = w.y[r][c];
-            if (a.kw > 1) {
-                v = part[(rw * a.kw * RTN * C + r * C + c) * 64 + lane];
-                for (int o = 1; o < a.kw; o++)
-                    v += part[((rw * a.kw + o) * RTN * C + r * C + c) * 64 + lane];
-            }
-            const int64_t j = (rt0 + r) * 16 + lane % 16;
-            if (j >= a.n)
-                continue;
-            const float bias = a.bias ? a.bias[j] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < I; i++) {
-                const int64_t t = tok0 + 16 * c + lane / 16 + 4 * i;
-                if (t < a.m) {
-                    float o = activate(v[i] + bias, a.act);
-                    if (a.res)
-                        o += load_as(a.res, t * a.n + j, a.y_dtype);
-                    store_as(a.y, t * a.n + j, o, a.y_dtype);
-                }
-            }
+    for (int o = 0; o < kOuts; o++) {
+        if (o % a.kw != kw) // the set's waves take turns
+            continue;
+        const int r = o / (C * Wave::N), c = o / Wave::N % C, i = o % Wave::N;
+        float v = w.y[r][c][i];
+        if (a.kw > 1) {
+            v = part[(rw * a.kw * kOuts + o) * 64 + lane];
+            for (int p = 1; p < a.kw; p++)
+                v += part[((rw * a.kw + p) * kOuts + o) * 64 + lane];
         }
+        const int64_t j = (rt0 + r) * 16 + lane % 16, t = tok0 + kTokens * c + Wave::out_of(lane, i);
+        if (j >= a.n || t >= a.m)
+            continue;
+        v = activate(a.bias ? v + a.bias[j] : v, a.act);
+        if (a.res)
+            v += load_as(a.res, t * a.n + j, a.y_dtype);
+        store_as(a.y, t * a.n + j, v, a.y_dtype);
+    }
 }
 
-template <int TX, int GRP, int RTN, int C, int I, int D>
+template <int TX, int GRP, int RTN, int C, int PK, int D>
 hipError_t linear_c(Q4gLinear a, int kw, int rw, hipStream_t s)
 {
+    constexpr int kTokens = 16 / PK * C; // of a workgroup
     a.kw = kw, a.rw = rw;
     const int64_t sets = ((a.n + 15) / 16 + RTN * rw - 1) / (RTN * rw), threads = 64 * kw * rw;
-    const size_t lds = kw > 1 ? (size_t)rw * kw * RTN * C * 64 * sizeof(f32x4) : 0;
-    const int64_t groups = (a.m + 16 * C - 1) / (16 * C);
+    const size_t lds = kw > 1 ? (size_t)rw * kw * RTN * C * (4 / PK) * 64 * sizeof(float) : 0;
+    const int64_t groups = (a.m + kTokens - 1) / kTokens;
     hipError_t e = hipSuccess;
     for (int64_t g0 = 0; g0 < groups && e == hipSuccess; g0 += 1 << 12) {
         const int64_t gn = groups - g0 < 1 << 12 ? groups - g0 : 1 << 12;
-        a.tok0 = g0 * 16 * C, a.tok_groups = (int)gn;
+        a.tok0 = g0 * kTokens, a.tok_groups = (int)gn;
         // parts of eight sets, so that only the last one's grid reaches past its rows
         e = launch_parts(sets, kPartThreads / (threads * gn) / 8 * 8, [&](int64_t first, int64_t count) {
             a.row0 = first * rw;
             const int64_t blocks = (count + 7) / 8 * 8 * gn;
-            q4g_linear_kernel<TX, GRP, RTN, C, I, D><<<(unsigned)blocks, (unsigned)threads, lds, s>>>(a);
+            q4g_linear_kernel<TX, GRP, RTN, C, PK, D><<<(unsigned)blocks, (unsigned)threads, lds, s>>>(a);
         });
     }
     return e;
@@ -219,20 +213,19 @@ hipError_t linear_x(const Q4gLinear &a, hipStream_t s)
     const int64_t rt = (a.n + 15) / 16, kt = (a.k + 127) / 128;
     auto split = [&](int64_t sets) { // waves along k: enough to fill the chip, two tiles each at least
         int kw = 1;
-        while (kw < 8 && sets * kw < 2048 && 4 * kw <= kt)
+        while (kw < 8 && sets * kw < 4096 && 2 * kw <= kt)
             kw *= 2;
         return kw;
     };
-    if (a.m <= 4) {
-        const int kw = split(rt);
-        return linear_c<TX, GRP, 1, 1, 1, 2>(a, kw, kw < 4 ? 4 / kw : 1, s);
-    }
-    if (a.m <= 16) {
-        const int kw = split(rt);
-        return linear_c<TX, GRP, 1, 1, 4, 2>(a, kw, kw < 4 ? 4 / kw : 1, s);
-    }
+    const int kw1 = split(rt), rw1 = kw1 < 4 ? 4 / kw1 : 1;
+    if (a.m <= 4)
+        return linear_c<TX, GRP, 1, 1, 4, 4>(a, kw1, rw1, s);
+    if (a.m <= 8)
+        return linear_c<TX, GRP, 1, 1, 2, 4>(a, kw1, rw1, s);
+    if (a.m <= 16)
+        return linear_c<TX, GRP, 1, 1, 1, 2>(a, kw1, rw1, s);
     const int kw = split((rt + 1) / 2 * ((a.m + 31) / 32));
-    return linear_c<TX, GRP, 2, 2, 4, 1>(a, kw, kw < 4 ? 4 / kw : 1, s);
+    return linear_c<TX, GRP, 2, 2, 1, 1>(a, kw, kw < 4 ? 4 / kw : 1, s);
 }
 
 template <int TX>
