@@ -454,7 +454,7 @@ __device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeTokens
 }
 
 template <int TX, int GRP>
-__global__ void __launch_bounds__(512) moe_gated_kernel(MoeArgs a)
+__global__ void __launch_bounds__(512, 4) moe_gated_kernel(MoeArgs a)
 {
     __shared__ MoeShared sh;
     extern __shared__ float part[];
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__(512) moe_gated_kernel(MoeArgs a)
     const int64_t tiles = (a.n + 15) / 16, step = (int64_t)gridDim.x * sets;
     for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
         if (n <= 4)
-            moe_gated_tile<TX, GRP, 4, 4>(a, who, e, 0, rt + rw, part);
+            moe_gated_tile<TX, GRP, 4, 2>(a, who, e, 0, rt + rw, part);
         else if (n <= 8)
-            moe_gated_tile<TX, GRP, 2, 2>(a, who, e, 0, rt + rw, part);
+            moe_gated_tile<TX, GRP, 2, 1>(a, who, e, 0, rt + rw, part);
         else
             for (int p = 0; p < n; p += 16)
                 moe_gated_tile<TX, GRP, 1, 1>(a, who, e, p, rt + rw, part);
@@ -511,7 +511,7 @@ __device__ __forceinline__ void moe_down_tile(const MoeArgs &a, const MoeTokens 
 // One workgroup for 16 rows: the waves share out the active experts and the parts
 // of n; each adds up its own, then their sums are added in order.
 template <int TX, int GRP>
-__global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs a)
+__global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a)
 {
     extern __shared__ float sums[]; // [waves][m][16]
     const int wave = wave_number(), lane = threadIdx.x % 64, waves = blockDim.x / 64;
@@ -531,9 +531,9 @@ __global__ void __launch_bounds__(512) moe_down_kernel(MoeArgs a)
         const int e = __builtin_amdgcn_readfirstlane(plan.expert);
         const int t0 = item % a.parts * per, t1 = t0 + per < kt ? t0 + per : kt;
         if (n <= 4)
-            moe_down_tile<TX, GRP, 4, 4>(a, who, weight, e, 0, rt, t0, t1, own);
+            moe_down_tile<TX, GRP, 4, 2>(a, who, weight, e, 0, rt, t0, t1, own);
         else if (n <= 8)
-            moe_down_tile<TX, GRP, 2, 2>(a, who, weight, e, 0, rt, t0, t1, own);
+            moe_down_tile<TX, GRP, 2, 1>(a, who, weight, e, 0, rt, t0, t1, own);
         else
             for (int p = 0; p < n; p += 16)
                 moe_down_tile<TX, GRP, 1, 1>(a, who, weight, e, p, rt, t0, t1, own);
@@ -569,7 +569,7 @@ hipError_t experts(MoeArgs a, hipStream_t s)
     a.parts = 1;
     while (a.parts < 16 && a.active * a.parts < 64 && 4 * a.parts <= nt)
         a.parts *= 2;
-    const int items = a.active * a.parts, waves = items < 8 ? items : 8;
+    const int items = a.active * a.parts, waves = items < 16 ? items : 16;
     constexpr int TH = TX == Q4G_X_F32 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
     moe_down_kernel<TH, GRP><<<(unsigned)dt, 64 * waves, (size_t)waves * a.m * 16 * sizeof(float), s>>>(a);
     return hipGetLastError();
