@@ -290,15 +290,33 @@ hipError_t top_e(const double *l, const float *bias, int sigmoid, int renorm, fl
 // ------------------------------------------------------------ experts
 
 constexpr int kMoeTokens = 64; // at most, in one go
+constexpr int kMoePairs = kMoeTokens * (int)kMaxTop;
+constexpr int kMoeEntries = (int)kMaxExperts + kMoePairs / 16;
 
-// The experts that a group of at most 64 tokens chose, in ascending order, are its
-// active ones; active expert a's tokens are numbered in ascending order too.  A token
-// that names an expert twice counts once, with the sum of its weights.
+// Who chose whom, for a group of at most 64 tokens.  An entry is up to 4, 8 or 16 tokens of
+// an expert (class 0, 1, 2): an expert with at most four tokens is one entry of class 0, up to eight
+// one of class 1, more of them entries of sixteen.  begin[c] is class c's first entry,
+// begin[3] their number; entries stand in ascending order of the experts within
+// a class.  A token that names an expert twice counts once, with the sum of its weights.
 struct MoePlan {
-    int32_t expert, count; // count 0: no such active expert
-    uint32_t row[kMoeTokens]; // per token of the expert: token << 16 | its row in h, token * top + first slot of it
-    float weight[kMoeTokens];
+    int32_t begin[4];
+    uint32_t entry[kMoeEntries]; // expert | first pair << 10 | pairs << 21
+    uint16_t row[kMoePairs];     // per pair: its row in h, token * top + the first slot of that expert
+    float weight[kMoePairs];
 };
+
+struct MoeEntry {
+    int expert, first, count;
+    __device__ __forceinline__ explicit MoeEntry(uint32_t v)
+        : expert(v & 1023), first(v >> 10 & 2047), count(v >> 21)
+    {
+    }
+    __host__ __device__ static constexpr uint32_t packed(int expert, int first, int count)
+    {
+        return (uint32_t)expert | (uint32_t)first << 10 | (uint32_t)count << 21;
+    }
+};
+static_assert(kMaxExperts <= 1024 && kMoePairs <= 2048, "the fields of an entry");
 
 // The gated products between the two kernels: two bf16 parts of each where the
 // stream has 16 bits (what is left out is below 2^-17 of the value, against 2^-9 and 2^-12 of
@@ -315,107 +333,97 @@ struct MoeArgs {
     MoePlan *plan;
     int64_t n, k, gu_bytes, d_bytes; // bytes from one expert to the next
     int m, top, e, fmt, act, dtype;
-    int kw;    // gated products: waves along k
-    int active, parts; // down products: active experts at most, parts of n
+    int kw; // gated products: waves along k
 };
 
-struct MoeShared { // what a workgroup finds out about the choices first
-    int32_t ids[kMoeTokens * kMaxTop];
-    uint32_t active[kMaxExperts / 32];
-};
-
-__device__ __forceinline__ void moe_choices(MoeShared &sh, const MoeArgs &a)
+// One workgroup makes the plan; threads are experts, then pairs.
+__device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weights, int m, int top, int e, MoePlan &plan)
 {
-    for (int i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x)
-        sh.active[i] = 0;
+    __shared__ unsigned long long chose[kMaxExperts]; // tokens that named it
+    __shared__ unsigned long long sums[16];
+    __shared__ int32_t id[kMoePairs];
+    __shared__ uint16_t first[kMaxExperts];
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64; // 1024 threads
+    chose[tid] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.m * a.top; i += blockDim.x) {
-        const int id = a.ids[i];
-        sh.ids[i] = id;
-        if (id >= 0 && id < a.e)
-            atomicOr(&sh.active[id >> 5], 1u << (id & 31));
+    for (int i = tid; i < m * top; i += 1024) {
+        const int v = ids[i];
+        id[i] = v;
+        if (v >= 0 && v < e)
+            atomicOr(&chose[v], 1ull << (i / top));
     }
     __syncthreads();
-}
-
-// Active expert number a, or -1.
-__device__ __forceinline__ int moe_expert(const MoeShared &sh, int a)
-{
-    const int lane = threadIdx.x % 64;
-    const uint32_t word = lane < kMaxExperts / 32 ? sh.active[lane] : 0;
-    int before = __builtin_popcount(word);
-    const int own = before;
+    const int count = __builtin_popcountll(chose[tid]);
+    const int cls = count <= 4 ? 0 : count <= 8 ? 1 : 2, entries = cls < 2 ? count > 0 : (count + 15) / 16;
+    // running sums of the pairs and of each class's entries, 16 bits each
+    const uint64_t own = (uint64_t)count | (uint64_t)entries << (16 * (cls + 1));
+    uint64_t upto = own;
 #pragma unroll
-    for (int o = 1; o < kMaxExperts / 32; o <<= 1) {
-        const int v = __shfl_up(before, o);
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t v = __shfl_up((unsigned long long)upto, o);
         if (lane >= o)
-            before += v;
+            upto += v;
     }
-    before -= own;
-    int id = -1;
-    if (a >= before && a < before + own) {
-        uint32_t w = word;
-        for (int i = before; i < a; i++)
-            w &= w - 1;
-        id = lane * 32 + __builtin_ctz(w);
+    if (lane == 63)
+        sums[wave] = upto;
+    __syncthreads();
+    uint64_t before = upto - own, all = 0;
+    for (int w = 0; w < 16; w++) {
+        if (w < wave)
+            before += sums[w];
+        all += sums[w];
     }
-    const uint64_t who = __ballot(id >= 0);
-    return who ? __shfl(id, __builtin_ctzll(who)) : -1;
+    const int c0 = all >> 16 & 0xffff, c1 = all >> 32 & 0xffff, c2 = all >> 48;
+    if (tid == 0)
+        plan.begin[0] = 0, plan.begin[1] = c0, plan.begin[2] = c0 + c1, plan.begin[3] = c0 + c1 + c2;
+    first[tid] = (uint16_t)before;
+    const int at = (int)(before >> (16 * (cls + 1)) & 0xffff) + (cls == 0 ? 0 : cls == 1 ? c0 : c0 + c1);
+    for (int i = 0; i < entries; i++)
+        plan.entry[at + i] = MoeEntry::packed(tid, (int)(before & 0xffff) + 16 * i, min(count - 16 * i, 16));
+    __syncthreads();
+    for (int i = tid; i < m * top; i += 1024) {
+        const int v = id[i], t = i / top;
+        bool once = v >= 0 && v < e;
+        for (int j = t * top; j < i; j++)
+            once = once && id[j] != v;
+        if (once) {
+            float w = 0.0f;
+            for (int j = i; j < (t + 1) * top; j++)
+                w += id[j] == v ? weights[j] : 0.0f;
+            const int p = first[v] + __builtin_popcountll(chose[v] & ((1ull << t) - 1));
+            plan.row[p] = (uint16_t)i;
+            plan.weight[p] = w;
+        }
+    }
 }
 
-// An expert's tokens: lane p holds number p (the last one past the end) as token << 16 | row.
-struct MoeTokens {
-    int count;
-    uint32_t row;
-    __device__ __forceinline__ uint32_t of(int p) const { return __shfl(row, p < count ? p : count - 1); }
-};
-
-__device__ __forceinline__ MoeTokens moe_tokens(const MoeShared &sh, const MoeArgs &a, int e, MoePlan *plan)
-{
-    const int t = threadIdx.x % 64;
-    int slot = -1;
-    float weight = 0.0f;
-    if (t < a.m)
-        for (int j = a.top - 1; j >= 0; j--)
-            if (sh.ids[t * a.top + j] == e) {
-                slot = j;
-                if (plan)
-                    weight += a.weights[t * a.top + j];
-            }
-    const uint64_t mask = __ballot(slot >= 0);
-    const int at = __builtin_popcountll(mask & (((uint64_t)1 << t) - 1)), count = __builtin_popcountll(mask);
-    const uint32_t mine = (uint32_t)t << 16 | (uint32_t)(t * a.top + slot);
-    if (plan && slot >= 0)
-        plan->row[at] = mine, plan->weight[at] = weight;
-    // token number p stands in the lane of the mask's p-th bit
-    uint64_t left = mask;
-    for (int i = t < count ? t : count - 1; i > 0; i--)
-        left &= left - 1;
-    return {count, (uint32_t)__shfl(mine, __builtin_ctzll(left))};
-}
+__global__ void __launch_bounds__(1024) moe_plan_kernel(MoeArgs a) { moe_plan(a.ids, a.weights, a.m, a.top, a.e, *a.plan); }
 
 __device__ __forceinline__ void store_part(uint8_t *h, int64_t at, float v)
 {
     reinterpret_cast<uint16_t *>(h)[at] = (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
 }
 
-// Gated products of an expert's tokens [p0, p0 + 16 / PK) on one row tile of gate and up a wave.
-template <int TX, int GRP, int PK, int D>
-__device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeTokens &who, int e, int p0, int64_t rt,
-                                               float *part)
+// Gated products of an entry's tokens on one row tile of gate and up a wave.  ONE: the
+// only token's choice number entry.first, without a plan.
+template <int TX, int GRP, int PK, int D, bool ONE>
+__device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeEntry &entry, int64_t rt, float *part)
 {
     using Wave = Q4gWave<TX, GRP, 2, 1, PK, D>;
     constexpr int N = Wave::N;
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
     const int lane = opaque_lane(), wave = wave_number(), kw = wave % a.kw, set = wave - kw;
+    const auto row = [&](int p) { // of h; past the last the last one
+        return ONE ? entry.first : (int)a.plan->row[entry.first + (p < entry.count ? p : entry.count - 1)];
+    };
     Wave w;
     w.clear();
     if (rt < sh.rt) {
         typename Wave::Rows rows;
-        rows.w[0] = Q4gRows(a.wg + e * a.gu_bytes, sh, rt, GRP, a.fmt);
-        rows.w[1] = Q4gRows(a.wu + e * a.gu_bytes, sh, rt, GRP, a.fmt);
+        rows.w[0] = Q4gRows(a.wg + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
+        rows.w[1] = Q4gRows(a.wu + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
         rows.x = static_cast<const uint8_t *>(a.x); // 64 rows of under 2^24 elements: offsets below 2^32
-        rows.at[0] = (who.of(p0 + Wave::row_of(lane)) >> 16) * (uint32_t)a.k * q4g_x_size(TX);
+        rows.at[0] = ONE ? 0 : (uint32_t)(row(Wave::row_of(lane)) / a.top) * (uint32_t)a.k * q4g_x_size(TX);
         rows.part = 0, rows.last = (int)a.k - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
         const int kt = (int)sh.kt, per = (kt + a.kw - 1) / a.kw, t0 = kw * per;
         w.run(rows, t0, t0 + per < kt ? t0 + per : kt);
@@ -437,9 +445,9 @@ __device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeTokens
             for (int o = 1; o < a.kw; o++)
                 g += part[((set + o) * 2 * N + i) * 64 + lane], u += part[(((set + o) * 2 + 1) * N + i) * 64 + lane];
         }
-        const int p = p0 + Wave::out_of(lane, i);
-        const int64_t at = (int64_t)(who.of(p) & 0xffffu) * a.n + j;
-        if (p < who.count && j < a.n) {
+        const int p = Wave::out_of(lane, i);
+        if (p < entry.count && j < a.n) {
+            const int64_t at = row(p) * a.n + j;
             const float v = activate(g, a.act) * u, v1 = below_bf16(v);
             store_part(a.h, at, v);
             if (TX == Q4G_X_F32) {
@@ -453,96 +461,166 @@ __device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeTokens
         __syncthreads();
 }
 
-template <int TX, int GRP>
+template <int TX, int GRP, bool ONE>
 __global__ void __launch_bounds__(512, 4) moe_gated_kernel(MoeArgs a)
 {
-    __shared__ MoeShared sh;
     extern __shared__ float part[];
-    moe_choices(sh, a);
-    const int e = __builtin_amdgcn_readfirstlane(moe_expert(sh, blockIdx.y));
-    MoePlan *plan = blockIdx.x == 0 && threadIdx.x < 64 ? a.plan + blockIdx.y : nullptr; // the down kernel's
-    if (e < 0) {
-        if (plan && threadIdx.x == 0)
-            plan->count = 0;
-        return;
-    }
-    const MoeTokens who = moe_tokens(sh, a, e, plan);
-    if (plan && threadIdx.x == 0)
-        plan->expert = e, plan->count = who.count;
-    const int rw = wave_number() / a.kw, sets = blockDim.x / 64 / a.kw, n = who.count;
+    const int rw = wave_number() / a.kw, sets = blockDim.x / 64 / a.kw, y = blockIdx.y;
     const int64_t tiles = (a.n + 15) / 16, step = (int64_t)gridDim.x * sets;
-    for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
-        if (n <= 4)
-            moe_gated_tile<TX, GRP, 4, 2>(a, who, e, 0, rt + rw, part);
-        else if (n <= 8)
-            moe_gated_tile<TX, GRP, 2, 1>(a, who, e, 0, rt + rw, part);
-        else
-            for (int p = 0; p < n; p += 16)
-                moe_gated_tile<TX, GRP, 1, 1>(a, who, e, p, rt + rw, part);
+    if constexpr (ONE) {
+        const int id = a.ids[y];
+        if (id < 0 || id >= a.e)
+            return;
+        const MoeEntry entry(MoeEntry::packed(id, y, 1));
+        for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
+            moe_gated_tile<TX, GRP, 4, 2, true>(a, entry, rt + rw, part);
+    } else {
+        if (y >= a.plan->begin[3])
+            return;
+        const MoeEntry entry(__builtin_amdgcn_readfirstlane(a.plan->entry[y]));
+        for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
+            if (y < a.plan->begin[1])
+                moe_gated_tile<TX, GRP, 4, 2, false>(a, entry, rt + rw, part);
+            else if (y < a.plan->begin[2])
+                moe_gated_tile<TX, GRP, 2, 1, false>(a, entry, rt + rw, part);
+            else
+                moe_gated_tile<TX, GRP, 1, 1, false>(a, entry, rt + rw, part);
+    }
 }
 
-// Down products of 16 rows and an expert's tokens [p0, p0 + 16 / PK), weighted and added
-// to the wave's own sums [m][16].  No two of them are one token's.
+// What a workgroup of the down products keeps in LDS.
+struct MoeLists {
+    float *sums, *weight;  // sums [waves][m][16]
+    uint32_t *entry;
+    uint16_t *row;
+};
+
+// Down products of 16 rows with the entries [e0, e1) of a class.  The tiles of their
+// matrices' 16 rows, one entry after another, are one sequence that the waves
+// share evenly, each with D tiles in flight across the entries' ends; at such an end it adds its
+// weighted products to its own sums [m][16].  No two products of an entry are one token's.
 template <int TX, int GRP, int PK, int D>
-__device__ __forceinline__ void moe_down_tile(const MoeArgs &a, const MoeTokens &who, float weight, int e, int p0,
-                                              int64_t rt, int t0, int t1, float *sums)
+__device__ __forceinline__ void moe_down_stream(const MoeArgs &a, const MoeLists &l, int e0, int e1, int64_t rt,
+                                                int waves)
 {
     using Wave = Q4gWave<TX, GRP, 1, 1, PK, D>;
     const Q4gShape sh(a.k, a.n, GRP, a.fmt);
-    const int lane = opaque_lane();
+    const int lane = opaque_lane(), wave = wave_number(), kt = (int)sh.kt;
+    const int64_t tiles = (int64_t)(e1 - e0) * kt;
+    const int64_t f0 = tiles * wave / waves, f1 = tiles * (wave + 1) / waves;
+    if (f0 >= f1)
+        return;
+    float *sums = l.sums + wave * a.m * 16;
     typename Wave::Rows rows;
-    rows.w[0] = Q4gRows(a.wd + e * a.d_bytes, sh, rt, GRP, a.fmt);
     rows.x = a.h; // 2048 rows of under 2^20 elements: offsets below 2^32
-    rows.at[0] = (who.of(p0 + Wave::row_of(lane)) & 0xffffu) * (uint32_t)a.n * 2;
     rows.part = (int64_t)a.m * a.top * a.n * 2, rows.last = (int)a.n - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
     Wave w;
     w.clear();
-    w.run(rows, t0, t1);
+    typename Wave::Stage st[D];
+    int le = e0 + (int)(f0 / kt), lt = (int)(f0 % kt), ue = le, ut = lt; // the next tile to load, to use
+    const auto enter = [&]() {
+        const MoeEntry en(__builtin_amdgcn_readfirstlane(l.entry[le]));
+        const int p = Wave::row_of(lane);
+        rows.w[0] = Q4gRows(a.wd + en.expert * a.d_bytes, sh, rt, GRP, a.fmt);
+        rows.at[0] = l.row[en.first + (p < en.count ? p : en.count - 1)] * (uint32_t)a.n * 2;
+    };
+    const auto leave = [&]() {
+        const MoeEntry en(__builtin_amdgcn_readfirstlane(l.entry[ue]));
 #pragma unroll
-    for (int i = 0; i < Wave::N; i++) {
-        const int p = p0 + Wave::out_of(lane, i);
-        float *to = sums + (who.of(p) >> 16) * 16 + lane % 16;
-        const float f = __shfl(weight, p & 63);
-        if (p < who.count)
-            *to = fmaf(f, w.y[0][0][i], *to);
+        for (int i = 0; i < Wave::N; i++) {
+            const int p = Wave::out_of(lane, i);
+            if (p < en.count) {
+                float *to = sums + l.row[en.first + p] / a.top * 16 + lane % 16;
+                *to = fmaf(l.weight[en.first + p], w.y[0][0][i], *to);
+            }
+        }
+        w.clear();
+    };
+    int64_t left = f1 - f0; // tiles to load
+    const auto load = [&](typename Wave::Stage &s) {
+        Wave::load(s, rows, lt);
+        if (--left > 0 && ++lt == kt) { // past the end: the last one again
+            lt = 0, le++;
+            enter();
+        }
+    };
+    const auto use = [&](const typename Wave::Stage &s) {
+        w.use(s, rows.bf16, ut);
+        if (++ut == kt) {
+            leave();
+            ut = 0, ue++;
+        }
+    };
+    enter();
+#pragma unroll
+    for (int i = 0; i < D; i++)
+        load(st[i]);
+    int64_t f = f0;
+    for (; f + D < f1; f += D) {
+#pragma unroll
+        for (int i = 0; i < D; i++) {
+            use(st[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(st[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < D; i++) {
+        if (f + i < f1)
+            use(st[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (ut > 0)
+        leave();
 }
 
-// One workgroup for 16 rows: the waves share out the active experts and the parts
-// of n; each adds up its own, then their sums are added in order.
-template <int TX, int GRP>
-__global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a)
+constexpr int kDownWaves = 16;
+
+// One workgroup for 16 rows, over all entries; the waves' sums are added in order.
+template <int TX, int GRP, bool ONE>
+__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
 {
-    extern __shared__ float sums[]; // [waves][m][16]
-    const int wave = wave_number(), lane = threadIdx.x % 64, waves = blockDim.x / 64;
-    float *own = sums + wave * a.m * 16;
-    for (int i = lane; i < a.m * 16; i += 64)
-        own[i] = 0.0f;
+    extern __shared__ float lds[];
+    const int waves = blockDim.x / 64, pairs = a.m * a.top;
+    MoeLists l;
+    l.sums = lds, l.weight = l.sums + waves * a.m * 16;
+    l.entry = reinterpret_cast<uint32_t *>(l.weight + pairs);
+    for (int i = threadIdx.x; i < waves * a.m * 16; i += blockDim.x)
+        l.sums[i] = 0.0f;
     const int64_t rt = blockIdx.x;
-    const int kt = (int)((a.n + 127) / 128), per = (kt + a.parts - 1) / a.parts;
-    for (int item = wave; item < a.active * a.parts; item += waves) {
-        const MoePlan &plan = a.plan[item / a.parts];
-        const int n = __builtin_amdgcn_readfirstlane(plan.count);
-        if (n == 0)
-            break;
-        const int at = lane < n ? lane : n - 1;
-        const MoeTokens who = {n, plan.row[at]};
-        const float weight = plan.weight[at];
-        const int e = __builtin_amdgcn_readfirstlane(plan.expert);
-        const int t0 = item % a.parts * per, t1 = t0 + per < kt ? t0 + per : kt;
-        if (n <= 4)
-            moe_down_tile<TX, GRP, 4, 2>(a, who, weight, e, 0, rt, t0, t1, own);
-        else if (n <= 8)
-            moe_down_tile<TX, GRP, 2, 1>(a, who, weight, e, 0, rt, t0, t1, own);
-        else
-            for (int p = 0; p < n; p += 16)
-                moe_down_tile<TX, GRP, 1, 1>(a, who, weight, e, p, rt, t0, t1, own);
+    if constexpr (ONE) { // the only token's choices are the entries, but for padding
+        l.row = reinterpret_cast<uint16_t *>(l.entry + pairs);
+        const int i = threadIdx.x, id = i < a.top ? a.ids[i] : -1;
+        const bool in = id >= 0 && id < a.e;
+        const uint64_t who = __ballot(in);
+        if (in) {
+            const int at = __builtin_popcountll(who & ((1ull << i) - 1));
+            l.entry[at] = MoeEntry::packed(id, at, 1);
+            l.row[at] = (uint16_t)i, l.weight[at] = a.weights[i];
+        }
+        __shared__ int count;
+        if (i == 0)
+            count = __builtin_popcountll(who);
+        __syncthreads();
+        moe_down_stream<TX, GRP, 4, 4>(a, l, 0, count, rt, waves);
+    } else {
+        const int c1 = a.plan->begin[1], c2 = a.plan->begin[2], c3 = a.plan->begin[3];
+        l.row = reinterpret_cast<uint16_t *>(l.entry + c3);
+        for (int i = threadIdx.x; i < c3; i += blockDim.x)
+            l.entry[i] = a.plan->entry[i];
+        for (int i = threadIdx.x; i < pairs; i += blockDim.x)
+            l.row[i] = a.plan->row[i], l.weight[i] = a.plan->weight[i];
+        __syncthreads();
+        moe_down_stream<TX, GRP, 4, 4>(a, l, 0, c1, rt, waves);
+        moe_down_stream<TX, GRP, 2, 2>(a, l, c1, c2, rt, waves);
+        moe_down_stream<TX, GRP, 1, 1>(a, l, c2, c3, rt, waves);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.m * 16; i += blockDim.x) {
-        float v = sums[i];
+        float v = l.sums[i];
         for (int o = 1; o < waves; o++)
-            v += sums[o * a.m * 16 + i];
+            v += l.sums[o * a.m * 16 + i];
         const int64_t j = rt * 16 + i % 16, at = i / 16 * a.k + j;
         if (j < a.k) {
             if (a.res)
@@ -552,33 +630,38 @@ __global__ void __launch_bounds__(1024) moe_down_kernel(MoeArgs a)
     }
 }
 
-template <int TX, int GRP>
+template <int TX, int GRP, bool ONE>
 hipError_t experts(MoeArgs a, hipStream_t s)
 {
-    a.active = a.m * a.top < a.e ? a.m * a.top : a.e;
+    const int64_t pairs = (int64_t)a.m * a.top, active = pairs < a.e ? pairs : a.e;
     const int64_t rt = (a.n + 15) / 16, kt = (a.k + 127) / 128, dt = (a.k + 15) / 16, nt = (a.n + 127) / 128;
     a.kw = 1;
-    while (a.kw < 8 && rt * a.active * a.kw < 4096 && 2 * a.kw <= kt)
+    while (a.kw < 8 && rt * active * a.kw < 4096 && 2 * a.kw <= kt)
         a.kw *= 2;
-    const int64_t most = (rt * a.kw + 7) / 8, want = (1024 + a.active - 1) / a.active;
-    moe_gated_kernel<TX, GRP><<<dim3((unsigned)(most < want ? most : want), (unsigned)a.active), 512,
-                               a.kw > 1 ? (size_t)8 * 2 * 4 * 64 * sizeof(float) : 0, s>>>(a);
+    const int64_t most = (rt * a.kw + 7) / 8, want = (1024 + active - 1) / active;
+    const int64_t entries = ONE ? pairs : active + pairs / 16; // at most
+    moe_gated_kernel<TX, GRP, ONE><<<dim3((unsigned)(most < want ? most : want), (unsigned)entries), 512,
+                                    a.kw > 1 ? (size_t)8 * 2 * 4 * 64 * sizeof(float) : 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    a.parts = 1;
-    while (a.parts < 16 && a.active * a.parts < 64 && 4 * a.parts <= nt)
-        a.parts *= 2;
-    const int items = a.active * a.parts, waves = items < 16 ? items : 16;
+    const int64_t most_waves = a.m > 32 ? 8 : kDownWaves, waves = active * nt < most_waves ? active * nt : most_waves;
+    const size_t lds = (size_t)waves * a.m * 64 + pairs * 6 + entries * 4;
     constexpr int TH = TX == Q4G_X_F32 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
-    moe_down_kernel<TH, GRP><<<(unsigned)dt, 64 * waves, (size_t)waves * a.m * 16 * sizeof(float), s>>>(a);
+    moe_down_kernel<TH, GRP, ONE><<<(unsigned)dt, (unsigned)(64 * waves), lds, s>>>(a);
     return hipGetLastError();
 }
 
 template <int TX>
 hipError_t experts_g(const MoeArgs &a, int64_t group, hipStream_t s)
 {
-    return group == 32 ? experts<TX, 32>(a, s) : group == 64 ? experts<TX, 64>(a, s) : experts<TX, 128>(a, s);
+    if (a.m == 1)
+        return group == 32 ? experts<TX, 32, true>(a, s) : group == 64 ? experts<TX, 64, true>(a, s) : experts<TX, 128, true>(a, s);
+    moe_plan_kernel<<<1, 1024, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    return group == 32 ? experts<TX, 32, false>(a, s) : group == 64 ? experts<TX, 64, false>(a, s) : experts<TX, 128, false>(a, s);
 }
 
 } // namespace
@@ -599,17 +682,13 @@ hipError_t launch_moe_route(const void *x, int dtype, const void *w, int w_dtype
     return choose(l, bias, sigmoid, renorm, scale, ids, weights, top, m, e, s);
 }
 
-// Groups of 64 tokens, one after another, in the same workspace: plans, then h.
-static size_t moe_plan_bytes(int64_t tokens, int64_t top)
-{
-    const int64_t active = tokens * top < kMaxExperts ? tokens * top : kMaxExperts;
-    return ((size_t)active * sizeof(MoePlan) + 255) / 256 * 256;
-}
+// Groups of 64 tokens, one after another, in the same workspace: the plan, then h.
+constexpr size_t kMoePlanBytes = (sizeof(MoePlan) + 255) / 256 * 256;
 
 size_t q4g_moe_workspace(int64_t m, int64_t n, int64_t top)
 {
     const int64_t tokens = m < kMoeTokens ? m : kMoeTokens;
-    return moe_plan_bytes(tokens, top) + ((size_t)(tokens * top * n) * 6 + 255) / 256 * 256;
+    return kMoePlanBytes + ((size_t)(tokens * top * n) * 6 + 255) / 256 * 256;
 }
 
 hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top,
@@ -628,7 +707,7 @@ hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const fl
         a.n = n, a.k = k;
         a.gu_bytes = q4g_packed_bytes(n, k, group, fmt), a.d_bytes = q4g_packed_bytes(k, n, group, fmt);
         a.m = (int)(m - t0 < kMoeTokens ? m - t0 : kMoeTokens), a.top = (int)top, a.e = (int)e;
-        a.h = static_cast<uint8_t *>(ws) + moe_plan_bytes(a.m, top);
+        a.h = static_cast<uint8_t *>(ws) + kMoePlanBytes;
         a.fmt = fmt, a.act = act, a.dtype = dtype;
         const hipError_t rc = dtype == QLL_W_F32    ? experts_g<Q4G_X_F32>(a, group, s)
                               : dtype == QLL_W_BF16 ? experts_g<Q4G_X_BF16>(a, group, s)

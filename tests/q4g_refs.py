@@ -107,6 +107,8 @@ def moe(x, ids, weights, wg, wu, wd, act, residual, dtype):
                 continue
             row = x[t:t + 1]
             h, eh = E.gated(*wg.product(row, i=e), *wu.product(row, i=e), act)
+            if dtype != "f32":  # kept as two bf16 parts: the first cut off, the second rounded
+                eh = eh + (np.abs(h) + eh) * 2.0 ** -16
             d, ed = wd.product(h, eh, i=e)
             w = float(weights[t, j])
             y[t] += w * d[0]
