@@ -195,7 +195,7 @@ size_t qll_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
     case QLL_OP_Q4G_LINEAR:
         if (!dims_ok(m, k) || !dims_ok(n, k) || !dims_ok(m, n) || k % 32 != 0 || k >= kMaxGemmK)
             return SIZE_MAX;
-        return 0;
+        return q4g_linear_workspace(m, n, k);
     case QLL_OP_MOE_ROUTE:
         if (!route_dims_ok(m, n, k))
             return SIZE_MAX;
@@ -792,7 +792,6 @@ int qll_q4g_linear(const void *wp, int64_t group, int fmt, const void *x, int dt
                    const void *residual, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
                    size_t ws_bytes, void *stream)
 {
-    (void)ws_bytes;
     if (!wp || !x || !y)
         return QLL_ERR_NULL;
     if (!q4g_format_ok(group, fmt) || !dtype_ok(dtype) || !dtype_ok(y_dtype) || !act_ok(act))
@@ -801,10 +800,13 @@ int qll_q4g_linear(const void *wp, int64_t group, int fmt, const void *x, int dt
         return QLL_ERR_SHAPE;
     if (!aligned16(wp) || !aligned16(x) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) || !aligned16(ws))
         return QLL_ERR_ALIGN;
+    const size_t need = q4g_linear_workspace(m, n, k);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return QLL_ERR_WORKSPACE;
     if (int rc = check_device())
         return rc;
     return launched(launch_q4g_linear(static_cast<const uint8_t *>(wp), group, fmt, x, dtype, bias, act, residual, y,
-                                      y_dtype, m, n, k, as_stream(stream)));
+                                      y_dtype, m, n, k, ws, as_stream(stream)));
 }
 
 // What the router's arguments have to be; QLL_OK or the status to return.

@@ -421,8 +421,11 @@ hipError_t launch_q4g_pack(const uint8_t *codes, const uint16_t *scales, const u
                            uint8_t *wp, int64_t n, int64_t k, hipStream_t s);
 hipError_t launch_q4g_from_q4_0(const uint8_t *w, uint8_t *wp, int64_t n, int64_t k, hipStream_t s);
 hipError_t launch_q4g_linear(const uint8_t *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias,
-                             int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k,
+                             int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
                              hipStream_t s);
+size_t q4g_linear_workspace(int64_t m, int64_t n, int64_t k);
+// f32 values (a multiple of eight of them) as three bf16 parts, one after another.
+hipError_t launch_q4g_split(const void *x, void *parts, int64_t count, hipStream_t s);
 constexpr int64_t kMaxExperts = 1024, kMaxTop = 32;
 constexpr int64_t kMaxMoeN = (int64_t)1 << 20; // the experts' inner size: 32-bit offsets into the gated products
 size_t moe_route_workspace(int64_t m, int64_t e);

@@ -333,7 +333,9 @@ struct MoeArgs {
     MoePlan *plan;
     int64_t n, k, gu_bytes, d_bytes; // bytes from one expert to the next
     int m, top, e, fmt, act, dtype;
-    int kw; // gated products: waves along k
+    int kw;     // waves along k
+    float *out; // down products of each choice, [m * top][k]
+    uint8_t *x_parts; // f32 rows as three bf16 parts, [part][m][k] (in the same place, before them)
 };
 
 // One workgroup makes the plan; threads are experts, then pairs.
@@ -404,264 +406,349 @@ __device__ __forceinline__ void store_part(uint8_t *h, int64_t at, float v)
     reinterpret_cast<uint16_t *>(h)[at] = (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
 }
 
-// Gated products of an entry's tokens on one row tile of gate and up a wave.  ONE: the
-// only token's choice number entry.first, without a plan.
-template <int TX, int GRP, int PK, int D, bool ONE>
-__device__ __forceinline__ void moe_gated_tile(const MoeArgs &a, const MoeEntry &entry, int64_t rt, float *part)
+enum { MOE_ONE, MOE_FEW, MOE_ALL }; // one token; up to four; more
+
+// What becomes of an entry's products with one row tile, N a lane.  The waves of a set add up in LDS:
+// KW along k.  GATED: gate and up product meet, in a wave (R = 2) or as the set's KW waves on the
+// gate matrix and KW on the up matrix (R = 1), and the products' parts go to h.  Otherwise the products
+// go to `out` [m * top][k], f32, one row a choice.
+template <bool WIDE, bool GATED, int KIND, int R, int N>
+__device__ __forceinline__ void moe_outputs(const MoeArgs &a, const MoeEntry &entry, const float (&y)[R][1][N], int64_t rt,
+                                            int KW, float *sums, int lane)
 {
-    using Wave = Q4gWave<TX, GRP, 2, 1, PK, D>;
-    constexpr int N = Wave::N;
-    const Q4gShape sh(a.n, a.k, GRP, a.fmt);
-    const int lane = opaque_lane(), wave = wave_number(), kw = wave % a.kw, set = wave - kw;
-    const auto row = [&](int p) { // of h; past the last the last one
-        return ONE ? entry.first : (int)a.plan->row[entry.first + (p < entry.count ? p : entry.count - 1)];
-    };
-    Wave w;
-    w.clear();
-    if (rt < sh.rt) {
-        typename Wave::Rows rows;
-        rows.w[0] = Q4gRows(a.wg + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
-        rows.w[1] = Q4gRows(a.wu + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
-        rows.x = static_cast<const uint8_t *>(a.x); // 64 rows of under 2^24 elements: offsets below 2^32
-        rows.at[0] = ONE ? 0 : (uint32_t)(row(Wave::row_of(lane)) / a.top) * (uint32_t)a.k * q4g_x_size(TX);
-        rows.part = 0, rows.last = (int)a.k - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
-        const int kt = (int)sh.kt, per = (kt + a.kw - 1) / a.kw, t0 = kw * per;
-        w.run(rows, t0, t0 + per < kt ? t0 + per : kt);
-    }
-    if (a.kw > 1) {
+    const int SW = GATED && R == 1 ? 2 * KW : KW, wave = wave_number(), set = wave - wave % SW;
+    if (SW > 1) {
+        __syncthreads(); // LDS is read
 #pragma unroll
-        for (int i = 0; i < N; i++)
-            part[(wave * 2 * N + i) * 64 + lane] = w.y[0][0][i], part[((wave * 2 + 1) * N + i) * 64 + lane] = w.y[1][0][i];
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                sums[((wave * R + r) * N + i) * 64 + lane] = y[r][0][i];
         __syncthreads();
     }
-    const int64_t j = rt * 16 + lane % 16, whole = (int64_t)a.m * a.top * a.n;
+    const int64_t outs = GATED ? a.n : a.k, j = rt * 16 + lane % 16, whole = (int64_t)a.m * a.top * a.n;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        if (i % a.kw != kw) // the set's waves take turns
+        if (SW > 1 && i % SW != wave % SW) // the set's waves take turns
             continue;
-        float g = w.y[0][0][i], u = w.y[1][0][i];
-        if (a.kw > 1) {
-            g = part[(set * 2 * N + i) * 64 + lane], u = part[((set * 2 + 1) * N + i) * 64 + lane];
-            for (int o = 1; o < a.kw; o++)
-                g += part[((set + o) * 2 * N + i) * 64 + lane], u += part[(((set + o) * 2 + 1) * N + i) * 64 + lane];
-        }
-        const int p = Wave::out_of(lane, i);
-        if (p < entry.count && j < a.n) {
-            const int64_t at = row(p) * a.n + j;
-            const float v = activate(g, a.act) * u, v1 = below_bf16(v);
-            store_part(a.h, at, v);
-            if (TX == Q4G_X_F32) {
-                store_part(a.h, whole + at, v1);
-                store_part(a.h, 2 * whole + at, below_bf16(v1));
+        float v[2] = {y[0][0][i], y[R - 1][0][i]};
+        if (SW > 1)
+#pragma unroll
+            for (int b = 0; b < (GATED ? 2 : 1); b++) {
+                const int from = (R == 1 ? (set + b * KW) : set * R + b) * N + i;
+                v[b] = sums[from * 64 + lane];
+                for (int o = 1; o < KW; o++)
+                    v[b] += sums[(from + o * R * N) * 64 + lane];
+            }
+        const int p = lane / 16 * N + i;
+        if (p >= entry.count || j >= outs)
+            continue;
+        const int64_t to = (KIND == MOE_ONE ? entry.first : (int)a.plan->row[entry.first + p]) * outs + j;
+        if constexpr (GATED) {
+            const float h = activate(v[0], a.act) * v[1], rest = below_bf16(h);
+            store_part(a.h, to, h);
+            if (WIDE) {
+                store_part(a.h, whole + to, rest);
+                store_part(a.h, 2 * whole + to, below_bf16(rest));
             } else
-                reinterpret_cast<__bf16 *>(a.h)[whole + at] = (__bf16)v1;
-        }
+                reinterpret_cast<__bf16 *>(a.h)[whole + to] = (__bf16)rest;
+        } else
+            a.out[to] = v[0];
     }
-    if (a.kw > 1)
-        __syncthreads();
 }
 
-template <int TX, int GRP, bool ONE>
-__global__ void __launch_bounds__(512, 4) moe_gated_kernel(MoeArgs a)
+// An entry's products with every so-manieth set of row tiles, one of gate and one of up, or R of down.
+// Offsets into the rows are 32 bits: 64 rows of x of under 2^24 elements, 2048 of h of under 2^20.
+template <int TX, int GRP, bool GATED, int KIND>
+__device__ __forceinline__ void moe_few(const MoeArgs &a, const MoeEntry &entry, float *sums)
 {
-    extern __shared__ float part[];
-    const int rw = wave_number() / a.kw, sets = blockDim.x / 64 / a.kw, y = blockIdx.y;
-    const int64_t tiles = (a.n + 15) / 16, step = (int64_t)gridDim.x * sets;
-    if constexpr (ONE) {
+    constexpr int R = GATED ? 2 : 1;
+    using Wave = Q4gWave<TX, GRP, R, 4, GATED || TX == Q4G_X_PARTS3 ? 2 : 4>;
+    const int64_t outs = GATED ? a.n : a.k;
+    const int k = (int)(GATED ? a.k : a.n);
+    const Q4gShape sh(outs, k, GRP, a.fmt);
+    const int lane = opaque_lane(), wave = wave_number(), KW = a.kw, kw = wave % KW, sets = 8 / KW;
+    typename Wave::From f;
+    int row = entry.first;
+    if constexpr (KIND != MOE_ONE) { // past the last token: its row again
+        const int p = Wave::row_of(lane);
+        row = a.plan->row[entry.first + (p < entry.count ? p : entry.count - 1)];
+    }
+    f.x = !GATED ? a.h : TX == Q4G_X_PARTS3 ? a.x_parts : static_cast<const uint8_t *>(a.x);
+    f.at = (uint32_t)(GATED ? row / a.top : row) * (uint32_t)k * q4g_x_size(TX);
+    f.part = (int64_t)a.m * (GATED ? a.k : a.top * a.n) * 2, f.last = k - 32, f.kt = (int)sh.kt;
+    const int ks = (int)sh.ks, per = (ks + KW - 1) / KW, p0 = kw * per, p1 = p0 + per < ks ? p0 + per : ks;
+    for (int64_t at = (int64_t)blockIdx.x * sets; at < sh.rt; at += (int64_t)gridDim.x * sets) {
+        const int64_t rt = at + wave / KW;
+        Wave w;
+        w.clear();
+        if (rt < sh.rt) {
+            if constexpr (GATED) {
+                f.w[0] = Q4gRows(a.wg + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
+                f.w[1] = Q4gRows(a.wu + entry.expert * a.gu_bytes, sh, rt, GRP, a.fmt);
+            } else
+                f.w[0] = Q4gRows(a.wd + entry.expert * a.d_bytes, sh, rt, GRP, a.fmt);
+            w.run(f, p0, p1, a.fmt & kQ4gBf16, lane);
+        }
+        moe_outputs<TX == Q4G_X_F32 || TX == Q4G_X_PARTS3, GATED, KIND>(a, entry, w.y, rt, KW, sums, lane);
+    }
+}
+
+// The same for up to 16 / PK tokens, their rows in LDS, gate and up as two sets of waves (both in one
+// take up to 170 registers).
+template <int TX, int GRP, int PK, bool GATED>
+__device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry, uint8_t *lds)
+{
+    using Block = Q4gBlock<TX, GRP, 1, 1, PK, 4>;
+    const int64_t outs = GATED ? a.n : a.k;
+    const int k = (int)(GATED ? a.k : a.n);
+    const Q4gShape sh(outs, k, GRP, a.fmt);
+    const int KW = a.kw < Block::kPieces ? a.kw : Block::kPieces, SW = GATED ? 2 * KW : KW;
+    const int lane = opaque_lane(), wave = wave_number(), kw = wave % KW, sets = 8 / SW;
+    const uint8_t *matrix = GATED ? (wave / KW % 2 ? a.wu : a.wg) + entry.expert * a.gu_bytes : a.wd + entry.expert * a.d_bytes;
+    typename Block::X src;
+    src.base = !GATED ? a.h : TX == Q4G_X_PARTS3 ? a.x_parts : static_cast<const uint8_t *>(a.x), src.k = k;
+    src.part = (int64_t)a.m * (GATED ? a.k : a.top * a.n) * 2;
+    const int p = Block::row_of(lane);
+    src.at[0] = ~0u;
+    if (p < entry.count) {
+        const int row = a.plan->row[entry.first + p];
+        src.at[0] = (uint32_t)(GATED ? row / a.top : row) * (uint32_t)k * 2;
+    }
+    const int chunks = (k + Block::kChunk - 1) / Block::kChunk;
+    float *sums = reinterpret_cast<float *>(lds + (chunks == 1 ? Block::lds_bytes(k) : 0));
+    bool first = true;
+    for (int64_t at = (int64_t)blockIdx.x * sets; at < sh.rt; at += (int64_t)gridDim.x * sets) {
+        const int64_t rt = at + wave / SW;
+        const Q4gRows rows[1] = {Q4gRows(matrix, sh, rt < sh.rt ? rt : sh.rt - 1, GRP, a.fmt)};
+        Block w;
+        w.clear();
+        if (chunks > 1 && !first)
+            __syncthreads(); // LDS is read
+        w.run(rows, rt < sh.rt, src, 0, chunks, kw, KW, a.fmt & kQ4gBf16, chunks == 1 && !first, lds, lane);
+        first = false;
+        moe_outputs<TX == Q4G_X_PARTS3, GATED, MOE_ALL>(a, entry, w.y, rt, KW, sums, lane);
+    }
+}
+
+template <int TX, int GRP, bool GATED, int KIND>
+__global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t entry_lds[];
+    float *sums = reinterpret_cast<float *>(entry_lds);
+    const int y = blockIdx.y;
+    if constexpr (KIND == MOE_ONE) {
         const int id = a.ids[y];
-        if (id < 0 || id >= a.e)
-            return;
-        const MoeEntry entry(MoeEntry::packed(id, y, 1));
-        for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
-            moe_gated_tile<TX, GRP, 4, 2, true>(a, entry, rt + rw, part);
+        if (id >= 0 && id < a.e)
+            moe_few<TX, GRP, GATED, KIND>(a, MoeEntry(MoeEntry::packed(id, y, 1)), sums);
     } else {
         if (y >= a.plan->begin[3])
             return;
         const MoeEntry entry(__builtin_amdgcn_readfirstlane(a.plan->entry[y]));
-        for (int64_t rt = (int64_t)blockIdx.x * sets; rt < tiles; rt += step)
-            if (y < a.plan->begin[1])
-                moe_gated_tile<TX, GRP, 4, 2, false>(a, entry, rt + rw, part);
-            else if (y < a.plan->begin[2])
-                moe_gated_tile<TX, GRP, 2, 1, false>(a, entry, rt + rw, part);
-            else
-                moe_gated_tile<TX, GRP, 1, 1, false>(a, entry, rt + rw, part);
+        if constexpr (KIND == MOE_FEW)
+            moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
+        else if (y < a.plan->begin[1])
+            moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
+        else if (y < a.plan->begin[2])
+            moe_more<TX, GRP, 2, GATED>(a, entry, entry_lds);
+        else
+            moe_more<TX, GRP, 1, GATED>(a, entry, entry_lds);
     }
 }
 
-// What a workgroup of the down products keeps in LDS.
-struct MoeLists {
-    float *sums, *weight;  // sums [waves][m][16]
-    uint32_t *entry;
-    uint16_t *row;
-};
-
-// Down products of 16 rows with the entries [e0, e1) of a class.  The tiles of their
-// matrices' 16 rows, one entry after another, are one sequence that the waves
-// share evenly, each with D tiles in flight across the entries' ends; at such an end it adds its
-// weighted products to its own sums [m][16].  No two products of an entry are one token's.
-template <int TX, int GRP, int PK, int D>
-__device__ __forceinline__ void moe_down_stream(const MoeArgs &a, const MoeLists &l, int e0, int e1, int64_t rt,
-                                                int waves)
+// The weighted sum of a token's choices, in their order, and the residual: four columns a thread.
+__global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a)
 {
-    using Wave = Q4gWave<TX, GRP, 1, 1, PK, D>;
-    const Q4gShape sh(a.k, a.n, GRP, a.fmt);
-    const int lane = opaque_lane(), wave = wave_number(), kt = (int)sh.kt;
-    const int64_t tiles = (int64_t)(e1 - e0) * kt;
-    const int64_t f0 = tiles * wave / waves, f1 = tiles * (wave + 1) / waves;
-    if (f0 >= f1)
+    const int64_t j = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int t = blockIdx.y;
+    if (j >= a.k)
         return;
-    float *sums = l.sums + wave * a.m * 16;
-    typename Wave::Rows rows;
-    rows.x = a.h; // 2048 rows of under 2^20 elements: offsets below 2^32
-    rows.part = (int64_t)a.m * a.top * a.n * 2, rows.last = (int)a.n - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
-    Wave w;
-    w.clear();
-    typename Wave::Stage st[D];
-    int le = e0 + (int)(f0 / kt), lt = (int)(f0 % kt), ue = le, ut = lt; // the next tile to load, to use
-    const auto enter = [&]() {
-        const MoeEntry en(__builtin_amdgcn_readfirstlane(l.entry[le]));
-        const int p = Wave::row_of(lane);
-        rows.w[0] = Q4gRows(a.wd + en.expert * a.d_bytes, sh, rt, GRP, a.fmt);
-        rows.at[0] = l.row[en.first + (p < en.count ? p : en.count - 1)] * (uint32_t)a.n * 2;
-    };
-    const auto leave = [&]() {
-        const MoeEntry en(__builtin_amdgcn_readfirstlane(l.entry[ue]));
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int32_t *ids = a.ids + (int64_t)t * a.top;
+    for (int s0 = 0; s0 < a.top; s0 += 8) { // eight choices' loads at once
+        f32x4 p[8];
+        float w[8];
 #pragma unroll
-        for (int i = 0; i < Wave::N; i++) {
-            const int p = Wave::out_of(lane, i);
-            if (p < en.count) {
-                float *to = sums + l.row[en.first + p] / a.top * 16 + lane % 16;
-                *to = fmaf(l.weight[en.first + p], w.y[0][0][i], *to);
-            }
+        for (int b = 0; b < 8; b++) {
+            const int s = s0 + b, id = s < a.top ? ids[s] : -1;
+            int from = s; // the first slot that names it has the product
+            for (int o = s < a.top ? s - 1 : -1; o >= 0; o--)
+                from = ids[o] == id ? o : from;
+            w[b] = 0.0f;
+            if (id >= 0 && id < a.e) {
+                w[b] = a.weights[t * a.top + s];
+                p[b] = *reinterpret_cast<const f32x4 *>(a.out + (int64_t)(t * a.top + from) * a.k + j);
+            } else
+                p[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        w.clear();
-    };
-    int64_t left = f1 - f0; // tiles to load
-    const auto load = [&](typename Wave::Stage &s) {
-        Wave::load(s, rows, lt);
-        if (--left > 0 && ++lt == kt) { // past the end: the last one again
-            lt = 0, le++;
-            enter();
-        }
-    };
-    const auto use = [&](const typename Wave::Stage &s) {
-        w.use(s, rows.bf16, ut);
-        if (++ut == kt) {
-            leave();
-            ut = 0, ue++;
-        }
-    };
-    enter();
 #pragma unroll
-    for (int i = 0; i < D; i++)
-        load(st[i]);
-    int64_t f = f0;
-    for (; f + D < f1; f += D) {
+        for (int b = 0; b < 8; b++)
 #pragma unroll
-        for (int i = 0; i < D; i++) {
-            use(st[i]);
-            __builtin_amdgcn_sched_barrier(0);
-            load(st[i]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int i = 0; i < 4; i++)
+                v[i] = fmaf(w[b], p[b][i], v[i]);
     }
 #pragma unroll
-    for (int i = 0; i < D; i++) {
-        if (f + i < f1)
-            use(st[i]);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < 4; i++) {
+        const float o = a.res ? v[i] + load_as(a.res, t * a.k + j + i, a.dtype) : v[i];
+        store_as(a.y, t * a.k + j + i, o, a.dtype);
     }
-    if (ut > 0)
-        leave();
 }
 
 constexpr int kDownWaves = 16;
 
-// One workgroup for 16 rows, over all entries; the waves' sums are added in order.
-template <int TX, int GRP, bool ONE>
+// One token's down products of 16 rows, weighted and added up.  The pieces of its choices' matrices'
+// rows, one choice after another, are one sequence that the waves share evenly, with
+// loads in flight across the choices' ends; at such an end a wave adds its weighted products.
+template <int TX, int GRP>
 __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
 {
-    extern __shared__ float lds[];
-    const int waves = blockDim.x / 64, pairs = a.m * a.top;
-    MoeLists l;
-    l.sums = lds, l.weight = l.sums + waves * a.m * 16;
-    l.entry = reinterpret_cast<uint32_t *>(l.weight + pairs);
-    for (int i = threadIdx.x; i < waves * a.m * 16; i += blockDim.x)
-        l.sums[i] = 0.0f;
+    using Wave = Q4gWave<TX, GRP, 1, 4, 4>;
+    __shared__ float sums[kDownWaves][16], weights[kMaxTop];
+    __shared__ int expert[kMaxTop], slot[kMaxTop], count;
+    const int waves = blockDim.x / 64, wave = wave_number(), lane = threadIdx.x % 64;
     const int64_t rt = blockIdx.x;
-    if constexpr (ONE) { // the only token's choices are the entries, but for padding
-        l.row = reinterpret_cast<uint16_t *>(l.entry + pairs);
-        const int i = threadIdx.x, id = i < a.top ? a.ids[i] : -1;
+    if (wave == 0) { // the choices but for padding
+        const int id = lane < a.top ? a.ids[lane] : -1;
         const bool in = id >= 0 && id < a.e;
         const uint64_t who = __ballot(in);
         if (in) {
-            const int at = __builtin_popcountll(who & ((1ull << i) - 1));
-            l.entry[at] = MoeEntry::packed(id, at, 1);
-            l.row[at] = (uint16_t)i, l.weight[at] = a.weights[i];
+            const int at = __builtin_popcountll(who & ((1ull << lane) - 1));
+            expert[at] = id, slot[at] = lane, weights[at] = a.weights[lane];
         }
-        __shared__ int count;
-        if (i == 0)
+        if (lane == 0)
             count = __builtin_popcountll(who);
-        __syncthreads();
-        moe_down_stream<TX, GRP, 4, 4>(a, l, 0, count, rt, waves);
-    } else {
-        const int c1 = a.plan->begin[1], c2 = a.plan->begin[2], c3 = a.plan->begin[3];
-        l.row = reinterpret_cast<uint16_t *>(l.entry + c3);
-        for (int i = threadIdx.x; i < c3; i += blockDim.x)
-            l.entry[i] = a.plan->entry[i];
-        for (int i = threadIdx.x; i < pairs; i += blockDim.x)
-            l.row[i] = a.plan->row[i], l.weight[i] = a.plan->weight[i];
-        __syncthreads();
-        moe_down_stream<TX, GRP, 4, 4>(a, l, 0, c1, rt, waves);
-        moe_down_stream<TX, GRP, 2, 2>(a, l, c1, c2, rt, waves);
-        moe_down_stream<TX, GRP, 1, 1>(a, l, c2, c3, rt, waves);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.m * 16; i += blockDim.x) {
-        float v = l.sums[i];
-        for (int o = 1; o < waves; o++)
-            v += l.sums[o * a.m * 16 + i];
-        const int64_t j = rt * 16 + i % 16, at = i / 16 * a.k + j;
-        if (j < a.k) {
-            if (a.res)
-                v += load_as(a.res, at, a.dtype);
-            store_as(a.y, at, v, a.dtype);
+    const Q4gShape sh(a.k, a.n, GRP, a.fmt);
+    const int ks = (int)sh.ks, pieces = __builtin_amdgcn_readfirstlane(count) * ks; // below 2^5 * 2^11
+    const int f0 = pieces * wave / waves, f1 = pieces * (wave + 1) / waves;
+    float sum = 0.0f;
+    if (f0 < f1) {
+        const bool bf16 = a.fmt & kQ4gBf16;
+        typename Wave::From f;
+        f.x = a.h, f.part = (int64_t)a.top * a.n * 2, f.last = (int)a.n - 32, f.kt = (int)sh.kt;
+        const auto enter = [&](int choice) {
+            f.w[0] = Q4gRows(a.wd + __builtin_amdgcn_readfirstlane(expert[choice]) * a.d_bytes, sh, rt, GRP, a.fmt);
+            f.at = (uint32_t)slot[choice] * (uint32_t)a.n * 2;
+        };
+        int choice = f0 / ks, p = f0 % ks;
+        Wave w;
+        w.clear();
+        enter(choice);
+        w.start(f, p, lane);
+        for (int i = f0; i < f1; i++) {
+            const bool end = p + 1 == ks;
+            const int after = end ? 0 : p + 1;
+            if (i + 1 < f1) {
+                if (end)
+                    enter(choice + 1);
+                w.template use_piece<true>(f, p, f, after, bf16, lane); // four tiles in flight: f is the next one's
+            } else
+                w.template use_piece<false>(f, p, f, 0, bf16, lane);
+            if (end || i + 1 == f1) {
+                sum = fmaf(weights[choice], w.y[0][0][0], sum);
+                w.clear();
+                choice++;
+            }
+            p = after;
         }
+    }
+    if (lane < 16)
+        sums[wave][lane] = sum;
+    __syncthreads();
+    const int64_t j = rt * 16 + threadIdx.x;
+    if (threadIdx.x < 16 && j < a.k) {
+        float v = sums[0][lane];
+        for (int o = 1; o < waves; o++)
+            v += sums[o][lane];
+        if (a.res)
+            v += load_as(a.res, j, a.dtype);
+        store_as(a.y, j, v, a.dtype);
     }
 }
 
-template <int TX, int GRP, bool ONE>
-hipError_t experts(MoeArgs a, hipStream_t s)
+// Room for the down products of each choice, and before them for f32 rows as parts: up to 32768
+// columns, 32 MiB at most.
+int64_t moe_out_bytes(int64_t m, int64_t top)
 {
-    const int64_t pairs = (int64_t)a.m * a.top, active = pairs < a.e ? pairs : a.e;
-    const int64_t rt = (a.n + 15) / 16, kt = (a.k + 127) / 128, dt = (a.k + 15) / 16, nt = (a.n + 127) / 128;
-    a.kw = 1;
-    while (a.kw < 8 && rt * active * a.kw < 4096 && 2 * a.kw <= kt)
+    const int64_t all = m == 1 ? 0 : m * top * 32768 * (int64_t)sizeof(float);
+    return all < (int64_t)32 << 20 ? all : (int64_t)32 << 20;
+}
+
+// Tokens that go at once: 64, or as many as have that room; one needs none.
+int64_t moe_group(int64_t m, int64_t top, int64_t k)
+{
+    const int64_t tokens = m < kMoeTokens ? m : kMoeTokens, room = moe_out_bytes(tokens, top);
+    const int64_t each = k * (int64_t)sizeof(float) * (top < 2 ? 2 : top); // 4 bytes a choice, 6 for a row's parts
+    return room / each < 2 ? 1 : room / each < tokens ? room / each : tokens;
+}
+
+// Entries' products as one launch of up to some 1024 workgroups.
+template <int TX, int GRP, bool GATED, int KIND>
+hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
+{
+    const int64_t outs = GATED ? a.n : a.k, k = GATED ? a.k : a.n, ks = (k + 511) / 512, tiles = (outs + 15) / 16;
+    a.kw = 1; // waves along k, at most: a class whose chunks have fewer pieces takes fewer
+    while (a.kw < 8 && 2 * a.kw <= ks && tiles * active * a.kw < (GATED ? 2048 : 4096))
         a.kw *= 2;
-    const int64_t most = (rt * a.kw + 7) / 8, want = (1024 + active - 1) / active;
-    const int64_t entries = ONE ? pairs : active + pairs / 16; // at most
-    moe_gated_kernel<TX, GRP, ONE><<<dim3((unsigned)(most < want ? most : want), (unsigned)entries), 512,
-                                    a.kw > 1 ? (size_t)8 * 2 * 4 * 64 * sizeof(float) : 0, s>>>(a);
-    hipError_t e = hipGetLastError();
+    const int64_t most = (tiles * a.kw + 7) / 8, want = (1024 + active - 1) / active;
+    int64_t lds = (GATED ? 2 : 1) * 8 * 64 * sizeof(float);
+    if constexpr (KIND == MOE_ALL) { // whichever of the classes takes most
+        using B2 = Q4gBlock<TX, GRP, 1, 1, 2, 4>;
+        using B1 = Q4gBlock<TX, GRP, 1, 1, 1, 4>;
+        lds = 4 * lds + (a.m <= 8 || B2::lds_bytes(k) > B1::lds_bytes(k) ? B2::lds_bytes(k) : B1::lds_bytes(k));
+    }
+    moe_entry_kernel<TX, GRP, GATED, KIND><<<dim3((unsigned)(most < want ? most : want), (unsigned)count), 512,
+                                            (size_t)lds, s>>>(a);
+    return hipGetLastError();
+}
+
+// TX: the rows as the kernels take them, which for more than four f32 rows is as parts.
+template <int TX, int GRP, int KIND>
+hipError_t experts(const MoeArgs &a, hipStream_t s)
+{
+    constexpr int TH = TX == Q4G_X_F32 || TX == Q4G_X_PARTS3 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
+    const int64_t pairs = (int64_t)a.m * a.top, active = pairs < a.e ? pairs : a.e;
+    const int64_t count = KIND == MOE_ONE ? pairs : active + pairs / 16; // of entries, at most
+    hipError_t e = entries<TX, GRP, true, KIND>(a, active, count, s);
     if (e != hipSuccess)
         return e;
-    const int64_t most_waves = a.m > 32 ? 8 : kDownWaves, waves = active * nt < most_waves ? active * nt : most_waves;
-    const size_t lds = (size_t)waves * a.m * 64 + pairs * 6 + entries * 4;
-    constexpr int TH = TX == Q4G_X_F32 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
-    moe_down_kernel<TH, GRP, ONE><<<(unsigned)dt, (unsigned)(64 * waves), lds, s>>>(a);
+    if constexpr (KIND == MOE_ONE) {
+        const int64_t dt = (a.k + 15) / 16, pieces = active * ((a.n + 511) / 512), waves = pieces < kDownWaves ? pieces : kDownWaves;
+        moe_down_kernel<TH, GRP><<<(unsigned)dt, (unsigned)(64 * waves), 0, s>>>(a);
+    } else {
+        e = entries<TH, GRP, false, KIND>(a, active, count, s);
+        if (e != hipSuccess)
+            return e;
+        moe_combine_kernel<<<dim3((unsigned)((a.k + 1023) / 1024), (unsigned)a.m), 256, 0, s>>>(a);
+    }
     return hipGetLastError();
+}
+
+template <int TX, int GRP>
+hipError_t experts_k(const MoeArgs &a, hipStream_t s)
+{
+    if (a.m == 1)
+        return experts<TX, GRP, MOE_ONE>(a, s);
+    if (a.m <= 4)
+        return experts<TX, GRP, MOE_FEW>(a, s);
+    if constexpr (TX == Q4G_X_F32) {
+        const hipError_t e = launch_q4g_split(a.x, a.x_parts, a.m * a.k, s);
+        return e != hipSuccess ? e : experts<Q4G_X_PARTS3, GRP, MOE_ALL>(a, s);
+    } else
+        return experts<TX, GRP, MOE_ALL>(a, s);
 }
 
 template <int TX>
 hipError_t experts_g(const MoeArgs &a, int64_t group, hipStream_t s)
 {
-    if (a.m == 1)
-        return group == 32 ? experts<TX, 32, true>(a, s) : group == 64 ? experts<TX, 64, true>(a, s) : experts<TX, 128, true>(a, s);
-    moe_plan_kernel<<<1, 1024, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    return group == 32 ? experts<TX, 32, false>(a, s) : group == 64 ? experts<TX, 64, false>(a, s) : experts<TX, 128, false>(a, s);
+    if (a.m > 1) {
+        moe_plan_kernel<<<1, 1024, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return group == 32 ? experts_k<TX, 32>(a, s) : group == 64 ? experts_k<TX, 64>(a, s) : experts_k<TX, 128>(a, s);
 }
 
 } // namespace
@@ -682,13 +769,13 @@ hipError_t launch_moe_route(const void *x, int dtype, const void *w, int w_dtype
     return choose(l, bias, sigmoid, renorm, scale, ids, weights, top, m, e, s);
 }
 
-// Groups of 64 tokens, one after another, in the same workspace: the plan, then h.
+// Groups of tokens, one after another, in the same workspace: the plan, the down products, h.
 constexpr size_t kMoePlanBytes = (sizeof(MoePlan) + 255) / 256 * 256;
 
 size_t q4g_moe_workspace(int64_t m, int64_t n, int64_t top)
 {
     const int64_t tokens = m < kMoeTokens ? m : kMoeTokens;
-    return kMoePlanBytes + ((size_t)(tokens * top * n) * 6 + 255) / 256 * 256;
+    return kMoePlanBytes + (size_t)moe_out_bytes(tokens, top) + ((size_t)(tokens * top * n) * 6 + 255) / 256 * 256;
 }
 
 hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top,
@@ -696,7 +783,8 @@ hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const fl
                           const void *res, void *y, int64_t m, int64_t n, int64_t k, int64_t e, void *ws, hipStream_t s)
 {
     const int64_t row = k * (dtype == QLL_W_F32 ? 4 : 2);
-    for (int64_t t0 = 0; t0 < m; t0 += kMoeTokens) {
+    const int64_t group_of = moe_group(m, top, k), room = moe_out_bytes(m < kMoeTokens ? m : kMoeTokens, top);
+    for (int64_t t0 = 0; t0 < m; t0 += group_of) {
         MoeArgs a{};
         a.wg = wg, a.wu = wu, a.wd = wd;
         a.x = static_cast<const uint8_t *>(x) + t0 * row;
@@ -706,8 +794,10 @@ hipError_t launch_q4g_moe(const void *x, int dtype, const int32_t *ids, const fl
         a.plan = static_cast<MoePlan *>(ws);
         a.n = n, a.k = k;
         a.gu_bytes = q4g_packed_bytes(n, k, group, fmt), a.d_bytes = q4g_packed_bytes(k, n, group, fmt);
-        a.m = (int)(m - t0 < kMoeTokens ? m - t0 : kMoeTokens), a.top = (int)top, a.e = (int)e;
-        a.h = static_cast<uint8_t *>(ws) + kMoePlanBytes;
+        a.m = (int)(m - t0 < group_of ? m - t0 : group_of), a.top = (int)top, a.e = (int)e;
+        a.out = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMoePlanBytes);
+        a.x_parts = reinterpret_cast<uint8_t *>(a.out);
+        a.h = a.x_parts + room;
         a.fmt = fmt, a.act = act, a.dtype = dtype;
         const hipError_t rc = dtype == QLL_W_F32    ? experts_g<Q4G_X_F32>(a, group, s)
                               : dtype == QLL_W_BF16 ? experts_g<Q4G_X_BF16>(a, group, s)

@@ -120,64 +120,45 @@ struct Q4gLinear {
     const float *bias;
     const void *res;
     void *y;
-    int64_t m, n, k, row0, tok0; // row0, tok0: this launch's first group of row tiles, first activation row
+    float *part; // sums of parts of k, [part][m][n]
+    int64_t m, n, k, row0, tok0; // row0, tok0: this launch's first workgroup of row tiles, first activation row
     int fmt, act, y_dtype;
-    int kw, rw, tok_groups; // waves along k and along rows of a workgroup; groups of 16 C activation rows
+    int kw, parts, tok_groups; // waves along k of a workgroup, workgroups along k, groups of activation rows
 };
 
-// kw waves share RTN row tiles, each a part of k, and add up in LDS; rw such
-// sets a workgroup.  Workgroups eight apart land on the same XCD: those of one set of
-// rows follow each other there, so that its weights stay in that L2.
-template <int TX, int GRP, int RTN, int C, int PK, int D>
-__global__ void __launch_bounds__(512) q4g_linear_kernel(Q4gLinear a)
+// The sums of a workgroup's waves: RTN row tiles and C column groups each, sets of kw waves adding up
+// in LDS; then the epilogue, or a part of k as it is.
+template <int RTN, int C, int N>
+__device__ __forceinline__ void q4g_outputs(const Q4gLinear &a, const float (&y)[RTN][C][N], int64_t rt0, int64_t tok0,
+                                            float *sums, int lane)
 {
-    using Wave = Q4gWave<TX, GRP, RTN, C, PK, D>;
-    constexpr int kTokens = 16 / PK; // of a column group
-    extern __shared__ float part[];  // [rw][kw][RTN * C * N][64]
-    const Q4gShape sh(a.n, a.k, GRP, a.fmt);
-    const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw, rw = wave / a.kw;
-    const int64_t b = blockIdx.x, tg = b / 8 % a.tok_groups, rg = b / 8 / a.tok_groups * 8 + b % 8;
-    const int64_t rt0 = (a.row0 + rg * a.rw + rw) * RTN;
-    const int64_t tok0 = a.tok0 + tg * kTokens * C;
-    Wave w;
-    w.clear();
-    if (rt0 < sh.rt) {
-        typename Wave::Rows rows;
-#pragma unroll
-        for (int r = 0; r < RTN; r++) // past the last tile: the last one again, not stored
-            rows.w[r] = Q4gRows(a.wp, sh, rt0 + r < sh.rt ? rt0 + r : sh.rt - 1, GRP, a.fmt);
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-            int64_t t = kTokens * c + Wave::row_of(lane);
-            t = tok0 + t < a.m ? t : a.m - 1 - tok0; // rows past the last: its values again, not stored
-            rows.at[c] = (uint32_t)(t * a.k * q4g_x_size(TX)); // 32 rows of f32, 64 of 16 bits: below 2^32
-        }
-        rows.x = static_cast<const uint8_t *>(a.x) + tok0 * a.k * q4g_x_size(TX);
-        rows.part = 0, rows.last = (int)a.k - 32, rows.bf16 = a.fmt & kQ4gBf16, rows.lane = lane;
-        const int kt = (int)sh.kt, per = (kt + a.kw - 1) / a.kw, t0 = kw * per, t1 = t0 + per < kt ? t0 + per : kt;
-        w.run(rows, t0, t1);
-    }
-    constexpr int kOuts = RTN * C * Wave::N;
+    constexpr int kOuts = RTN * C * N, kTokens = 4 * N; // kTokens: of a column group
+    const int wave = wave_number(), kw = wave % a.kw, set = wave - kw;
     if (a.kw > 1) {
+        __syncthreads(); // LDS is read
 #pragma unroll
         for (int o = 0; o < kOuts; o++)
-            part[(wave * kOuts + o) * 64 + lane] = w.y[o / (C * Wave::N)][o / Wave::N % C][o % Wave::N];
+            sums[(wave * kOuts + o) * 64 + lane] = y[o / (C * N)][o / N % C][o % N];
         __syncthreads();
     }
 #pragma unroll
     for (int o = 0; o < kOuts; o++) {
-        if (o % a.kw != kw) // the set's waves take turns
+        if (a.kw > 1 && o % a.kw != kw) // the set's waves take turns
             continue;
-        const int r = o / (C * Wave::N), c = o / Wave::N % C, i = o % Wave::N;
-        float v = w.y[r][c][i];
+        const int r = o / (C * N), c = o / N % C, i = o % N;
+        float v = y[r][c][i];
         if (a.kw > 1) {
-            v = part[(rw * a.kw * kOuts + o) * 64 + lane];
+            v = sums[(set * kOuts + o) * 64 + lane];
             for (int p = 1; p < a.kw; p++)
-                v += part[((rw * a.kw + p) * kOuts + o) * 64 + lane];
+                v += sums[((set + p) * kOuts + o) * 64 + lane];
         }
-        const int64_t j = (rt0 + r) * 16 + lane % 16, t = tok0 + kTokens * c + Wave::out_of(lane, i);
+        const int64_t j = (rt0 + r) * 16 + lane % 16, t = tok0 + kTokens * c + lane / 16 * N + i;
         if (j >= a.n || t >= a.m)
             continue;
+        if (a.parts > 1) {
+            a.part[(blockIdx.y * a.m + t) * a.n + j] = v;
+            continue;
+        }
         v = activate(a.bias ? v + a.bias[j] : v, a.act);
         if (a.res)
             v += load_as(a.res, t * a.n + j, a.y_dtype);
@@ -185,53 +166,219 @@ __global__ void __launch_bounds__(512) q4g_linear_kernel(Q4gLinear a)
     }
 }
 
-template <int TX, int GRP, int RTN, int C, int PK, int D>
-hipError_t linear_c(Q4gLinear a, int kw, int rw, hipStream_t s)
+// Few activation rows, or a small product: the waves of a set share its row tile's pieces of k;
+// groups of 16 / PK activation rows along y.
+template <int TX, int GRP, int PK, int D>
+__global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 {
-    constexpr int kTokens = 16 / PK * C; // of a workgroup
-    a.kw = kw, a.rw = rw;
-    const int64_t sets = ((a.n + 15) / 16 + RTN * rw - 1) / (RTN * rw), threads = 64 * kw * rw;
-    const size_t lds = kw > 1 ? (size_t)rw * kw * RTN * C * (4 / PK) * 64 * sizeof(float) : 0;
-    const int64_t groups = (a.m + kTokens - 1) / kTokens;
+    using Wave = Q4gWave<TX, GRP, 1, PK, D>;
+    extern __shared__ float few_sums[]; // [8][N][64]
+    const Q4gShape sh(a.n, a.k, GRP, a.fmt);
+    const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
+    const int64_t rt = (a.row0 + blockIdx.x) * (8 / a.kw) + wave / a.kw, tok0 = a.tok0 + (int64_t)blockIdx.y * (16 / PK);
+    Wave w;
+    w.clear();
+    if (rt < sh.rt) {
+        typename Wave::From f;
+        const int64_t rows = a.m - tok0; // past the last row: its values again
+        const uint32_t row = Wave::row_of(lane) < rows ? Wave::row_of(lane) : (uint32_t)rows - 1;
+        f.w[0] = Q4gRows(a.wp, sh, rt, GRP, a.fmt);
+        f.x = static_cast<const uint8_t *>(a.x) + tok0 * a.k * q4g_x_size(TX), f.at = row * (uint32_t)a.k * q4g_x_size(TX);
+        f.part = 0, f.last = (int)a.k - 32, f.kt = (int)sh.kt;
+        const int ks = (int)sh.ks, per = (ks + a.kw - 1) / a.kw, p0 = kw * per;
+        w.run(f, p0, p0 + per < ks ? p0 + per : ks, a.fmt & kQ4gBf16, lane);
+    }
+    q4g_outputs(a, w.y, rt, tok0, few_sums, lane);
+}
+
+// More rows.  Workgroups eight apart land on the same XCD: those of one set of rows follow
+// each other there, so that its weights stay in that L2.
+template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
+__global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
+{
+    using Block = Q4gBlock<TX, GRP, RTN, C, PK, D>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const Q4gShape sh(a.n, a.k, GRP, a.fmt);
+    const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
+    const int64_t b = blockIdx.x, tg = b / 8 % a.tok_groups, rg = b / 8 / a.tok_groups * 8 + b % 8;
+    const int64_t rt0 = ((a.row0 + rg) * (8 / a.kw) + wave / a.kw) * RTN;
+    const int64_t tok0 = a.tok0 + tg * Block::T;
+    typename Block::X src;
+    src.base = static_cast<const uint8_t *>(a.x) + tok0 * a.k * 2;
+    src.part = a.m * a.k * 2, src.k = (int)a.k;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        const int row = 16 / PK * c + Block::row_of(lane);
+        src.at[c] = tok0 + row < a.m ? (uint32_t)row * (uint32_t)a.k * 2 : ~0u; // 64 rows: below 2^32 bytes
+    }
+    Q4gRows rows[RTN];
+#pragma unroll
+    for (int r = 0; r < RTN; r++) // past the last tile: the last one again, not stored
+        rows[r] = Q4gRows(a.wp, sh, rt0 + r < sh.rt ? rt0 + r : sh.rt - 1, GRP, a.fmt);
+    const int chunks = (int)((a.k + Block::kChunk - 1) / Block::kChunk), per = (chunks + a.parts - 1) / a.parts;
+    const int x0 = blockIdx.y * per, x1 = x0 + per < chunks ? x0 + per : chunks;
+    Block w;
+    w.clear();
+    if (x0 < x1)
+        w.run(rows, rt0 < sh.rt, src, x0, x1, kw, a.kw, a.fmt & kQ4gBf16, false, lds, lane);
+    q4g_outputs(a, w.y, rt0, tok0, reinterpret_cast<float *>(lds), lane);
+}
+
+// The parts of k added up in order, and the epilogue.
+__global__ void __launch_bounds__(256) q4g_finish_kernel(Q4gLinear a, int64_t first, int64_t count)
+{
+    const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= first + count)
+        return;
+    float v = a.part[i];
+    for (int p = 1; p < a.parts; p++)
+        v += a.part[p * a.m * a.n + i];
+    v = activate(a.bias ? v + a.bias[i % a.n] : v, a.act);
+    if (a.res)
+        v += load_as(a.res, i, a.y_dtype);
+    store_as(a.y, i, v, a.y_dtype);
+}
+
+// f32 rows as three bf16 parts [part][count], eight values a thread.
+__global__ void __launch_bounds__(256) q4g_split_kernel(const uint8_t *x, uint8_t *parts, int64_t first, int64_t eights,
+                                                        int64_t count)
+{
+    const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= eights)
+        return;
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(x + i * 32);
+    u32x4 a, b, c;
+    split3(from[0], from[1], a, b, c);
+    *reinterpret_cast<u32x4 *>(parts + i * 16) = a;
+    *reinterpret_cast<u32x4 *>(parts + count * 2 + i * 16) = b;
+    *reinterpret_cast<u32x4 *>(parts + count * 4 + i * 16) = c;
+}
+
+// Whether a product takes the waves that fetch their own activations, in one launch and without a
+// workspace: up to four rows, or so little work that launches and idle CUs count for more.
+bool q4g_small(int64_t m, int64_t n, int64_t k)
+{
+    return m <= 4 || (m <= 64 && (m + 15) / 16 * n * k <= (int64_t)1 << 25);
+}
+
+// How another product is split: T activation rows and `tiles` row tiles a wave, kw
+// waves and `parts` workgroups along k.
+struct Q4gSplit {
+    int rows, tiles, kw, parts;
+};
+
+// Up to 16 rows (8 as well, PK = 2) the weights are read once, and the work is split along k until some 4096
+// waves share it, along workgroups too.
+Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
+{
+    const int64_t rt = (n + 15) / 16, ks = (k + 511) / 512;
+    Q4gSplit s{m <= 8 ? 8 : 16, 1, 1, 1};
+    if (m > 16) {
+        s.tiles = 2;
+        if (!wide)
+            s.rows = m <= 32 ? 32 : 64;
+    }
+    const int64_t base = 16384 / (s.rows * (wide ? 3 : 1)) / 512 * 512, chunk = base < 512 ? 512 : base;
+    const int64_t pieces = chunk / 512, chunks = (k + chunk - 1) / chunk;
+    const int64_t sets = (rt + s.tiles - 1) / s.tiles * ((m + s.rows - 1) / s.rows);
+    while (2 * s.kw <= pieces && 2 * s.kw <= ks && sets * s.kw < 4096)
+        s.kw *= 2;
+    while (2 * s.parts <= chunks && s.parts < 8 && sets * s.kw * s.parts < 4096)
+        s.parts *= 2;
+    return s;
+}
+
+size_t part_bytes(const Q4gSplit &s, int64_t m, int64_t n)
+{
+    return s.parts > 1 ? ((size_t)s.parts * m * n * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+template <int TX, int GRP, int PK, int D>
+hipError_t linear_few(Q4gLinear a, hipStream_t s)
+{
+    const int64_t rt = (a.n + 15) / 16, ks = (a.k + 511) / 512, groups = (a.m + 16 / PK - 1) / (16 / PK);
+    a.kw = 1;
+    while (a.kw < 8 && 2 * a.kw <= ks && rt * groups * a.kw < 4096)
+        a.kw *= 2;
     hipError_t e = hipSuccess;
     for (int64_t g0 = 0; g0 < groups && e == hipSuccess; g0 += 1 << 12) {
         const int64_t gn = groups - g0 < 1 << 12 ? groups - g0 : 1 << 12;
-        a.tok0 = g0 * kTokens, a.tok_groups = (int)gn;
-        // parts of eight sets, so that only the last one's grid reaches past its rows
-        e = launch_parts(sets, kPartThreads / (threads * gn) / 8 * 8, [&](int64_t first, int64_t count) {
-            a.row0 = first * rw;
-            const int64_t blocks = (count + 7) / 8 * 8 * gn;
-            q4g_linear_kernel<TX, GRP, RTN, C, PK, D><<<(unsigned)blocks, (unsigned)threads, lds, s>>>(a);
+        a.tok0 = g0 * (16 / PK);
+        e = launch_parts((rt * a.kw + 7) / 8, kPartThreads / 512, [&](int64_t first, int64_t count) {
+            a.row0 = first;
+            q4g_few_kernel<TX, GRP, PK, D><<<dim3((unsigned)count, (unsigned)gn), 512,
+                                            a.kw > 1 ? 8 * (4 / PK) * 64 * sizeof(float) : 0, s>>>(a);
         });
     }
     return e;
 }
 
-template <int TX, int GRP>
-hipError_t linear_x(const Q4gLinear &a, hipStream_t s)
+template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
+hipError_t linear_c(Q4gLinear a, const Q4gSplit &split, hipStream_t s)
 {
-    const int64_t rt = (a.n + 15) / 16, kt = (a.k + 127) / 128;
-    auto split = [&](int64_t sets) { // waves along k: enough to fill the chip, two tiles each at least
-        int kw = 1;
-        while (kw < 8 && sets * kw < 4096 && 2 * kw <= kt)
-            kw *= 2;
-        return kw;
-    };
-    const int kw1 = split(rt), rw1 = kw1 < 4 ? 4 / kw1 : 1;
-    if (a.m <= 4)
-        return linear_c<TX, GRP, 1, 1, 4, 4>(a, kw1, rw1, s);
-    if (a.m <= 8)
-        return linear_c<TX, GRP, 1, 1, 2, 4>(a, kw1, rw1, s);
-    if (a.m <= 16)
-        return linear_c<TX, GRP, 1, 1, 1, 2>(a, kw1, rw1, s);
-    const int kw = split((rt + 1) / 2 * ((a.m + 31) / 32));
-    return linear_c<TX, GRP, 2, 2, 1, 1>(a, kw, kw < 4 ? 4 / kw : 1, s);
+    using Block = Q4gBlock<TX, GRP, RTN, C, PK, D>;
+    a.kw = split.kw, a.parts = split.parts;
+    const int64_t sets = ((a.n + 15) / 16 + RTN * (8 / a.kw) - 1) / (RTN * (8 / a.kw)), threads = 512;
+    const size_t sums = a.kw > 1 ? (size_t)8 * RTN * C * Block::N * 64 * sizeof(float) : 0;
+    const size_t x = Block::lds_bytes(a.k), lds = x > sums ? x : sums;
+    const int64_t groups = (a.m + Block::T - 1) / Block::T;
+    hipError_t e = hipSuccess;
+    for (int64_t g0 = 0; g0 < groups && e == hipSuccess; g0 += 1 << 12) {
+        const int64_t gn = groups - g0 < 1 << 12 ? groups - g0 : 1 << 12;
+        a.tok0 = g0 * Block::T, a.tok_groups = (int)gn;
+        // parts of eight sets, so that only the last one's grid reaches past its rows
+        e = launch_parts(sets, kPartThreads / (threads * gn) / 8 * 8, [&](int64_t first, int64_t count) {
+            a.row0 = first;
+            const dim3 grid((unsigned)((count + 7) / 8 * 8 * gn), (unsigned)a.parts);
+            q4g_linear_kernel<TX, GRP, RTN, C, PK, D, WPS><<<grid, (unsigned)threads, lds, s>>>(a);
+        });
+    }
+    if (e != hipSuccess || a.parts == 1)
+        return e;
+    return launch_parts(a.m * a.n, kPartThreads, [&](int64_t first, int64_t count) {
+        q4g_finish_kernel<<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a, first, count);
+    });
 }
 
-template <int TX>
-hipError_t linear_g(const Q4gLinear &a, int64_t group, hipStream_t s)
+template <int TX, int GRP>
+hipError_t linear_more(const Q4gLinear &a, const Q4gSplit &split, hipStream_t s)
 {
-    return group == 32 ? linear_x<TX, 32>(a, s) : group == 64 ? linear_x<TX, 64>(a, s) : linear_x<TX, 128>(a, s);
+    if (split.rows == 8)
+        return linear_c<TX, GRP, 1, 1, 2, 4, 4>(a, split, s);
+    if (split.tiles == 1)
+        return linear_c<TX, GRP, 1, 1, 1, 4, 4>(a, split, s);
+    if constexpr (TX == Q4G_X_PARTS3)
+        return linear_c<TX, GRP, 2, 1, 1, 4, 2>(a, split, s);
+    else
+        return split.rows == 32 ? linear_c<TX, GRP, 2, 2, 1, 2, 2>(a, split, s)
+                                : linear_c<TX, GRP, 2, 4, 1, 2, 2>(a, split, s);
+}
+
+template <int TX, int GRP>
+hipError_t linear_small(const Q4gLinear &a, hipStream_t s)
+{
+    return a.m <= 4   ? linear_few<TX, GRP, 4, 4>(a, s)
+           : a.m <= 8 ? linear_few<TX, GRP, 2, 2>(a, s)
+                      : linear_few<TX, GRP, 1, TX == Q4G_X_F32 ? 1 : 2>(a, s);
+}
+
+template <int GRP>
+hipError_t linear_g(Q4gLinear a, int dtype, uint8_t *ws, hipStream_t s)
+{
+    if (q4g_small(a.m, a.n, a.k))
+        return dtype == QLL_W_F32    ? linear_small<Q4G_X_F32, GRP>(a, s)
+               : dtype == QLL_W_BF16 ? linear_small<Q4G_X_BF16, GRP>(a, s)
+                                     : linear_small<Q4G_X_F16, GRP>(a, s);
+    const Q4gSplit split = q4g_split(dtype == QLL_W_F32, a.m, a.n, a.k);
+    a.part = reinterpret_cast<float *>(ws);
+    if (dtype != QLL_W_F32)
+        return dtype == QLL_W_BF16 ? linear_more<Q4G_X_BF16, GRP>(a, split, s) : linear_more<Q4G_X_F16, GRP>(a, split, s);
+    uint8_t *parts = ws + part_bytes(split, a.m, a.n);
+    const hipError_t e = launch_q4g_split(a.x, parts, a.m * a.k, s);
+    if (e != hipSuccess)
+        return e;
+    a.x = parts;
+    return linear_more<Q4G_X_PARTS3, GRP>(a, split, s);
 }
 
 } // namespace
@@ -249,14 +396,32 @@ hipError_t launch_q4g_from_q4_0(const uint8_t *w, uint8_t *wp, int64_t n, int64_
     return pack(CodeBlocks{w}, ScaleBlocks{w}, 32, 0, wp, n, k, s);
 }
 
+hipError_t launch_q4g_split(const void *x, void *parts, int64_t count, hipStream_t s)
+{
+    return launch_parts(count / 8, kPartThreads, [&](int64_t first, int64_t n) {
+        q4g_split_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<const uint8_t *>(x),
+                                                                    static_cast<uint8_t *>(parts), first, count / 8, count);
+    });
+}
+
+size_t q4g_linear_workspace(int64_t m, int64_t n, int64_t k)
+{
+    if (q4g_small(m, n, k))
+        return 0;
+    const size_t a = part_bytes(q4g_split(false, m, n, k), m, n), b = part_bytes(q4g_split(true, m, n, k), m, n) + (size_t)(m * k) * 6;
+    return a > b ? a : b;
+}
+
 hipError_t launch_q4g_linear(const uint8_t *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias,
-                             int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k,
+                             int act, const void *res, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
                              hipStream_t s)
 {
-    const Q4gLinear a{wp, x, bias, res, y, m, n, k, 0, 0, fmt, act, y_dtype, 1, 1, 1};
-    return dtype == QLL_W_F32    ? linear_g<Q4G_X_F32>(a, group, s)
-           : dtype == QLL_W_BF16 ? linear_g<Q4G_X_BF16>(a, group, s)
-                                 : linear_g<Q4G_X_F16>(a, group, s);
+    Q4gLinear a{};
+    a.wp = wp, a.x = x, a.bias = bias, a.res = res, a.y = y;
+    a.m = m, a.n = n, a.k = k, a.fmt = fmt, a.act = act, a.y_dtype = y_dtype;
+    a.kw = a.parts = a.tok_groups = 1;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    return group == 32 ? linear_g<32>(a, dtype, w, s) : group == 64 ? linear_g<64>(a, dtype, w, s) : linear_g<128>(a, dtype, w, s);
 }
 
 } // namespace qll
