@@ -291,11 +291,12 @@ hipError_t top_e(const double *l, const float *bias, int sigmoid, int renorm, fl
 
 constexpr int kMoeTokens = 64; // at most, in one go
 constexpr int kMoePairs = kMoeTokens * (int)kMaxTop;
-constexpr int kMoeEntries = (int)kMaxExperts + kMoePairs / 16;
+constexpr int kMoeEntries = (int)kMaxExperts + kMoePairs / 8;
 
 // Who chose whom, for a group of at most 64 tokens.  An entry is up to 4, 8 or 16 tokens of
 // an expert (class 0, 1, 2): an expert with at most four tokens is one entry of class 0, up to eight
-// one of class 1, more of them entries of sixteen.  begin[c] is class c's first entry,
+// one of class 1, more of them entries of sixteen (of eight, class 1, where rows come as three
+// parts: sixteen such rows take the LDS of two workgroups).  begin[c] is class c's first entry,
 // begin[3] their number; entries stand in ascending order of the experts within
 // a class.  A token that names an expert twice counts once, with the sum of its weights.
 struct MoePlan {
@@ -339,7 +340,7 @@ struct MoeArgs {
 };
 
 // One workgroup makes the plan; threads are experts, then pairs.
-__device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weights, int m, int top, int e, MoePlan &plan)
+__device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weights, int m, int top, int e, bool wide, MoePlan &plan)
 {
     __shared__ unsigned long long chose[kMaxExperts]; // tokens that named it
     __shared__ unsigned long long sums[16];
@@ -356,7 +357,7 @@ __device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weight
     }
     __syncthreads();
     const int count = __builtin_popcountll(chose[tid]);
-    const int cls = count <= 4 ? 0 : count <= 8 ? 1 : 2, entries = cls < 2 ? count > 0 : (count + 15) / 16;
+    const int cls = count <= 4 ? 0 : count <= 8 || wide ? 1 : 2, most = 4 << cls, entries = (count + most - 1) / most;
     // running sums of the pairs and of each class's entries, 16 bits each
     const uint64_t own = (uint64_t)count | (uint64_t)entries << (16 * (cls + 1));
     uint64_t upto = own;
@@ -381,7 +382,7 @@ __device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weight
     first[tid] = (uint16_t)before;
     const int at = (int)(before >> (16 * (cls + 1)) & 0xffff) + (cls == 0 ? 0 : cls == 1 ? c0 : c0 + c1);
     for (int i = 0; i < entries; i++)
-        plan.entry[at + i] = MoeEntry::packed(tid, (int)(before & 0xffff) + 16 * i, min(count - 16 * i, 16));
+        plan.entry[at + i] = MoeEntry::packed(tid, (int)(before & 0xffff) + most * i, min(count - most * i, most));
     __syncthreads();
     for (int i = tid; i < m * top; i += 1024) {
         const int v = id[i], t = i / top;
@@ -399,7 +400,7 @@ __device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weight
     }
 }
 
-__global__ void __launch_bounds__(1024) moe_plan_kernel(MoeArgs a) { moe_plan(a.ids, a.weights, a.m, a.top, a.e, *a.plan); }
+__global__ void __launch_bounds__(1024) moe_plan_kernel(MoeArgs a) { moe_plan(a.ids, a.weights, a.m, a.top, a.e, a.dtype == QLL_W_F32, *a.plan); }
 
 __device__ __forceinline__ void store_part(uint8_t *h, int64_t at, float v)
 {
@@ -547,11 +548,14 @@ __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
         const MoeEntry entry(__builtin_amdgcn_readfirstlane(a.plan->entry[y]));
         if constexpr (KIND == MOE_FEW)
             moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
-        else if (y < a.plan->begin[1])
-            moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
-        else if (y < a.plan->begin[2])
+        else if (y < a.plan->begin[1]) {
+            if constexpr (TX == Q4G_X_PARTS3) // three operands a quad
+                moe_more<TX, GRP, 4, GATED>(a, entry, entry_lds);
+            else
+                moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
+        } else if (y < a.plan->begin[2])
             moe_more<TX, GRP, 2, GATED>(a, entry, entry_lds);
-        else
+        else if constexpr (TX != Q4G_X_PARTS3)
             moe_more<TX, GRP, 1, GATED>(a, entry, entry_lds);
     }
 }
@@ -559,27 +563,24 @@ __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
 // The weighted sum of a token's choices, in their order, and the residual: four columns a thread.
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a)
 {
-    const int64_t j = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t column = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, j = column < a.k ? column : 0; // whole waves stay
     const int t = blockIdx.y;
-    if (j >= a.k)
-        return;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int32_t *ids = a.ids + (int64_t)t * a.top;
+    const int slot = threadIdx.x % 64; // a lane holds a choice
+    const int id = slot < a.top ? a.ids[t * a.top + slot] : -1;
+    const float weight = id >= 0 && id < a.e ? a.weights[t * a.top + slot] : 0.0f;
     for (int s0 = 0; s0 < a.top; s0 += 8) { // eight choices' loads at once
         f32x4 p[8];
         float w[8];
 #pragma unroll
         for (int b = 0; b < 8; b++) {
-            const int s = s0 + b, id = s < a.top ? ids[s] : -1;
-            int from = s; // the first slot that names it has the product
-            for (int o = s < a.top ? s - 1 : -1; o >= 0; o--)
-                from = ids[o] == id ? o : from;
-            w[b] = 0.0f;
-            if (id >= 0 && id < a.e) {
-                w[b] = a.weights[t * a.top + s];
+            const int other = __builtin_amdgcn_readlane(id, s0 + b); // top <= 32
+            w[b] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), s0 + b));
+            p[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (other >= 0 && other < a.e) { // the first slot that names it has the product
+                const int from = __builtin_ctzll(__ballot(id == other));
                 p[b] = *reinterpret_cast<const f32x4 *>(a.out + (int64_t)(t * a.top + from) * a.k + j);
-            } else
-                p[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
         }
 #pragma unroll
         for (int b = 0; b < 8; b++)
@@ -587,6 +588,8 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a)
             for (int i = 0; i < 4; i++)
                 v[i] = fmaf(w[b], p[b][i], v[i]);
     }
+    if (column >= a.k)
+        return;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const float o = a.res ? v[i] + load_as(a.res, t * a.k + j + i, a.dtype) : v[i];
@@ -696,7 +699,9 @@ hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
     if constexpr (KIND == MOE_ALL) { // whichever of the classes takes most
         using B2 = Q4gBlock<TX, GRP, 1, 1, 2, 4>;
         using B1 = Q4gBlock<TX, GRP, 1, 1, 1, 4>;
-        lds = 4 * lds + (a.m <= 8 || B2::lds_bytes(k) > B1::lds_bytes(k) ? B2::lds_bytes(k) : B1::lds_bytes(k));
+        // (classes 1 and 2: class 0 has half of class 1's operands)
+        const int64_t x1 = a.m <= 8 || TX == Q4G_X_PARTS3 ? 0 : B1::lds_bytes(k);
+        lds = 4 * lds + (B2::lds_bytes(k) > x1 ? B2::lds_bytes(k) : x1);
     }
     moe_entry_kernel<TX, GRP, GATED, KIND><<<dim3((unsigned)(most < want ? most : want), (unsigned)count), 512,
                                             (size_t)lds, s>>>(a);
@@ -709,7 +714,7 @@ hipError_t experts(const MoeArgs &a, hipStream_t s)
 {
     constexpr int TH = TX == Q4G_X_F32 || TX == Q4G_X_PARTS3 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
     const int64_t pairs = (int64_t)a.m * a.top, active = pairs < a.e ? pairs : a.e;
-    const int64_t count = KIND == MOE_ONE ? pairs : active + pairs / 16; // of entries, at most
+    const int64_t count = KIND == MOE_ONE ? pairs : active + pairs / (TH == Q4G_X_PARTS3 ? 8 : 16); // of entries, at most
     hipError_t e = entries<TX, GRP, true, KIND>(a, active, count, s);
     if (e != hipSuccess)
         return e;

@@ -124,6 +124,7 @@ struct Q4gLinear {
     int64_t m, n, k, row0, tok0; // row0, tok0: this launch's first workgroup of row tiles, first activation row
     int fmt, act, y_dtype;
     int kw, parts, tok_groups; // waves along k of a workgroup, workgroups along k, groups of activation rows
+    int rw;                    // few rows: sets of kw waves
 };
 
 // The sums of a workgroup's waves: RTN row tiles and C column groups each, sets of kw waves adding up
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
     extern __shared__ float few_sums[]; // [8][N][64]
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
     const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
-    const int64_t rt = (a.row0 + blockIdx.x) * (8 / a.kw) + wave / a.kw, tok0 = a.tok0 + (int64_t)blockIdx.y * (16 / PK);
+    const int64_t rt = (a.row0 + blockIdx.x) * a.rw + wave / a.kw, tok0 = a.tok0 + (int64_t)blockIdx.y * (16 / PK);
     Wave w;
     w.clear();
     if (rt < sh.rt) {
@@ -224,15 +225,22 @@ __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
     q4g_outputs(a, w.y, rt0, tok0, reinterpret_cast<float *>(lds), lane);
 }
 
+constexpr int kMaxParts = 8; // of k, over workgroups
+
 // The parts of k added up in order, and the epilogue.
 __global__ void __launch_bounds__(256) q4g_finish_kernel(Q4gLinear a, int64_t first, int64_t count)
 {
     const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= first + count)
         return;
-    float v = a.part[i];
-    for (int p = 1; p < a.parts; p++)
-        v += a.part[p * a.m * a.n + i];
+    float parts[kMaxParts];
+#pragma unroll
+    for (int p = 0; p < kMaxParts; p++)
+        parts[p] = p < a.parts ? a.part[p * a.m * a.n + i] : 0.0f;
+    float v = parts[0];
+#pragma unroll
+    for (int p = 1; p < kMaxParts; p++)
+        v += parts[p];
     v = activate(a.bias ? v + a.bias[i % a.n] : v, a.act);
     if (a.res)
         v += load_as(a.res, i, a.y_dtype);
@@ -268,11 +276,11 @@ struct Q4gSplit {
 };
 
 // Up to 16 rows (8 as well, PK = 2) the weights are read once, and the work is split along k until some 4096
-// waves share it, along workgroups too.
+// waves share it, along workgroups too (whose sums a second launch adds up, which more rows make dear).
 Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rt = (n + 15) / 16, ks = (k + 511) / 512;
-    Q4gSplit s{m <= 8 ? 8 : 16, 1, 1, 1};
+    Q4gSplit s{m <= 8 || (wide && m <= 16) ? 8 : 16, 1, 1, 1}; // (16 rows of three parts: LDS of two workgroups)
     if (m > 16) {
         s.tiles = 2;
         if (!wide)
@@ -283,7 +291,7 @@ Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
     const int64_t sets = (rt + s.tiles - 1) / s.tiles * ((m + s.rows - 1) / s.rows);
     while (2 * s.kw <= pieces && 2 * s.kw <= ks && sets * s.kw < 4096)
         s.kw *= 2;
-    while (2 * s.parts <= chunks && s.parts < 8 && sets * s.kw * s.parts < 4096)
+    while (m <= 16 && 2 * s.parts <= chunks && s.parts < kMaxParts && sets * s.kw * s.parts < 4096)
         s.parts *= 2;
     return s;
 }
@@ -297,16 +305,17 @@ template <int TX, int GRP, int PK, int D>
 hipError_t linear_few(Q4gLinear a, hipStream_t s)
 {
     const int64_t rt = (a.n + 15) / 16, ks = (a.k + 511) / 512, groups = (a.m + 16 / PK - 1) / (16 / PK);
-    a.kw = 1;
-    while (a.kw < 8 && 2 * a.kw <= ks && rt * groups * a.kw < 4096)
-        a.kw *= 2;
+    int64_t kw = (4096 + rt * groups - 1) / (rt * groups); // some 4096 waves, a piece each at least
+    kw = kw < ks ? kw : ks, kw = kw < 8 ? kw : 8;
+    a.kw = (int)kw, a.rw = (int)(8 / kw);
+    const unsigned threads = 64 * a.kw * a.rw;
     hipError_t e = hipSuccess;
     for (int64_t g0 = 0; g0 < groups && e == hipSuccess; g0 += 1 << 12) {
         const int64_t gn = groups - g0 < 1 << 12 ? groups - g0 : 1 << 12;
         a.tok0 = g0 * (16 / PK);
-        e = launch_parts((rt * a.kw + 7) / 8, kPartThreads / 512, [&](int64_t first, int64_t count) {
+        e = launch_parts((rt + a.rw - 1) / a.rw, kPartThreads / 512, [&](int64_t first, int64_t count) {
             a.row0 = first;
-            q4g_few_kernel<TX, GRP, PK, D><<<dim3((unsigned)count, (unsigned)gn), 512,
+            q4g_few_kernel<TX, GRP, PK, D><<<dim3((unsigned)count, (unsigned)gn), threads,
                                             a.kw > 1 ? 8 * (4 / PK) * 64 * sizeof(float) : 0, s>>>(a);
         });
     }
@@ -345,13 +354,12 @@ hipError_t linear_more(const Q4gLinear &a, const Q4gSplit &split, hipStream_t s)
 {
     if (split.rows == 8)
         return linear_c<TX, GRP, 1, 1, 2, 4, 4>(a, split, s);
-    if (split.tiles == 1)
-        return linear_c<TX, GRP, 1, 1, 1, 4, 4>(a, split, s);
     if constexpr (TX == Q4G_X_PARTS3)
         return linear_c<TX, GRP, 2, 1, 1, 4, 2>(a, split, s);
     else
-        return split.rows == 32 ? linear_c<TX, GRP, 2, 2, 1, 2, 2>(a, split, s)
-                                : linear_c<TX, GRP, 2, 4, 1, 2, 2>(a, split, s);
+        return split.tiles == 1   ? linear_c<TX, GRP, 1, 1, 1, 4, 4>(a, split, s)
+               : split.rows == 32 ? linear_c<TX, GRP, 2, 2, 1, 2, 2>(a, split, s)
+                                  : linear_c<TX, GRP, 2, 4, 1, 2, 2>(a, split, s);
 }
 
 template <int TX, int GRP>
@@ -359,7 +367,7 @@ hipError_t linear_small(const Q4gLinear &a, hipStream_t s)
 {
     return a.m <= 4   ? linear_few<TX, GRP, 4, 4>(a, s)
            : a.m <= 8 ? linear_few<TX, GRP, 2, 2>(a, s)
-                      : linear_few<TX, GRP, 1, TX == Q4G_X_F32 ? 1 : 2>(a, s);
+                      : linear_few<TX, GRP, 1, 2>(a, s);
 }
 
 template <int GRP>
