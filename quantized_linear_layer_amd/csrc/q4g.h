@@ -182,10 +182,18 @@ struct Q4gTile {
         }
     }
 
+    // (w & m) | b in one instruction: it takes no literals, so the constants stay in registers, where the
+    // compiler would rather have two instructions with a literal each.
+    __device__ __forceinline__ static uint32_t and_or(uint32_t w, uint32_t m, uint32_t b)
+    {
+        asm("" : "+s"(m));
+        asm("" : "+v"(b));
+        return (w & m) | b;
+    }
     __device__ __forceinline__ static bf16x8 widen(uint32_t w) // 16 + c of the eight codes
     {
         constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
-        const u32x4 v = {((w << 3) & m) | b, ((w >> 1) & m) | b, ((w >> 5) & m) | b, ((w >> 9) & m) | b};
+        const u32x4 v = {and_or(w << 3, m, b), and_or(w >> 1, m, b), and_or(w >> 5, m, b), and_or(w >> 9, m, b)};
         return __builtin_bit_cast(bf16x8, v);
     }
     // c - z: 1024 + c as f16 bits at a nibble's place, 1024 + 16 c one place up
@@ -196,10 +204,10 @@ struct Q4gTile {
         const f16x2 less1024 = __builtin_bit_cast(f16x2, 0xe400e400u + z * 0x00010001u); // -1024 - z
         const f16x2 less64 = __builtin_bit_cast(f16x2, 0xd400d400u + z * 0x00100010u);   // -64 - z
         const uint32_t u = w >> 8;
-        const f16x2 p0 = __builtin_bit_cast(f16x2, (w & lo) | b) + less1024;
-        const f16x2 p1 = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w & hi) | b), sixteenth, less64);
-        const f16x2 p2 = __builtin_bit_cast(f16x2, (u & lo) | b) + less1024;
-        const f16x2 p3 = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (u & hi) | b), sixteenth, less64);
+        const f16x2 p0 = __builtin_bit_cast(f16x2, and_or(w, lo, b)) + less1024;
+        const f16x2 p1 = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, and_or(w, hi, b)), sixteenth, less64);
+        const f16x2 p2 = __builtin_bit_cast(f16x2, and_or(u, lo, b)) + less1024;
+        const f16x2 p3 = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, and_or(u, hi, b)), sixteenth, less64);
         return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
     }
 
@@ -218,6 +226,8 @@ struct Q4gTile {
     {
         const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
         const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+        uint32_t which = bf16 ? ~0u : 0u;
+        asm("" : "+v"(which));
         f32x4 sum[C];
 #pragma unroll
         for (int g = 0; g < kGroups; g++) {
@@ -228,8 +238,9 @@ struct Q4gTile {
             for (int r = 0; r < RTN; r++) {
                 uint32_t pair = piece.scale[r][number / 2];
                 asm volatile("" : "+v"(pair)); // converted here, not the whole piece's at once
-                const uint32_t bits = number & 1 ? pair >> 16 : pair & 0xffffu;
-                s[r] = bf16 ? __builtin_bit_cast(float, bits << 16) : half_bits_to_float(bits);
+                const uint32_t as_bf16 = number & 1 ? pair & 0xffff0000u : pair << 16;
+                const uint32_t as_f16 = __builtin_bit_cast(uint32_t, half_bits_to_float(number & 1 ? pair >> 16 : pair));
+                s[r] = __builtin_bit_cast(float, (as_bf16 & which) | (as_f16 & ~which)); // one instruction, no branch
                 z[r] = (piece.zero[r][number / 8] >> (4 * (number & 7))) & 15u;
             }
             f32x4 d[RTN][C][PK];

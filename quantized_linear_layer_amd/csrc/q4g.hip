@@ -167,23 +167,25 @@ __device__ __forceinline__ void q4g_outputs(const Q4gLinear &a, const float (&y)
     }
 }
 
-// Few activation rows, or a small product: the waves of a set share its row tile's pieces of k;
+// Few activation rows, or a small product: the waves of a set share its row tiles' pieces of k;
 // groups of 16 / PK activation rows along y.
-template <int TX, int GRP, int PK, int D>
+template <int TX, int GRP, int RTN, int PK, int D>
 __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 {
-    using Wave = Q4gWave<TX, GRP, 1, PK, D>;
-    extern __shared__ float few_sums[]; // [8][N][64]
+    using Wave = Q4gWave<TX, GRP, RTN, PK, D>;
+    extern __shared__ float few_sums[]; // [8][RTN * N][64]
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
     const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
-    const int64_t rt = (a.row0 + blockIdx.x) * a.rw + wave / a.kw, tok0 = a.tok0 + (int64_t)blockIdx.y * (16 / PK);
+    const int64_t rt = ((a.row0 + blockIdx.x) * a.rw + wave / a.kw) * RTN, tok0 = a.tok0 + (int64_t)blockIdx.y * (16 / PK);
     Wave w;
     w.clear();
     if (rt < sh.rt) {
         typename Wave::From f;
         const int64_t rows = a.m - tok0; // past the last row: its values again
         const uint32_t row = Wave::row_of(lane) < rows ? Wave::row_of(lane) : (uint32_t)rows - 1;
-        f.w[0] = Q4gRows(a.wp, sh, rt, GRP, a.fmt);
+#pragma unroll
+        for (int r = 0; r < RTN; r++) // past the last tile: the last one again, not stored
+            f.w[r] = Q4gRows(a.wp, sh, rt + r < sh.rt ? rt + r : sh.rt - 1, GRP, a.fmt);
         f.x = static_cast<const uint8_t *>(a.x) + tok0 * a.k * q4g_x_size(TX), f.at = row * (uint32_t)a.k * q4g_x_size(TX);
         f.part = 0, f.last = (int)a.k - 32, f.kt = (int)sh.kt;
         const int ks = (int)sh.ks, per = (ks + a.kw - 1) / a.kw, p0 = kw * per;
@@ -301,13 +303,15 @@ size_t part_bytes(const Q4gSplit &s, int64_t m, int64_t n)
     return s.parts > 1 ? ((size_t)s.parts * m * n * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
-template <int TX, int GRP, int PK, int D>
+template <int TX, int GRP, int RTN, int PK, int D>
 hipError_t linear_few(Q4gLinear a, hipStream_t s)
 {
-    const int64_t rt = (a.n + 15) / 16, ks = (a.k + 511) / 512, groups = (a.m + 16 / PK - 1) / (16 / PK);
+    const int64_t rt = ((a.n + 15) / 16 + RTN - 1) / RTN, ks = (a.k + 511) / 512, groups = (a.m + 16 / PK - 1) / (16 / PK);
     int64_t kw = (4096 + rt * groups - 1) / (rt * groups); // some 4096 waves, a piece each at least
     kw = kw < ks ? kw : ks, kw = kw < 8 ? kw : 8;
-    a.kw = (int)kw, a.rw = (int)(8 / kw);
+    // sets a workgroup: one, until there are two workgroups for every CU
+    const int64_t rw = rt * groups / 512;
+    a.kw = (int)kw, a.rw = (int)(rw < 1 ? 1 : rw < 8 / kw ? rw : 8 / kw);
     const unsigned threads = 64 * a.kw * a.rw;
     hipError_t e = hipSuccess;
     for (int64_t g0 = 0; g0 < groups && e == hipSuccess; g0 += 1 << 12) {
@@ -315,8 +319,8 @@ hipError_t linear_few(Q4gLinear a, hipStream_t s)
         a.tok0 = g0 * (16 / PK);
         e = launch_parts((rt + a.rw - 1) / a.rw, kPartThreads / 512, [&](int64_t first, int64_t count) {
             a.row0 = first;
-            q4g_few_kernel<TX, GRP, PK, D><<<dim3((unsigned)count, (unsigned)gn), threads,
-                                            a.kw > 1 ? 8 * (4 / PK) * 64 * sizeof(float) : 0, s>>>(a);
+            q4g_few_kernel<TX, GRP, RTN, PK, D><<<dim3((unsigned)count, (unsigned)gn), threads,
+                                                 a.kw > 1 ? 8 * RTN * (4 / PK) * 64 * sizeof(float) : 0, s>>>(a);
         });
     }
     return e;
@@ -365,9 +369,9 @@ hipError_t linear_more(const Q4gLinear &a, const Q4gSplit &split, hipStream_t s)
 template <int TX, int GRP>
 hipError_t linear_small(const Q4gLinear &a, hipStream_t s)
 {
-    return a.m <= 4   ? linear_few<TX, GRP, 4, 4>(a, s)
-           : a.m <= 8 ? linear_few<TX, GRP, 2, 2>(a, s)
-                      : linear_few<TX, GRP, 1, 2>(a, s);
+    return a.m <= 4   ? linear_few<TX, GRP, 1, 4, 4>(a, s)
+           : a.m <= 8 ? linear_few<TX, GRP, 1, 2, 2>(a, s)
+                      : linear_few<TX, GRP, 2, 1, TX == Q4G_X_F32 ? 1 : 2>(a, s);
 }
 
 template <int GRP>
