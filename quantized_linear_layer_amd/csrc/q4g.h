@@ -228,6 +228,16 @@ struct Q4gTile {
         const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
         uint32_t which = bf16 ? ~0u : 0u;
         asm("" : "+v"(which));
+        // a quad's operands are asked for while the one before it is multiplied
+        u32x4 xs[2][C][P];
+        const auto ask = [&](int q) {
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int p = 0; p < P; p++)
+                    xs[q & 1][c][p] = operand(q, c, p);
+        };
+        ask(0);
         f32x4 sum[C];
 #pragma unroll
         for (int g = 0; g < kGroups; g++) {
@@ -247,12 +257,9 @@ struct Q4gTile {
 #pragma unroll
             for (int e = 0; e < kSteps; e++) {
                 const int step = g * kSteps + e, q = step / PK, b = step % PK;
-                u32x4 x[C][P];
-#pragma unroll
-                for (int c = 0; c < C; c++)
-#pragma unroll
-                    for (int p = 0; p < P; p++)
-                        x[c][p] = operand(q, c, p);
+                u32x4 (&x)[C][P] = xs[q & 1];
+                if (step % PK == 0 && q + 1 < kQuads)
+                    ask(q + 1);
                 if constexpr (TX == Q4G_X_F16) {
 #pragma unroll
                     for (int r = 0; r < RTN; r++) {
