@@ -418,7 +418,7 @@ __device__ __forceinline__ void lds_operand16(const uint8_t *base, uint32_t off,
                  : "memory", "m0");
 }
 
-// More rows: a workgroup of eight waves with the activations in LDS, in the order of
+// More rows: a workgroup of up to eight waves with the activations in LDS, in the order of
 // the matrix instruction's operands.  A wave that fetches them itself moves, for every KB of
 // codes, 2 KB (8 rows) to 4 KB (16) of them through a path that gives 12 to 15 bytes a
 // clock and CU whatever cache they come from (14336 -> 4096, 16 rows: 19 us, with the operands
@@ -451,9 +451,9 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
     // operand (q, c, p) of tile t of a chunk at (((t * kQuads + q) * C + c) * P + p) * 1024 + lane * 16
     __device__ __forceinline__ static void fetch_x(const X &src, int chunk, uint32_t lds, int lane)
     {
-        const int wave = wave_number(), kt = (src.k + 127) / 128 - chunk * (kChunk / 128);
+        const int wave = wave_number(), waves = blockDim.x / 64, kt = (src.k + 127) / 128 - chunk * (kChunk / 128);
         const int count = (kt < kChunk / 128 ? kt : kChunk / 128) * kQuads;
-        for (int i = wave; i < count; i += 8) { // tile i / kQuads, quad i % kQuads
+        for (int i = wave; i < count; i += waves) { // tile i / kQuads, quad i % kQuads
             const int step = chunk * kChunk + i / kQuads * 128 + 32 * (i % kQuads * PK + lane % PK);
             const uint32_t at_k = ((uint32_t)(step < src.k - 32 ? step : src.k - 32) + 8 * (lane / 16)) * 2;
 #pragma unroll

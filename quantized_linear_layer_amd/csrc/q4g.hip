@@ -124,7 +124,7 @@ struct Q4gLinear {
     int64_t m, n, k, row0, tok0; // row0, tok0: this launch's first workgroup of row tiles, first activation row
     int fmt, act, y_dtype;
     int kw, parts, tok_groups; // waves along k of a workgroup, workgroups along k, groups of activation rows
-    int rw;                    // few rows: sets of kw waves
+    int rw;                    // sets of kw waves of a workgroup
 };
 
 // The sums of a workgroup's waves: RTN row tiles and C column groups each, sets of kw waves adding up
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
     const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
     const int64_t b = blockIdx.x, tg = b / 8 % a.tok_groups, rg = b / 8 / a.tok_groups * 8 + b % 8;
-    const int64_t rt0 = ((a.row0 + rg) * (8 / a.kw) + wave / a.kw) * RTN;
+    const int64_t rt0 = ((a.row0 + rg) * a.rw + wave / a.kw) * RTN;
     const int64_t tok0 = a.tok0 + tg * Block::T;
     typename Block::X src;
     src.base = static_cast<const uint8_t *>(a.x) + tok0 * a.k * 2;
@@ -265,16 +265,21 @@ __global__ void __launch_bounds__(256) q4g_split_kernel(const uint8_t *x, uint8_
 }
 
 // Whether a product takes the waves that fetch their own activations, in one launch and without a
-// workspace: up to four rows, or so little work that launches and idle CUs count for more.
-bool q4g_small(int64_t m, int64_t n, int64_t k)
+// workspace: up to four rows; while the codes that all groups of 16 rows read are few (us, so and with
+// the rows in LDS: 14336 x 4096, 8 rows 10.2 and 14.3, 64 rows 39 and 55, 128 rows 70 and 55; 4096 x 4096,
+// 256 rows 38 and 54; f32, 14336 x 4096, 32 rows 36 and 39, 33 rows 46 and 45), but on short and wide matrices
+// with 9 to 16 rows, where four operands a tile are too much (4096 x 14336, 16 rows 19.2 and 14.4).
+bool q4g_small(bool wide, int64_t m, int64_t n, int64_t k)
 {
-    return m <= 4 || (m <= 64 && (m + 15) / 16 * n * k <= (int64_t)1 << 25);
+    if (m > 8 && m <= 16 && n < 8192 && n * k > (int64_t)1 << 25)
+        return false;
+    return m <= 4 || (m + 15) / 16 <= ((int64_t)1 << (wide ? 27 : 28)) / (n * k);
 }
 
 // How another product is split: T activation rows and `tiles` row tiles a wave, kw
 // waves and `parts` workgroups along k.
 struct Q4gSplit {
-    int rows, tiles, kw, parts;
+    int rows, tiles, kw, parts, sets; // sets of kw waves of a workgroup
 };
 
 // Up to 16 rows (8 as well, PK = 2) the weights are read once, and the work is split along k until some 4096
@@ -282,7 +287,7 @@ struct Q4gSplit {
 Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
 {
     const int64_t rt = (n + 15) / 16, ks = (k + 511) / 512;
-    Q4gSplit s{m <= 8 || (wide && m <= 16) ? 8 : 16, 1, 1, 1}; // (16 rows of three parts: LDS of two workgroups)
+    Q4gSplit s{m <= 8 || (wide && m <= 16) ? 8 : 16, 1, 1, 1, 8}; // (16 rows of three parts: LDS of two workgroups)
     if (m > 16) {
         s.tiles = 2;
         if (!wide)
@@ -293,8 +298,26 @@ Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
     const int64_t sets = (rt + s.tiles - 1) / s.tiles * ((m + s.rows - 1) / s.rows);
     while (2 * s.kw <= pieces && 2 * s.kw <= ks && sets * s.kw < 4096)
         s.kw *= 2;
-    while (m <= 16 && 2 * s.parts <= chunks && s.parts < kMaxParts && sets * s.kw * s.parts < 4096)
-        s.parts *= 2;
+    s.sets = 8 / s.kw;
+    if (m <= 16) {
+        while (2 * s.parts <= chunks && s.parts < kMaxParts && sets * s.kw * s.parts < 4096)
+            s.parts *= 2;
+        return s;
+    }
+    // More rows: the sets of a workgroup and the parts of k by what their rounds of workgroups cost, in us:
+    // a chunk takes some 6 us at eight sets of 64 rows, where a quarter is the activations' and the wait's,
+    // and the parts are written, read and added up by another launch.
+    const double unit = 0.6 * s.rows / 64 * (wide ? 3 : 1);
+    const int64_t at_once = s.rows == 32 ? 512 : 256;
+    double least = 0;
+    for (int parts = 1; parts <= kMaxParts && parts <= chunks; parts *= 2)
+        for (int w = 8; w >= 1; w /= 2) {
+            const int64_t groups = (rt + s.tiles * w - 1) / (s.tiles * w) * ((m + s.rows - 1) / s.rows) * parts;
+            const double cost = (double)((groups + at_once - 1) / at_once * ((chunks + parts - 1) / parts)) * unit * (w + 2) +
+                                (parts > 1 ? 4 + parts * m * n * 2e-6 : 0);
+            if (least == 0 || cost < least)
+                least = cost, s.sets = w, s.parts = parts;
+        }
     return s;
 }
 
@@ -330,8 +353,8 @@ template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
 hipError_t linear_c(Q4gLinear a, const Q4gSplit &split, hipStream_t s)
 {
     using Block = Q4gBlock<TX, GRP, RTN, C, PK, D>;
-    a.kw = split.kw, a.parts = split.parts;
-    const int64_t sets = ((a.n + 15) / 16 + RTN * (8 / a.kw) - 1) / (RTN * (8 / a.kw)), threads = 512;
+    a.kw = split.kw, a.rw = split.sets, a.parts = split.parts;
+    const int64_t sets = ((a.n + 15) / 16 + RTN * a.rw - 1) / (RTN * a.rw), threads = 64 * a.kw * a.rw;
     const size_t sums = a.kw > 1 ? (size_t)8 * RTN * C * Block::N * 64 * sizeof(float) : 0;
     const size_t x = Block::lds_bytes(a.k), lds = x > sums ? x : sums;
     const int64_t groups = (a.m + Block::T - 1) / Block::T;
@@ -377,7 +400,7 @@ hipError_t linear_small(const Q4gLinear &a, hipStream_t s)
 template <int GRP>
 hipError_t linear_g(Q4gLinear a, int dtype, uint8_t *ws, hipStream_t s)
 {
-    if (q4g_small(a.m, a.n, a.k))
+    if (q4g_small(dtype == QLL_W_F32, a.m, a.n, a.k))
         return dtype == QLL_W_F32    ? linear_small<Q4G_X_F32, GRP>(a, s)
                : dtype == QLL_W_BF16 ? linear_small<Q4G_X_BF16, GRP>(a, s)
                                      : linear_small<Q4G_X_F16, GRP>(a, s);
@@ -418,10 +441,14 @@ hipError_t launch_q4g_split(const void *x, void *parts, int64_t count, hipStream
 
 size_t q4g_linear_workspace(int64_t m, int64_t n, int64_t k)
 {
-    if (q4g_small(m, n, k))
-        return 0;
-    const size_t a = part_bytes(q4g_split(false, m, n, k), m, n), b = part_bytes(q4g_split(true, m, n, k), m, n) + (size_t)(m * k) * 6;
-    return a > b ? a : b;
+    size_t need = 0; // of whichever type of rows takes more
+    if (!q4g_small(false, m, n, k))
+        need = part_bytes(q4g_split(false, m, n, k), m, n);
+    if (!q4g_small(true, m, n, k)) {
+        const size_t wide = part_bytes(q4g_split(true, m, n, k), m, n) + (size_t)(m * k) * 6;
+        need = need > wide ? need : wide;
+    }
+    return need;
 }
 
 hipError_t launch_q4g_linear(const uint8_t *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias,

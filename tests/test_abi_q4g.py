@@ -72,6 +72,15 @@ def test_linear(L):
     for at, values in ((1, (0, 16, 48, 256)), (2, (-1, 4)), (4, (-1, 3)), (6, (-1, 5)), (9, (-1, 3))):
         for v in values:
             refusals(f, ok, {at: v}, VALUE)
+    W = qll.qll_workspace_bytes
+    for m, n, k in ((1, 2 ** 20, 4096), (4, 14336, 4096), (8, 14336, 4096), (64, 1024, 1024), (512, 64, 96)):
+        assert W(qll.QLL_OP_Q4G_LINEAR, m, n, k) == 0
+    for m, n, k in ((16, 4096, 14336), (512, 14336, 4096)):  # parts of k, or f32 rows as parts
+        need = W(qll.QLL_OP_Q4G_LINEAR, m, n, k)
+        assert need > 0
+        for v in (0, 1, 2):
+            refusals(f, ok, {4: v, 10: m, 11: n, 12: k, 14: need - 1}, WORKSPACE)
+            refusals(f, ok, {4: v, 10: m, 11: n, 12: k, 13: NUL, 14: 0}, WORKSPACE)
     for m, n, k in ((0, 70, 128), (5, 0, 128), (5, 70, 0), (5, 70, 96), (5, 70, 2 ** 24), (2 ** 31, 70, 128),
                     (2 ** 25, 2 ** 25, 128)):
         refusals(f, ok, {10: m, 11: n, 12: k}, SHAPE)

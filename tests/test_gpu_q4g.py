@@ -167,6 +167,53 @@ def test_captured_and_on_another_stream(qll_gpu, dtype, m):
         assert torch.equal(y, want), f"replay {i}"
 
 
+# The kernels whose workgroups hold activation rows in LDS take products too large for the
+# oracle's side on the CPU: (m, n, k, group), of 16-bit rows with 8, 16, 32 and 64 of them at once, k in
+# parts over workgroups and not, ends of k inside a tile and a chunk; of f32 rows with 8 and 16.
+LARGE = [("bf16", 8, 70001, 3872, 32), ("f16", 5, 66000, 4160, 64), ("bf16", 16, 1000, 33664, 64),
+         ("f16", 9, 517, 66432, 32), ("f16", 20, 33001, 4128, 32), ("bf16", 32, 32800, 4224, 128),
+         ("bf16", 70, 13000, 4256, 32), ("f16", 130, 8200, 4224, 128), ("bf16", 512, 520, 16576, 64),
+         ("f16", 300, 3000, 8288, 32), ("f32", 7, 33000, 4128, 32), ("f32", 8, 32800, 4224, 128),
+         ("f32", 12, 1000, 33664, 64), ("f32", 40, 11000, 4192, 32), ("f32", 130, 3700, 4224, 128),
+         ("f32", 64, 600, 57472, 64)]
+
+
+@pytest.mark.parametrize("dtype,m,n,k,group", LARGE)
+def test_rows_in_lds(qll_gpu, dtype, m, n, k, group):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + n)
+    fmt = FMTS[(m + n) % 4]
+    groups, sdt = k // group, torch.bfloat16 if fmt & qll.QLL_Q4G_BF16 else torch.float16
+    codes = torch.randint(0, 16, (n, k), generator=g, device="cuda", dtype=torch.uint8)
+    scales = ((torch.rand(n, groups, generator=g, device="cuda") - 0.5) / k ** 0.5).to(sdt)
+    zeros = torch.randint(0, 16, (n, groups), generator=g, device="cuda", dtype=torch.uint8)
+    wp = empty(qll.qll_q4g_packed_bytes(n, k, group, fmt))
+    qll.qll_q4g_pack(codes, scales, zeros, group, fmt, wp, n, k)
+    if not fmt & qll.QLL_Q4G_ZEROS:
+        zeros.fill_(8)
+    x = torch.randn(m, k, generator=g, device="cuda").to(R.TYPES[dtype])
+    bias, res = torch.randn(n, generator=g, device="cuda"), torch.randn(m, n, generator=g, device="cuda").to(x.dtype)
+    y = torch.full((m * n + GUARD,), 3.25, dtype=x.dtype, device="cuda")
+    assert qll.qll_workspace_bytes(qll.QLL_OP_Q4G_LINEAR, m, n, k) > 0 or dtype != "f32"
+    for _ in range(2):  # again in the same workspace
+        qll.qll_q4g_linear(wp, group, fmt, x, R.CODES[dtype], bias, qll.QLL_ACT_SILU, res, y, R.CODES[dtype], m, n, k,
+                           ws=workspace(m, n, k))
+    torch.cuda.synchronize()
+    assert (y[m * n:] == 3.25).all(), "wrote past the outputs"
+    xd = x.double()
+    for at in range(0, n, 8192):  # the bounds of q4g_refs, some rows at a time
+        rows = slice(at, min(at + 8192, n))
+        s = scales[rows].double().repeat_interleave(group, 1)
+        z = zeros[rows].double().repeat_interleave(group, 1)
+        c = codes[rows].double()
+        want = xd @ (s * (c - z)).T
+        mag = xd.abs() @ (s.abs() * (c - z).abs()).T
+        off = 3 * group * R.U * (xd.abs() @ (s.abs() * (32.0 + c + z)).T)
+        off += (groups + 12) * R.U * (mag + off) + 1e-36
+        want, off = E.linear(want.cpu().numpy(), off.cpu().numpy(), bias[rows].cpu().numpy(), "silu", R.f64(res[:, rows]))
+        E.assert_bound(R.f64(y[:m * n].view(m, n)[:, rows]), want, R.rounded(want, off, dtype), f"rows from {at}")
+
+
 def test_offsets_past_32_bits(qll_gpu):
     """Codes of 4.3 GB: the first, the middle and the last rows, as packed on their own."""
     n, k, group, fmt = (1 << 21) + 40, 4096, 128, qll.QLL_Q4G_ZEROS
