@@ -548,12 +548,9 @@ __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
         const MoeEntry entry(__builtin_amdgcn_readfirstlane(a.plan->entry[y]));
         if constexpr (KIND == MOE_FEW)
             moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
-        else if (y < a.plan->begin[1]) {
-            if constexpr (TX == Q4G_X_PARTS3) // three operands a quad
-                moe_more<TX, GRP, 4, GATED>(a, entry, entry_lds);
-            else
-                moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
-        } else if (y < a.plan->begin[2])
+        else if (y < a.plan->begin[1])
+            moe_few<TX, GRP, GATED, KIND>(a, entry, sums);
+        else if (y < a.plan->begin[2])
             moe_more<TX, GRP, 2, GATED>(a, entry, entry_lds);
         else if constexpr (TX != Q4G_X_PARTS3)
             moe_more<TX, GRP, 1, GATED>(a, entry, entry_lds);
@@ -686,7 +683,8 @@ int64_t moe_group(int64_t m, int64_t top, int64_t k)
     return room / each < 2 ? 1 : room / each < tokens ? room / each : tokens;
 }
 
-// Entries' products as one launch of up to some 1024 workgroups.
+// Entries' products as one launch of up to some 4096 workgroups: mostly one set of row tiles each, whose
+// ends overlap with others' work (1024 with several each: down products 5% slower).
 template <int TX, int GRP, bool GATED, int KIND>
 hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
 {
@@ -694,12 +692,11 @@ hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
     a.kw = 1; // waves along k, at most: a class whose chunks have fewer pieces takes fewer
     while (a.kw < 8 && 2 * a.kw <= ks && tiles * active * a.kw < (GATED ? 2048 : 4096))
         a.kw *= 2;
-    const int64_t most = (tiles * a.kw + 7) / 8, want = (1024 + active - 1) / active;
+    const int64_t most = (tiles * a.kw + 7) / 8, want = (4096 + active - 1) / active;
     int64_t lds = (GATED ? 2 : 1) * 8 * 64 * sizeof(float);
     if constexpr (KIND == MOE_ALL) { // whichever of the classes takes most
         using B2 = Q4gBlock<TX, GRP, 1, 1, 2, 4>;
         using B1 = Q4gBlock<TX, GRP, 1, 1, 1, 4>;
-        // (classes 1 and 2: class 0 has half of class 1's operands)
         const int64_t x1 = a.m <= 8 || TX == Q4G_X_PARTS3 ? 0 : B1::lds_bytes(k);
         lds = 4 * lds + (B2::lds_bytes(k) > x1 ? B2::lds_bytes(k) : x1);
     }

@@ -242,16 +242,16 @@ struct Q4gTile {
 #pragma unroll
         for (int g = 0; g < kGroups; g++) {
             const int number = j * kGroups + g; // of the piece's groups
-            float s[RTN];
+            float s[RTN], z16[RTN]; // the scale, and 16 + z by its bits
             uint32_t z[RTN];
 #pragma unroll
             for (int r = 0; r < RTN; r++) {
-                uint32_t pair = piece.scale[r][number / 2];
-                asm volatile("" : "+v"(pair)); // converted here, not the whole piece's at once
+                const uint32_t pair = piece.scale[r][number / 2];
                 const uint32_t as_bf16 = number & 1 ? pair & 0xffff0000u : pair << 16;
                 const uint32_t as_f16 = __builtin_bit_cast(uint32_t, half_bits_to_float(number & 1 ? pair >> 16 : pair));
                 s[r] = __builtin_bit_cast(float, (as_bf16 & which) | (as_f16 & ~which)); // one instruction, no branch
                 z[r] = (piece.zero[r][number / 8] >> (4 * (number & 7))) & 15u;
+                z16[r] = __builtin_bit_cast(float, z[r] << 19 | 0x41800000u);
             }
             f32x4 d[RTN][C][PK];
 #pragma unroll
@@ -308,7 +308,7 @@ struct Q4gTile {
                         for (int b = 1; b < count; b++)
                             v += d[r][c][b0 + b][i * PK + b0 + b];
                         if constexpr (TX != Q4G_X_F16)
-                            v = fmaf(-(16.0f + (float)z[r]), whole, v);
+                            v = fmaf(-z16[r], whole, v);
                         y[r][c][i] = fmaf(s[r], v, y[r][c][i]);
                     }
                 }
