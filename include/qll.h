@@ -499,7 +499,8 @@ int qll_q4g_from_q4_0(const void *w, void *wp, int64_t n, int64_t k, void *strea
  * 1e-4 * sum_t |x s| (|c - z| + 16) of the exact sum.  |x| < 2^120.  A row of x with
  * NaN or an infinity in it has unspecified outputs, other rows do not change.  k % group == 0,
  * k < 2^24 (else QLL_ERR_SHAPE).  ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_LINEAR,
- * m, n, k) bytes (0 so far: ws may be NULL).  QLL_ERR_VALUE for another group, fmt, dtype or act. */
+ * m, n, k) bytes (0 where one launch does without, as up to four rows do: ws may be NULL
+ * then); contents on return unspecified.  QLL_ERR_VALUE for another group, fmt, dtype or act. */
 int qll_q4g_linear(const void *wp, int64_t group, int fmt, const void *x, int dtype, const float *bias, int act,
                    const void *residual, void *y, int y_dtype, int64_t m, int64_t n, int64_t k, void *ws,
                    size_t ws_bytes, void *stream);
@@ -522,19 +523,22 @@ int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const 
                   float scale, int32_t *ids, float *weights, int64_t top, int64_t m, int64_t e, int64_t k, void *ws,
                   size_t ws_bytes, void *stream);
 
-/* The experts of a feed-forward block on the tokens that chose them, two kernels:
+/* The experts of a feed-forward block on the tokens that chose them:
  *     Y[i] = T(sum_j weights[i][j] * Wd_e.(act(Wg_e.x_i) * (Wu_e.x_i)) + residual[i]),  e = ids[i][j].
  * wg, wu: e packed matrices [n][k], one every qll_q4g_packed_bytes(n, k, group, fmt) bytes; wd: e
  * packed matrices [k][n] likewise; x, residual (or NULL; may be y), y: [m][k] of type T = dtype;
  * ids: int32[m][top], weights: float[m][top].  An id outside [0, e) (padding) adds nothing, and
  * its weight is not read; a row of such ids gets its residual, or 0.  An expert that a token names
- * twice counts with the sum of its weights.  The gated products keep 16 bits of
- * precision between the two kernels, 24 where x is f32.  Made for few tokens: up to 64 read each chosen expert's weights once, more go in
- * groups of 64.  n % group == 0, k % group == 0, n < 2^20, k < 2^24; e and top as in
- * qll_moe_route.  NaN and infinities in x, and its size: as in qll_q4g_linear.  The result does
- * not depend on what other tokens are in the call beyond the order of f32 sums.
- * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_MOE, m, n, top) bytes; contents on
- * return unspecified. */
+ * twice counts with both weights.  The gated products keep 16 bits of
+ * precision between the two products, 24 where x is f32.  One token takes two launches, more take
+ * four or five.  Made for few tokens: up to 64 go at once, and an expert's weights are read once for
+ * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, or of fewer from
+ * top * k > 131072 (k > 32768 with fewer than 64 tokens) on.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;
+ * e and top as in qll_moe_route (else QLL_ERR_SHAPE); QLL_ERR_VALUE for another group, fmt, dtype or act.
+ * NaN and infinities, and the size of x and of the gated products: as x in qll_q4g_linear, token by token.
+ * The result does not depend on what other tokens are in the call beyond the order of f32 sums.
+ * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_MOE, m, n, top) bytes (up to 32 MiB and
+ * 6 * top * n for each of up to 64 tokens); contents on return unspecified. */
 int qll_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top, const void *wg,
                 const void *wu, const void *wd, int64_t group, int fmt, int act, const void *residual, void *y,
                 int64_t m, int64_t n, int64_t k, int64_t e, void *ws, size_t ws_bytes, void *stream);

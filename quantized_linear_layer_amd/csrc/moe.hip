@@ -53,7 +53,9 @@ __device__ __forceinline__ int route_reduce(double (&v)[ALL])
 // Logits in 64 bits: an f32 sum's order would decide between two experts whose
 // logits lie next to each other.  The products are exact in f64 for every type.  A
 // workgroup's four waves share the k of TE experts and TT tokens; with VEC (k a multiple of
-// eight) a lane takes eight elements of a row at a time.
+// eight) a lane takes eight elements of a row at a time.  One token, 128 x 4096 bf16: 2.8 us, a trip to memory and
+// the sums over the lanes; 64 tokens, 256 x 4096 f32 11 us (12 TFLOP/s of f64): converting and multiplying in f64,
+// and every expert's row loaded again for eight tokens (tiles of 8 x 8: 14.5).
 template <class TX, class TW, int TE, int TT, bool VEC>
 __global__ void __launch_bounds__(256) moe_logits_kernel(const TX *x, const TW *w, double *logits, int m, int e, int k)
 {
@@ -166,7 +168,9 @@ __device__ __forceinline__ double wave_sum(double v)
 }
 
 // One wave a token, PER experts a lane (lane * PER + i): scores in 64 bits, then `top` times the
-// largest that is left, the lower index first among equal ones.
+// largest that is left, the lower index first among equal ones.  Latency of dependent f64 steps (exp, sums and
+// maxima over the lanes, `top` of these one after another): 3.3 us for 8 of 128, 4.1 for 8 of 256, of
+// which 1.8 is the launch.
 template <int PER>
 __global__ void __launch_bounds__(64) moe_top_kernel(const double *logits, const float *bias, int sigmoid, int renorm,
                                                      float scale, int32_t *ids, float *weights, int top, int e)
@@ -298,12 +302,11 @@ constexpr int kMoeEntries = (int)kMaxExperts + kMoePairs / 8;
 // one of class 1, more of them entries of sixteen (of eight, class 1, where rows come as three
 // parts: sixteen such rows take the LDS of two workgroups).  begin[c] is class c's first entry,
 // begin[3] their number; entries stand in ascending order of the experts within
-// a class.  A token that names an expert twice counts once, with the sum of its weights.
+// a class.  A token that names an expert twice is one pair.
 struct MoePlan {
     int32_t begin[4];
     uint32_t entry[kMoeEntries]; // expert | first pair << 10 | pairs << 21
     uint16_t row[kMoePairs];     // per pair: its row in h, token * top + the first slot of that expert
-    float weight[kMoePairs];
 };
 
 struct MoeEntry {
@@ -319,7 +322,7 @@ struct MoeEntry {
 };
 static_assert(kMaxExperts <= 1024 && kMoePairs <= 2048, "the fields of an entry");
 
-// The gated products between the two kernels: two bf16 parts of each where the
+// The gated products between the two: two bf16 parts of each where the
 // stream has 16 bits (what is left out is below 2^-17 of the value, against 2^-9 and 2^-12 of
 // the outputs' own rounding), three (all 24 bits) where it is f32.  The parts are what the
 // matrix core reads, so the down kernel's waves load them as they stand: splitting
@@ -339,8 +342,9 @@ struct MoeArgs {
     uint8_t *x_parts; // f32 rows as three bf16 parts, [part][m][k] (in the same place, before them)
 };
 
-// One workgroup makes the plan; threads are experts, then pairs.
-__device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weights, int m, int top, int e, bool wide, MoePlan &plan)
+// One workgroup makes the plan; threads are experts, then pairs.  Latency of its five steps: 3.8 to 5 us (made by
+// the choice's workgroup instead, one for all tokens, both take 10.7 against 4.6 + 4.9).
+__device__ __forceinline__ void moe_plan(const int32_t *ids, int m, int top, int e, bool wide, MoePlan &plan)
 {
     __shared__ unsigned long long chose[kMaxExperts]; // tokens that named it
     __shared__ unsigned long long sums[16];
@@ -390,17 +394,13 @@ __device__ __forceinline__ void moe_plan(const int32_t *ids, const float *weight
         for (int j = t * top; j < i; j++)
             once = once && id[j] != v;
         if (once) {
-            float w = 0.0f;
-            for (int j = i; j < (t + 1) * top; j++)
-                w += id[j] == v ? weights[j] : 0.0f;
             const int p = first[v] + __builtin_popcountll(chose[v] & ((1ull << t) - 1));
             plan.row[p] = (uint16_t)i;
-            plan.weight[p] = w;
         }
     }
 }
 
-__global__ void __launch_bounds__(1024) moe_plan_kernel(MoeArgs a) { moe_plan(a.ids, a.weights, a.m, a.top, a.e, a.dtype == QLL_W_F32, *a.plan); }
+__global__ void __launch_bounds__(1024) moe_plan_kernel(MoeArgs a) { moe_plan(a.ids, a.m, a.top, a.e, a.dtype == QLL_W_F32, *a.plan); }
 
 __device__ __forceinline__ void store_part(uint8_t *h, int64_t at, float v)
 {
@@ -532,6 +532,11 @@ __device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry
     }
 }
 
+// The products of entry blockIdx.y.  What bounds them is the experts' weights: one token, two experts of 3 x 14336 x
+// 4096 gate and up in 23 to 26 us (122 MB, 4.7 to 5.3 TB/s); 64 tokens, six of 64 experts of 3 x 1536 x 4096, 81 to 86
+// us (418 MB, 4.9 to 5.2 TB/s) and down 52 to 56 (3.7 to 4.0).  37 f32 tokens, three of 23 experts of 3 x 1440 x 2592, take
+// 50 us (99 MB, 2.0 TB/s) and 25: three parts a value are three times the matrix instructions
+// (busy 30% of the time) and LDS reads.
 template <int TX, int GRP, bool GATED, int KIND>
 __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
 {
@@ -557,7 +562,9 @@ __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
     }
 }
 
-// The weighted sum of a token's choices, in their order, and the residual: four columns a thread.
+// The weighted sum of a token's choices, in their order, and the residual: four columns a thread.  The
+// choices' order makes results repeat, where atomic additions would not.  64 x 6 x 4096: 4.8 us (8 MB, mostly
+// latency).
 __global__ void __launch_bounds__(256) moe_combine_kernel(MoeArgs a)
 {
     const int64_t column = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, j = column < a.k ? column : 0; // whole waves stay
@@ -598,7 +605,9 @@ constexpr int kDownWaves = 16;
 
 // One token's down products of 16 rows, weighted and added up.  The pieces of its choices' matrices'
 // rows, one choice after another, are one sequence that the waves share evenly, with
-// loads in flight across the choices' ends; at such an end a wave adds its weighted products.
+// loads in flight across the choices' ends; at such an end a wave adds its weighted products.  Two experts of
+// 14336 -> 4096: 16 us (61 MB, 3.7 TB/s), 16 waves a row tile that wait a third of their time to issue; eight of
+// 1024 -> 2048 6 to 7 us, latency.
 template <int TX, int GRP>
 __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
 {

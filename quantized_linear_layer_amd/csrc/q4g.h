@@ -12,7 +12,7 @@
 //           weights 32 j + 8 (l / 16) + 0..7 of the tile, number 2 p at bits 4 p, number
 //           2 p + 1 at bits 16 + 4 p, so that a shift and a mask give two neighbours in
 //           the halves of a register
-//   scales  for chunks of 512 weights (index ks, KS = ceil(k / 512)), 16 rows a chunk and 512 / g
+//   scales  for pieces of 512 weights (index ks, KS = ceil(k / 512)), 16 rows a piece and 512 / g
 //           scales a row: 1024 / g bytes at (rt * KS + ks) * 16 + row
 //   zeros   the same with 4 bits each, lowest first: 256 / g bytes a row
 // One wave-wide load of 16 bytes a lane fetches a tile without a gap, and it is four
@@ -31,7 +31,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 constexpr int kQ4gBf16 = 1, kQ4gZeros = 2; // the ABI's QLL_Q4G_*
 
 struct Q4gShape {
-    int64_t rt, kt, ks;                     // tiles of 16 rows, of 128 weights, chunks of 512
+    int64_t rt, kt, ks;                     // tiles of 16 rows, of 128 weights, pieces of 512
     int64_t scales, zeros, bytes;           // byte offsets of the regions, and the end
     __host__ __device__ Q4gShape(int64_t n, int64_t k, int64_t group, int fmt)
         : rt((n + 15) / 16), kt((k + 127) / 128), ks((k + 511) / 512)

@@ -38,24 +38,7 @@ struct CodeBlocks {
     }
 };
 
-template <class Codes>
-__global__ void __launch_bounds__(256) q4g_pack_codes_kernel(Codes codes, uint8_t *wp, int64_t tile0, int64_t tiles,
-                                                             int64_t kt, int64_t n, int64_t k)
-{
-    const int64_t tile = tile0 + (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    if (tile >= tile0 + tiles)
-        return;
-    const int lane = threadIdx.x % 64;
-    const int64_t row = tile / kt * 16 + lane % 16, t = tile % kt * 128 + lane / 16 * 8;
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (row < n && t + 32 * j < k)
-            v[j] = codes.eight(row, t + 32 * j, k);
-    *reinterpret_cast<u32x4 *>(wp + tile * 1024 + lane * 16) = v;
-}
-
-// Scales (and zeros) of one row and chunk of 512 weights a thread.
+// Where the scales come from, and the zero points.
 struct ScaleArray {
     const uint16_t *scales;
     const uint8_t *zeros;
@@ -71,20 +54,32 @@ struct ScaleBlocks {
     __device__ uint32_t zero(int64_t, int64_t, int64_t) const { return 0; }
 };
 
-template <class Scales>
-__global__ void __launch_bounds__(256) q4g_pack_scales_kernel(Scales from, uint8_t *scales, uint8_t *zeros,
-                                                              int64_t item0, int64_t items, int64_t ks, int64_t n,
-                                                              int64_t groups, int group)
+// A tile of codes.
+template <class Codes>
+__device__ __forceinline__ void pack_codes(const Codes &codes, uint8_t *wp, const Q4gShape &sh, int64_t tile, int64_t n,
+                                           int64_t k)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= items)
-        return;
-    const int64_t item = item0 + i, row = item / 16 / ks * 16 + item % 16, chunk = item / 16 % ks;
+    const int lane = threadIdx.x % 64;
+    const int64_t row = tile / sh.kt * 16 + lane % 16, t = tile % sh.kt * 128 + lane / 16 * 8;
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (row < n && t + 32 * j < k)
+            v[j] = codes.eight(row, t + 32 * j, k);
+    *reinterpret_cast<u32x4 *>(wp + tile * 1024 + lane * 16) = v;
+}
+
+// Scales (and zero points) of one row and 512 weights.
+template <class Scales>
+__device__ __forceinline__ void pack_scales(const Scales &from, uint8_t *scales, uint8_t *zeros, int64_t ks, int64_t item,
+                                            int64_t n, int64_t groups, int group)
+{
+    const int64_t row = item / 16 / ks * 16 + item % 16, piece = item / 16 % ks;
     const int per = 512 / group;
     uint16_t *s = reinterpret_cast<uint16_t *>(scales) + item * per;
     uint64_t z = 0;
     for (int g = 0; g < per; g++) {
-        const int64_t at = chunk * per + g;
+        const int64_t at = piece * per + g;
         const bool in = row < n && at < groups;
         s[g] = in ? (uint16_t)from.scale(row, at, groups) : (uint16_t)0;
         if (zeros && in)
@@ -95,20 +90,33 @@ __global__ void __launch_bounds__(256) q4g_pack_scales_kernel(Scales from, uint8
             zeros[item * (per / 2) + b] = (uint8_t)(z >> (8 * b));
 }
 
+// The first workgroups pack the codes, a tile a wave, the others the scales, an item a thread: one
+// launch, as many a small matrix is packed (an expert's, one at a time).  Its reads and writes bound it.
+template <class Codes, class Scales>
+__global__ void __launch_bounds__(256) q4g_pack_kernel(Codes codes, Scales from, uint8_t *wp, int64_t first, int64_t n,
+                                                       int64_t k, int group, int fmt)
+{
+    const Q4gShape sh(n, k, group, fmt);
+    const int64_t tiles = sh.rt * sh.kt, block = first + blockIdx.x, code_blocks = (tiles + 3) / 4;
+    if (block < code_blocks) {
+        const int64_t tile = block * 4 + threadIdx.x / 64;
+        if (tile < tiles)
+            pack_codes(codes, wp, sh, tile, n, k);
+    } else {
+        const int64_t item = (block - code_blocks) * 256 + threadIdx.x;
+        if (item < sh.rt * sh.ks * 16)
+            pack_scales(from, wp + sh.scales, (fmt & kQ4gZeros) ? wp + sh.zeros : nullptr, sh.ks, item, n, k / group, group);
+    }
+}
+
 template <class Codes, class Scales>
 hipError_t pack(const Codes &codes, const Scales &from, int64_t group, int fmt, uint8_t *wp, int64_t n, int64_t k,
                 hipStream_t s)
 {
     const Q4gShape sh(n, k, group, fmt);
-    hipError_t e = launch_parts(sh.rt * sh.kt, kPartThreads / 64, [&](int64_t first, int64_t count) {
-        q4g_pack_codes_kernel<<<(unsigned)((count + 3) / 4), 256, 0, s>>>(codes, wp, first, count, sh.kt, n, k);
-    });
-    if (e != hipSuccess)
-        return e;
-    return launch_parts(sh.rt * sh.ks * 16, kPartThreads, [&](int64_t first, int64_t count) {
-        q4g_pack_scales_kernel<<<(unsigned)((count + 255) / 256), 256, 0, s>>>(
-            from, wp + sh.scales, (fmt & kQ4gZeros) ? wp + sh.zeros : nullptr, first, count, sh.ks, n, k / group,
-            (int)group);
+    const int64_t blocks = (sh.rt * sh.kt + 3) / 4 + (sh.rt * sh.ks * 16 + 255) / 256;
+    return launch_parts(blocks, kPartThreads / 256, [&](int64_t first, int64_t count) {
+        q4g_pack_kernel<<<(unsigned)count, 256, 0, s>>>(codes, from, wp, first, n, k, (int)group, fmt);
     });
 }
 
@@ -168,7 +176,12 @@ __device__ __forceinline__ void q4g_outputs(const Q4gLinear &a, const float (&y)
 }
 
 // Few activation rows, or a small product: the waves of a set share its row tiles' pieces of k;
-// groups of 16 / PK activation rows along y.
+// groups of 16 / PK activation rows along y.  Four steps an operand while there are four rows, each wave
+// fetching them: 4096 -> 14336, one row, 7.7 us (31 MB, 4.0 TB/s; loading alone would take 6.1): memory, with
+// waves that wait a third of their time to issue.  512 -> 512 takes 4.1 us, of which 1.8 is an empty
+// launch's and the rest one trip to memory for a wave, the sums and the store.  1440 -> 4099 on 37 rows of f32 13 us:
+// three groups read the codes, and a wave's 144 matrix instructions and 1856 others wait for
+// one tile at a time (more in flight takes more registers than two workgroups a CU leave).
 template <int TX, int GRP, int RTN, int PK, int D>
 __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 {
@@ -196,6 +209,13 @@ __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 
 // More rows.  Workgroups eight apart land on the same XCD: those of one set of rows follow
 // each other there, so that its weights stay in that L2.
+//
+// 16 rows, 14336 -> 4096: 13.5 us (33 MB, 2.4 TB/s), 2 to 4 to add up the parts; four waves a SIMD that wait for
+// memory and for instructions to issue, each weight widened for one operand of 16 rows.  512 rows, 4096 ->
+// 14336: 118 us (510 TFLOP/s, the matrix cores busy a quarter of the time): 6990 vector instructions a wave against
+// 1024 of the matrix core, which widen the codes (two for two weights, again in each of the eight workgroups that
+// share them) and scale each group's sum.  64 x 32 outputs a wave are what 256 registers hold: 64 x 64 takes
+// 303 us (spills), 16 x 64 152; without activation loads it takes 99, without codes' 116, loads alone 68.
 template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
 __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
 {
@@ -229,7 +249,8 @@ __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
 
 constexpr int kMaxParts = 8; // of k, over workgroups
 
-// The parts of k added up in order, and the epilogue.
+// The parts of k added up in order, and the epilogue: eight loads at once an output, bound by that trip to
+// memory (16 x 4096 outputs 2 to 4 us).
 __global__ void __launch_bounds__(256) q4g_finish_kernel(Q4gLinear a, int64_t first, int64_t count)
 {
     const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -249,7 +270,8 @@ __global__ void __launch_bounds__(256) q4g_finish_kernel(Q4gLinear a, int64_t fi
     store_as(a.y, i, v, a.y_dtype);
 }
 
-// f32 rows as three bf16 parts [part][count], eight values a thread.
+// f32 rows as three bf16 parts [part][count], eight values a thread: split once, not by every wave that reads
+// them (37 x 2592: 2.5 to 4.8 us, launch and memory latency).
 __global__ void __launch_bounds__(256) q4g_split_kernel(const uint8_t *x, uint8_t *parts, int64_t first, int64_t eights,
                                                         int64_t count)
 {
