@@ -651,9 +651,9 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
             if (i + 1 < f1) {
                 if (end)
                     enter(choice + 1);
-                w.template use_piece<true>(f, p, f, after, bf16, lane); // four tiles in flight: f is the next one's
+                w.template use_piece<true, false>(f, p, f, after, bf16, lane); // four tiles in flight: f is the next one's
             } else
-                w.template use_piece<false>(f, p, f, 0, bf16, lane);
+                w.template use_piece<false, false>(f, p, f, 0, bf16, lane);
             if (end || i + 1 == f1) {
                 sum = fmaf(weights[choice], w.y[0][0][0], sum);
                 w.clear();

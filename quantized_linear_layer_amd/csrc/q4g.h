@@ -363,8 +363,9 @@ struct Q4gWave : Q4gTile<TX, GRP, RTN, 1, PK> {
         for (int j = 0; j < D; j++)
             load(slot[j], f, 4 * piece + j, lane);
     }
-    // Piece `piece` of `now_f`; MORE: with the loads of the one after it, piece `after` of f.
-    template <bool MORE>
+    // Piece `piece` of `now_f`; MORE: with the loads of the one after it, piece `after` of f.  WHOLE: it has
+    // all four tiles (a branch around a tile costs copies of the sums).
+    template <bool MORE, bool WHOLE>
     __device__ __forceinline__ void use_piece(const From &now_f, int piece, const From &f, int after, bool bf16, uint32_t lane)
     {
         const Piece now = next;
@@ -374,7 +375,7 @@ struct Q4gWave : Q4gTile<TX, GRP, RTN, 1, PK> {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             Slot &s = slot[j % D];
-            if (j < tiles) {
+            if (WHOLE || j < tiles) {
                 u32x4 x[kQuads][Tile::P];
 #pragma unroll
                 for (int q = 0; q < kQuads; q++) {
@@ -402,8 +403,8 @@ struct Q4gWave : Q4gTile<TX, GRP, RTN, 1, PK> {
             return;
         start(f, p0, lane);
         for (int p = p0; p + 1 < p1; p++)
-            use_piece<true>(f, p, f, p + 1, bf16, lane);
-        use_piece<false>(f, p1 - 1, f, 0, bf16, lane);
+            use_piece<true, true>(f, p, f, p + 1, bf16, lane);
+        use_piece<false, false>(f, p1 - 1, f, 0, bf16, lane);
     }
 };
 
@@ -477,7 +478,8 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
         asm volatile("" ::: "memory");
     }
 
-    // A piece; MORE: with the loads of the piece `after` it.
+    // A piece; MORE: with the loads of the piece `after` it (then it has all four tiles; a branch around
+    // a tile costs copies of the sums).
     template <bool MORE>
     __device__ __forceinline__ void use_piece(u32x4 (&codes)[D][RTN], Piece &next, const Q4gRows (&w)[RTN], int piece,
                                               int after, int kt, const uint8_t *at, bool bf16, uint32_t lane)
@@ -487,7 +489,7 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
             Tile::load_piece(next, w, after, lane);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            if (4 * piece + j < kt)
+            if (MORE || 4 * piece + j < kt)
                 Tile::use(codes[j % D], now, j, [&](int q, int c, int p) {
                     return *reinterpret_cast<const u32x4 *>(at + j * kTileBytes + ((q * C + c) * P + p) * 1024);
                 }, bf16);
@@ -503,11 +505,11 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
     // Chunks [x0, x1) of the activations.  The wave is part kw of KW (which divides kPieces) of the
     // ones on its row tiles.  Every wave of the workgroup calls it alike; `busy` is false
     // for one that has no rows.  staged: the one chunk is in LDS already; else all waves are done with LDS.
-    // Nothing is asked for that is not used: the load path is what bounds short rows.
+    // Next to nothing is asked for that is not used: the load path is what bounds short rows.
     __device__ __forceinline__ void run(const Q4gRows (&w)[RTN], bool busy, const X &src, int x0, int x1, int kw, int KW,
                                         bool bf16, bool staged, const uint8_t *lds, uint32_t lane)
     {
-        const int kt = (src.k + 127) / 128, per = kPieces / KW;
+        const int kt = (src.k + 127) / 128, per = kPieces / KW, last = x1 - 1;
         const int whole = (src.k + 511) / 512, ks = x1 * kPieces < whole ? x1 * kPieces : whole; // pieces end here
         const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)lds;
         u32x4 codes[D][RTN];
@@ -524,25 +526,28 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
         }
         if (!staged)
             arrive(some && D == 4);
-        for (int xc = x0; xc < x1; xc++) {
-            if (xc + 1 < x1)
-                fetch_x(src, xc + 1, base + ((xc - x0 + 1) & 1) * kBuffer, lane);
-            bool more = false;
-            for (int r = 0; r < per; r++) {
-                piece = xc * kPieces + kw * per + r;
-                if (!busy || piece >= ks)
-                    break;
-                const int after = r + 1 < per ? piece + 1 : (xc + 1) * kPieces + kw * per;
-                const uint8_t *at = lds + ((xc - x0) & 1) * kBuffer + (kw * per + r) * 4 * kTileBytes + lane * 16;
-                more = after < ks;
-                if (more)
-                    use_piece<true>(codes, next, w, piece, after, kt, at, bf16, lane);
-                else
-                    use_piece<false>(codes, next, w, piece, after, kt, at, bf16, lane);
-            }
-            if (xc + 1 < x1)
-                arrive(more);
+        const uint8_t *at = lds + kw * per * 4 * kTileBytes + lane * 16;
+        for (int xc = x0; xc < last; xc++) { // whole chunks
+            fetch_x(src, xc + 1, base + ((xc - x0 + 1) & 1) * kBuffer, lane);
+            if (busy)
+                for (int r = 0; r < per; r++) {
+                    piece = xc * kPieces + kw * per + r;
+                    int after = r + 1 < per ? piece + 1 : (xc + 1) * kPieces + kw * per;
+                    after = after < ks ? after : ks - 1; // a wave without a piece in the last chunk: not used
+                    use_piece<true>(codes, next, w, piece, after, kt, at + ((xc - x0) & 1) * kBuffer + r * 4 * kTileBytes, bf16,
+                                    lane);
+                }
+            arrive(busy);
         }
+        piece = last * kPieces + kw * per;
+        if (!busy || piece >= ks)
+            return;
+        const int end = piece + per < ks ? piece + per : ks;
+        at += ((last - x0) & 1) * kBuffer;
+        if constexpr (kPieces > 1)
+            for (; piece + 1 < end; piece++, at += 4 * kTileBytes)
+                use_piece<true>(codes, next, w, piece, piece + 1, kt, at, bf16, lane);
+        use_piece<false>(codes, next, w, piece, 0, kt, at, bf16, lane);
     }
 };
 
