@@ -500,7 +500,7 @@ __device__ __forceinline__ void moe_few(const MoeArgs &a, const MoeEntry &entry,
 template <int TX, int GRP, int PK, bool GATED>
 __device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry, uint8_t *lds)
 {
-    using Block = Q4gBlock<TX, GRP, 1, 1, PK, 4>;
+    using Block = Q4gBlock<TX, GRP, 1, 1, PK>;
     const int64_t outs = GATED ? a.n : a.k;
     const int k = (int)(GATED ? a.k : a.n);
     const Q4gShape sh(outs, k, GRP, a.fmt);
@@ -704,8 +704,8 @@ hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
     const int64_t most = (tiles * a.kw + 7) / 8, want = (4096 + active - 1) / active;
     int64_t lds = (GATED ? 2 : 1) * 8 * 64 * sizeof(float);
     if constexpr (KIND == MOE_ALL) { // whichever of the classes takes most
-        using B2 = Q4gBlock<TX, GRP, 1, 1, 2, 4>;
-        using B1 = Q4gBlock<TX, GRP, 1, 1, 1, 4>;
+        using B2 = Q4gBlock<TX, GRP, 1, 1, 2>;
+        using B1 = Q4gBlock<TX, GRP, 1, 1, 1>;
         const int64_t x1 = a.m <= 8 || TX == Q4G_X_PARTS3 ? 0 : B1::lds_bytes(k);
         lds = 4 * lds + (B2::lds_bytes(k) > x1 ? B2::lds_bytes(k) : x1);
     }

@@ -425,7 +425,7 @@ __device__ __forceinline__ void lds_operand16(const uint8_t *base, uint32_t off,
 // clock and CU whatever cache they come from (14336 -> 4096, 16 rows: 19 us, with the operands
 // left out 10).  Waves take row tiles, or parts of every chunk of activations: kChunk
 // elements of T rows, which loads straight into LDS bring in while the chunk before it is in use.
-template <int TX, int GRP, int RTN, int C, int PK, int D>
+template <int TX, int GRP, int RTN, int C, int PK>
 struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
     using Tile = Q4gTile<TX, GRP, RTN, C, PK>;
     using Piece = typename Tile::Piece;
@@ -478,10 +478,10 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
         asm volatile("" ::: "memory");
     }
 
-    // A piece; MORE: with the loads of the piece `after` it (then it has all four tiles; a branch around
+    // A piece, whose four tiles are in flight; MORE: with the loads of the piece `after` it (then it has all four tiles; a branch around
     // a tile costs copies of the sums).
     template <bool MORE>
-    __device__ __forceinline__ void use_piece(u32x4 (&codes)[D][RTN], Piece &next, const Q4gRows (&w)[RTN], int piece,
+    __device__ __forceinline__ void use_piece(u32x4 (&codes)[4][RTN], Piece &next, const Q4gRows (&w)[RTN], int piece,
                                               int after, int kt, const uint8_t *at, bool bf16, uint32_t lane)
     {
         const Piece now = next;
@@ -490,14 +490,12 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             if (MORE || 4 * piece + j < kt)
-                Tile::use(codes[j % D], now, j, [&](int q, int c, int p) {
+                Tile::use(codes[j], now, j, [&](int q, int c, int p) {
                     return *reinterpret_cast<const u32x4 *>(at + j * kTileBytes + ((q * C + c) * P + p) * 1024);
                 }, bf16);
             __builtin_amdgcn_sched_barrier(0);
-            if (MORE || j + D < 4) {
-                const int t = j + D < 4 ? 4 * piece + j + D : 4 * after + j + D - 4;
-                Tile::load_tile(codes[j % D], w, t < kt ? t : kt - 1, lane);
-            }
+            if (MORE)
+                Tile::load_tile(codes[j], w, 4 * after + j < kt ? 4 * after + j : kt - 1, lane);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -512,7 +510,7 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
         const int kt = (src.k + 127) / 128, per = kPieces / KW, last = x1 - 1;
         const int whole = (src.k + 511) / 512, ks = x1 * kPieces < whole ? x1 * kPieces : whole; // pieces end here
         const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)lds;
-        u32x4 codes[D][RTN];
+        u32x4 codes[4][RTN];
         Piece next;
         if (!staged)
             fetch_x(src, x0, base, lane);
@@ -521,11 +519,11 @@ struct Q4gBlock : Q4gTile<TX, GRP, RTN, C, PK> {
         if (some) {
             Tile::load_piece(next, w, piece, lane);
 #pragma unroll
-            for (int i = 0; i < D; i++)
+            for (int i = 0; i < 4; i++)
                 Tile::load_tile(codes[i], w, 4 * piece + i < kt ? 4 * piece + i : kt - 1, lane);
         }
         if (!staged)
-            arrive(some && D == 4);
+            arrive(some);
         const uint8_t *at = lds + kw * per * 4 * kTileBytes + lane * 16;
         for (int xc = x0; xc < last; xc++) { // whole chunks
             fetch_x(src, xc + 1, base + ((xc - x0 + 1) & 1) * kBuffer, lane);

@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 // 1024 of the matrix core, which widen the codes (two for two weights, again in each of the eight workgroups that
 // share them) and scale each group's sum.  64 x 32 outputs a wave are what 256 registers hold: 64 x 64 takes
 // 303 us (spills), 16 x 64 152; without activation loads it takes 99, without codes' 116, loads alone 68.
-template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
+template <int TX, int GRP, int RTN, int C, int PK, int WPS>
 __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
 {
-    using Block = Q4gBlock<TX, GRP, RTN, C, PK, D>;
+    using Block = Q4gBlock<TX, GRP, RTN, C, PK>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const Q4gShape sh(a.n, a.k, GRP, a.fmt);
     const int lane = threadIdx.x % 64, wave = wave_number(), kw = wave % a.kw;
@@ -287,15 +287,19 @@ __global__ void __launch_bounds__(256) q4g_split_kernel(const uint8_t *x, uint8_
 }
 
 // Whether a product takes the waves that fetch their own activations, in one launch and without a
-// workspace: up to four rows; while the codes that all groups of 16 rows read are few (us, so and with
-// the rows in LDS: 14336 x 4096, 8 rows 10.2 and 14.3, 64 rows 39 and 55, 128 rows 70 and 55; 4096 x 4096,
-// 256 rows 38 and 54; f32, 14336 x 4096, 32 rows 36 and 39, 33 rows 46 and 45), but on short and wide matrices
-// with 9 to 16 rows, where four operands a tile are too much (4096 x 14336, 16 rows 19.2 and 14.4).
+// workspace: up to four rows; up to 16 while the codes are few (us, so and with the rows in LDS: 14336 x 4096, 16
+// rows 13.9 and 16.6, f32 21 and 25; 32000 x 4096, 22 and 25, f32 49 and 42), but on short and wide matrices
+// with 9 to 16 rows, where four operands a tile are too much (4096 x 14336, 16 rows 19.1 and 14.1); with more
+// rows while the codes that all groups of 16 rows read are few (4096 x 4096, 96 rows 17.9 and 19.4, 128 rows 21.1 and 19.8,
+// f32 32 rows 12.4 and 14.7, 64 rows 20.3 and 18.5; 2048 x 2048, 256 rows 13.1 and 15.3; 14336 x 4096, 17 rows 18.6
+// and 18.2, 64 rows 39 and 27).
 bool q4g_small(bool wide, int64_t m, int64_t n, int64_t k)
 {
-    if (m > 8 && m <= 16 && n < 8192 && n * k > (int64_t)1 << 25)
-        return false;
-    return m <= 4 || (m + 15) / 16 <= ((int64_t)1 << (wide ? 27 : 28)) / (n * k);
+    if (m <= 4)
+        return true;
+    if (m <= 16)
+        return !(m > 8 && n < 8192 && n * k > (int64_t)1 << 25) && n * k <= (int64_t)1 << (wide ? 27 : 28);
+    return (m + 15) / 16 <= ((int64_t)3 << (wide ? 24 : 25)) / (n * k);
 }
 
 // How another product is split: T activation rows and `tiles` row tiles a wave, kw
@@ -326,17 +330,19 @@ Q4gSplit q4g_split(bool wide, int64_t m, int64_t n, int64_t k)
             s.parts *= 2;
         return s;
     }
-    // More rows: the sets of a workgroup and the parts of k by what their rounds of workgroups cost, in us:
-    // a chunk takes some 6 us at eight sets of 64 rows, where a quarter is the activations' and the wait's,
-    // and the parts are written, read and added up by another launch.
-    const double unit = 0.6 * s.rows / 64 * (wide ? 3 : 1);
+    // More rows: the sets of a workgroup and the parts of k by what their rounds of workgroups cost, in us.  A
+    // chunk takes 5.8, 5.3, 5.2, 6.5 us at one, two, four, eight sets of 64 rows and 4.0, 3.5, 3.4, 4.2 of 32 or of
+    // three parts, as its loads and the wait for them are most of it; the parts are written, read
+    // and added up by another launch (128 rows, 4096 x 4096, one set of all k 49 us, eight 53, four in four parts 20).
+    constexpr double kSetCost[9] = {0, 5.8, 5.3, 0, 5.2, 0, 0, 0, 6.5};
+    const double unit = s.rows == 64 ? 1.0 : 0.65;
     const int64_t at_once = s.rows == 32 ? 512 : 256;
     double least = 0;
     for (int parts = 1; parts <= kMaxParts && parts <= chunks; parts *= 2)
         for (int w = 8; w >= 1; w /= 2) {
             const int64_t groups = (rt + s.tiles * w - 1) / (s.tiles * w) * ((m + s.rows - 1) / s.rows) * parts;
-            const double cost = (double)((groups + at_once - 1) / at_once * ((chunks + parts - 1) / parts)) * unit * (w + 2) +
-                                (parts > 1 ? 4 + parts * m * n * 2e-6 : 0);
+            const double cost = (double)((groups + at_once - 1) / at_once * ((chunks + parts - 1) / parts)) * unit * kSetCost[w] +
+                                (parts > 1 ? 3 + parts * m * n * 2.3e-6 : 0);
             if (least == 0 || cost < least)
                 least = cost, s.sets = w, s.parts = parts;
         }
@@ -371,10 +377,10 @@ hipError_t linear_few(Q4gLinear a, hipStream_t s)
     return e;
 }
 
-template <int TX, int GRP, int RTN, int C, int PK, int D, int WPS>
+template <int TX, int GRP, int RTN, int C, int PK, int WPS>
 hipError_t linear_c(Q4gLinear a, const Q4gSplit &split, hipStream_t s)
 {
-    using Block = Q4gBlock<TX, GRP, RTN, C, PK, D>;
+    using Block = Q4gBlock<TX, GRP, RTN, C, PK>;
     a.kw = split.kw, a.rw = split.sets, a.parts = split.parts;
     const int64_t sets = ((a.n + 15) / 16 + RTN * a.rw - 1) / (RTN * a.rw), threads = 64 * a.kw * a.rw;
     const size_t sums = a.kw > 1 ? (size_t)8 * RTN * C * Block::N * 64 * sizeof(float) : 0;
@@ -388,7 +394,7 @@ hipError_t linear_c(Q4gLinear a, const Q4gSplit &split, hipStream_t s)
         e = launch_parts(sets, kPartThreads / (threads * gn) / 8 * 8, [&](int64_t first, int64_t count) {
             a.row0 = first;
             const dim3 grid((unsigned)((count + 7) / 8 * 8 * gn), (unsigned)a.parts);
-            q4g_linear_kernel<TX, GRP, RTN, C, PK, D, WPS><<<grid, (unsigned)threads, lds, s>>>(a);
+            q4g_linear_kernel<TX, GRP, RTN, C, PK, WPS><<<grid, (unsigned)threads, lds, s>>>(a);
         });
     }
     if (e != hipSuccess || a.parts == 1)
@@ -402,13 +408,13 @@ template <int TX, int GRP>
 hipError_t linear_more(const Q4gLinear &a, const Q4gSplit &split, hipStream_t s)
 {
     if (split.rows == 8)
-        return linear_c<TX, GRP, 1, 1, 2, 4, 4>(a, split, s);
+        return linear_c<TX, GRP, 1, 1, 2, 4>(a, split, s);
     if constexpr (TX == Q4G_X_PARTS3)
-        return linear_c<TX, GRP, 2, 1, 1, 4, 2>(a, split, s);
+        return linear_c<TX, GRP, 2, 1, 1, 2>(a, split, s);
     else
-        return split.tiles == 1   ? linear_c<TX, GRP, 1, 1, 1, 4, 4>(a, split, s)
-               : split.rows == 32 ? linear_c<TX, GRP, 2, 2, 1, 2, 2>(a, split, s)
-                                  : linear_c<TX, GRP, 2, 4, 1, 2, 2>(a, split, s);
+        return split.tiles == 1   ? linear_c<TX, GRP, 1, 1, 1, 4>(a, split, s)
+               : split.rows == 32 ? linear_c<TX, GRP, 2, 2, 1, 2>(a, split, s)
+                                  : linear_c<TX, GRP, 2, 4, 1, 2>(a, split, s);
 }
 
 template <int TX, int GRP>
