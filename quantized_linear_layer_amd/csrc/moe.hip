@@ -533,9 +533,9 @@ __device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry
 }
 
 // The products of entry blockIdx.y.  What bounds them is the experts' weights: one token, two experts of 3 x 14336 x
-// 4096 gate and up in 23 to 26 us (122 MB, 4.7 to 5.3 TB/s); 64 tokens, six of 64 experts of 3 x 1536 x 4096, 81 to 86
-// us (418 MB, 4.9 to 5.2 TB/s) and down 52 to 56 (3.7 to 4.0).  37 f32 tokens, three of 23 experts of 3 x 1440 x 2592, take
-// 50 us (99 MB, 2.0 TB/s) and 25: three parts a value are three times the matrix instructions
+// 4096 gate and up in 23 to 26 us (122 MB, 4.7 to 5.3 TB/s); 64 tokens, six of 64 experts of 3 x 1536 x 4096, 79 to 81
+// us (418 MB, 5.2 TB/s) and down 50 to 55 (3.8 to 4.1).  37 f32 tokens, three of 23 experts of 3 x 1440 x 2592, take
+// 47 to 50 us (99 MB, 2.0 TB/s) and 24 to 27: three parts a value are three times the matrix instructions
 // (busy 30% of the time) and LDS reads.
 template <int TX, int GRP, bool GATED, int KIND>
 __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)

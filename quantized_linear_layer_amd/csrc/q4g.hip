@@ -210,12 +210,12 @@ __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 // More rows.  Workgroups eight apart land on the same XCD: those of one set of rows follow
 // each other there, so that its weights stay in that L2.
 //
-// 16 rows, 14336 -> 4096: 13.5 us (33 MB, 2.4 TB/s), 2 to 4 to add up the parts; four waves a SIMD that wait for
+// 16 rows, 14336 -> 4096: 13 us (33 MB, 2.5 TB/s), 2 to 4 to add up the parts; four waves a SIMD that wait for
 // memory and for instructions to issue, each weight widened for one operand of 16 rows.  512 rows, 4096 ->
-// 14336: 118 us (510 TFLOP/s, the matrix cores busy a quarter of the time): 6990 vector instructions a wave against
-// 1024 of the matrix core, which widen the codes (two for two weights, again in each of the eight workgroups that
-// share them) and scale each group's sum.  64 x 32 outputs a wave are what 256 registers hold: 64 x 64 takes
-// 303 us (spills), 16 x 64 152; without activation loads it takes 99, without codes' 116, loads alone 68.
+// 14336: 97 to 100 us (600 TFLOP/s; 90 back to back): some 5700 vector instructions a wave against 1024 of the matrix
+// core, which widen the codes (nine for eight weights, again in each of the eight workgroups that share them) and
+// scale each group's sum, and a wait for all eight waves every 512 weights.  64 x 32 outputs a wave: 64 x 64
+// takes 106 us and twice as long at 128 rows, 16 x 64 152; sixteen waves at 128 registers spill.
 template <int TX, int GRP, int RTN, int C, int PK, int WPS>
 __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
 {

@@ -176,9 +176,16 @@ LARGE = [("bf16", 8, 70001, 3872, 32), ("f16", 5, 66000, 4160, 64), ("bf16", 16,
          ("f16", 300, 3000, 8288, 32), ("f32", 7, 33000, 4128, 32), ("f32", 8, 32800, 4224, 128),
          ("f32", 12, 1000, 33664, 64), ("f32", 40, 11000, 4192, 32), ("f32", 130, 3700, 4224, 128),
          ("f32", 64, 600, 57472, 64)]
+# The same with 17 rows and more near the sizes where they begin, in one to eight parts of k, with one to
+# eight sets of waves a workgroup, one chunk of k and hundreds.
+MIDDLE = [("bf16", 512, 1800, 1792, 64), ("f16", 500, 6000, 544, 32), ("bf16", 511, 33, 98304, 128),
+          ("f16", 200, 16, 500000, 32), ("bf16", 128, 4099, 3104, 32), ("f16", 100, 20001, 768, 128),
+          ("bf16", 64, 6500, 3904, 64), ("f16", 33, 70000, 512, 32), ("bf16", 17, 14000, 4160, 64),
+          ("bf16", 32, 4000, 14400, 32), ("f32", 512, 1300, 1280, 128), ("f32", 64, 3300, 3840, 32),
+          ("f32", 20, 26000, 1024, 64), ("f32", 100, 129, 57344, 128), ("f32", 257, 3000, 992, 32)]
 
 
-@pytest.mark.parametrize("dtype,m,n,k,group", LARGE)
+@pytest.mark.parametrize("dtype,m,n,k,group", LARGE + MIDDLE)
 def test_rows_in_lds(qll_gpu, dtype, m, n, k, group):
     g = torch.Generator(device="cuda")
     g.manual_seed(m + n)
