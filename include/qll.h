@@ -495,8 +495,9 @@ int qll_q4g_from_q4_0(const void *w, void *wp, int64_t n, int64_t k, void *strea
 /* Y[m][n] = T(act(X.W^T + bias) + residual).  wp: packed weights; x: [m][k] of type dtype
  * (QLL_DTYPE_*); bias: float[n] or NULL; act a QLL_ACT_* value; residual: [m][n] of
  * type y_dtype or NULL, may be y itself; y: [m][n] of type T = y_dtype, rounded once, to
- * nearest even.  Sums are f32: without an epilogue, before that rounding, within
- * 1e-4 * sum_t |x s| (|c - z| + 16) of the exact sum.  |x| < 2^120.  A row of x with
+ * nearest even.  Products are of c - z itself and sums f32: without an epilogue, before that rounding, within
+ * (4 * group + k / group) * 2^-24 * sum_t |x s (c - z)| of the exact sum.  |x| < 2^117, so that a group's sum stays in
+ * f32's range.  A row of x with
  * NaN or an infinity in it has unspecified outputs, other rows do not change.  k % group == 0,
  * k < 2^24 (else QLL_ERR_SHAPE).  ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_LINEAR,
  * m, n, k) bytes (0 where one launch does without, as up to four rows do: ws may be NULL

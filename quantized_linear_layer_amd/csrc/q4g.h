@@ -95,13 +95,12 @@ __device__ __forceinline__ void split3(u32x4 lo, u32x4 hi, u32x4 &a, u32x4 &b, u
 // whose rows were empty.  y[r][c][i] of lane l is activation (l / 16) * 4 / PK + i of group c
 // with row l % 16 of tile r.
 //
-// f32 and bf16 activations: the weight operand is 16 + c as bf16 (exact; two
-// instructions two weights), the group's sum S of activations comes from the same
-// instruction with ones, and s * (D - (16 + z) * S) is the group's part.  The
-// difference loses up to 31 / |c - z| of f32's precision, a few bits of 24 (drawn layers of experts on f32
-// rows are 1.2 times as far from 64 bits as f32 products of dequantized weights are, 4 times at worst).  f32 activations
-// are split exactly into three bf16 parts.  f16 activations: the weights become
-// c - z in f16, exact, by the bits of 1024 + c and one packed subtraction.
+// The weight operand is c - z, exact in bf16 and f16: a weight of 0 adds nothing, however large its
+// activation.  For bf16 that takes 17 instructions for eight weights.  16 + c takes nine, with the group's sum S of
+// activations from the same matrix instruction and D - (16 + z) S as the group's part (4096 -> 14336, one
+// bf16 row: 8.6 us in place of 10.1; from eight rows on the two are alike), but D and S then carry the rounding
+// of an outlier whose own weight is 0 (an outlier 10^4 times the others: 160 times an f32 product's error).
+// f32 activations are split exactly into three bf16 parts.
 //
 // Codes are loaded by tiles of 128 weights, scales and zero points by pieces of 512: loads of
 // a few bytes cost nearly as much as those of 16 (4096 -> 14336, one row: 10.8 us with a load of
@@ -191,13 +190,23 @@ struct Q4gTile {
         asm("" : "+v"(b));
         return (w & m) | b;
     }
-    __device__ __forceinline__ static bf16x8 widen(uint32_t w) // 16 + c of the eight codes
+    // c - z as bf16: 1024 + c as f16 bits (1024 + 16 c where the code is one place up), less 1024 + z (a sixteenth
+    // of it less 64 + z) in f32 by one mixed fma a weight, whose upper half is the bf16.
+    __device__ __forceinline__ static bf16x8 widen(uint32_t w, float less1024, float less64)
     {
-        constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
-        const u32x4 v = {and_or(w << 3, m, b), and_or(w >> 1, m, b), and_or(w >> 5, m, b), and_or(w >> 9, m, b)};
+        constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, b = 0x64006400u;
+        float one = 1.0f, sixteenth = 0.0625f; // opaque: a product with 1 would become a conversion and a sum
+        asm("" : "+s"(one), "+s"(sixteenth));
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const f16x2 p = __builtin_bit_cast(f16x2, and_or(i < 2 ? w : w >> 8, i & 1 ? hi : lo, b));
+            const float by = i & 1 ? sixteenth : one, less = i & 1 ? less64 : less1024;
+            v[i] = upper_halves(fmaf((float)p[0], by, less), fmaf((float)p[1], by, less));
+        }
         return __builtin_bit_cast(bf16x8, v);
     }
-    // c - z: 1024 + c as f16 bits at a nibble's place, 1024 + 16 c one place up
+    // c - z as f16: the same bits, one packed subtraction or fma for two weights
     __device__ __forceinline__ static f16x8 widen16(uint32_t w, uint32_t z)
     {
         constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, b = 0x64006400u;
@@ -226,7 +235,6 @@ struct Q4gTile {
     __device__ __forceinline__ void use(const u32x4 (&codes)[RTN], const Piece &piece, int j, const X &operand, bool bf16)
     {
         const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
-        const u32x4 one = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
         uint32_t which = bf16 ? ~0u : 0u;
         asm("" : "+v"(which));
         // a quad's operands are asked for while the one before it is multiplied
@@ -239,11 +247,10 @@ struct Q4gTile {
                     xs[q & 1][c][p] = operand(q, c, p);
         };
         ask(0);
-        f32x4 sum[C];
 #pragma unroll
         for (int g = 0; g < kGroups; g++) {
             const int number = j * kGroups + g; // of the piece's groups
-            float s[RTN], z16[RTN]; // the scale, and 16 + z by its bits
+            float s[RTN];
             uint32_t z[RTN];
 #pragma unroll
             for (int r = 0; r < RTN; r++) {
@@ -252,7 +259,6 @@ struct Q4gTile {
                 const uint32_t as_f16 = __builtin_bit_cast(uint32_t, half_bits_to_float(number & 1 ? pair >> 16 : pair));
                 s[r] = __builtin_bit_cast(float, (as_bf16 & which) | (as_f16 & ~which)); // one instruction, no branch
                 z[r] = (piece.zero[r][number / 8] >> (4 * (number & 7))) & 15u;
-                z16[r] = __builtin_bit_cast(float, z[r] << 19 | 0x41800000u);
             }
             f32x4 d[RTN][C][PK];
 #pragma unroll
@@ -270,16 +276,11 @@ struct Q4gTile {
                             d[r][c][b] = mul16(x[c][0], w, e < PK ? none : d[r][c][b]);
                     }
                 } else {
-                    if (step % PK == 0) // a new quad: the sums of its steps, on top of the group's so far
-#pragma unroll
-                        for (int c = 0; c < C; c++)
-#pragma unroll
-                            for (int p = P - 1; p >= 0; p--) // small parts first
-                                sum[c] = mul(x[c][p], __builtin_bit_cast(bf16x8, one),
-                                             e == 0 && p == P - 1 ? none : sum[c]);
 #pragma unroll
                     for (int r = 0; r < RTN; r++) {
-                        const bf16x8 w = widen(codes[r][step]);
+                        const float less1024 = __builtin_bit_cast(float, 0xc4800000u | z[r] << 13); // by their bits
+                        const float less64 = __builtin_bit_cast(float, 0xc2800000u | z[r] << 17);
+                        const bf16x8 w = widen(codes[r][step], less1024, less64);
 #pragma unroll
                         for (int c = 0; c < C; c++)
 #pragma unroll
@@ -297,14 +298,10 @@ struct Q4gTile {
                 for (int i = 0; i < N; i++)
 #pragma unroll
                     for (int r = 0; r < RTN; r++) {
-                        float v = 0.0f;
+                        float v = d[r][c][b0][i * PK + b0];
 #pragma unroll
-                        for (int b = b0; b < b0 + count; b++) { // differences step by step: smaller than the sums
-                            float part = d[r][c][b][i * PK + b];
-                            if constexpr (TX != Q4G_X_F16)
-                                part = fmaf(-z16[r], sum[c][i * PK + b], part);
-                            v = b == b0 ? part : v + part;
-                        }
+                        for (int b = b0 + 1; b < b0 + count; b++)
+                            v += d[r][c][b][i * PK + b];
                         y[r][c][i] = fmaf(s[r], v, y[r][c][i]);
                     }
             if constexpr (RTN * C >= 8) // one group at a time, or they run out of registers
