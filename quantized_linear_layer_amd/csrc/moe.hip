@@ -323,8 +323,9 @@ struct MoeEntry {
 static_assert(kMaxExperts <= 1024 && kMoePairs <= 2048, "the fields of an entry");
 
 // The gated products between the two: two bf16 parts of each where the
-// stream has 16 bits (what is left out is below 2^-17 of the value, against 2^-9 and 2^-12 of
-// the outputs' own rounding), three (all 24 bits) where it is f32.  The parts are what the
+// stream has 16 bits (what is left out is up to 2^-17 of the value, against 2^-9 and 2^-12 of
+// the outputs' own rounding; all 24 bits would take a third part: 2 of 8 experts of 3 x 14336 x 4096, 32 tokens 303
+// us in place of 224, as sixteen such rows do not fit in LDS at once), three (all 24 bits) where it is f32.  The parts are what the
 // matrix core reads, so the down kernel's waves load them as they stand: splitting
 // f32 values there would be done again for every 16 output rows.
 struct MoeArgs {
@@ -446,13 +447,17 @@ __device__ __forceinline__ void moe_outputs(const MoeArgs &a, const MoeEntry &en
             continue;
         const int64_t to = (KIND == MOE_ONE ? entry.first : (int)a.plan->row[entry.first + p]) * outs + j;
         if constexpr (GATED) {
-            const float h = activate(v[0], a.act) * v[1], rest = below_bf16(h);
-            store_part(a.h, to, h);
+            const float h = activate(v[0], a.act) * v[1];
             if (WIDE) {
+                const float rest = below_bf16(h);
+                store_part(a.h, to, h);
                 store_part(a.h, whole + to, rest);
                 store_part(a.h, 2 * whole + to, below_bf16(rest));
-            } else
-                reinterpret_cast<__bf16 *>(a.h)[whole + to] = (__bf16)rest;
+            } else { // both parts to nearest
+                const __bf16 upper = (__bf16)h;
+                reinterpret_cast<__bf16 *>(a.h)[to] = upper;
+                reinterpret_cast<__bf16 *>(a.h)[whole + to] = (__bf16)(h - (float)upper);
+            }
         } else
             a.out[to] = v[0];
     }

@@ -191,3 +191,36 @@ def test_every_bit_through_the_experts(qll_gpu, m, e, group, fmt):
                     y, m, n, k, e, ws=empty(qll.qll_workspace_bytes(qll.QLL_OP_Q4G_MOE, m, n, top)))
     torch.cuda.synchronize()
     assert torch.all((y.double() - want).abs() <= 1.5 * 2.0 ** -23 * want.abs())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,e", [(1, 2), (3, 2), (6, 1), (20, 1)])
+def test_gated_products_of_a_16_bit_stream(qll_gpu, m, e, dtype):
+    """They keep 2^-17 of their leading power of two: each output is the small difference of
+    one in [1, 2) and of 1.5, which shows it; sums of few f32 terms below 2 add 4 u."""
+    n, k, group = 640, 320, 64
+    gate, up, down = (Drawn(*s, group, 0, m + i, e) for i, s in enumerate(((n, k), (n, k), (k, n))))
+    g = gate.g
+    for w in (gate, up, down):
+        w.codes.fill_(8)
+    gate.codes[:, :, 70] = up.codes[:, :, 70] = 9
+    first = 1.0 + torch.rand(e, n, generator=g, device="cuda") * 0.5
+    first[:, 0] = 1.0
+    gate.scales[:, :, 1] = first.half()
+    up.scales[:, :, 1] = (1.5 / gate.scales[:, :, 1].float()).half()
+    h = gate.scales[:, :, 1].double() * up.scales[:, :, 1].double()
+    assert (h[:, 0] == 1.5).all() and (h - 1.5).abs().max() < 2.0 ** -10
+    down.scales.fill_(0.125)
+    pick = torch.randint(1, n, (e, k), generator=g, device="cuda")
+    down.codes.scatter_(2, pick.unsqueeze(2), 9)
+    down.codes[:, :, 0] = 7
+    x = torch.zeros(m, k, device="cuda", dtype=R.TYPES[dtype])
+    x[:, 70] = 1.0
+    ids = (torch.arange(m, device="cuda") % e).int().view(m, 1)
+    y = torch.empty_like(x)
+    qll.qll_q4g_moe(x, R.CODES[dtype], ids, torch.ones(m, 1, device="cuda"), 1, gate.packed(), up.packed(), down.packed(),
+                    group, 0, qll.QLL_ACT_NONE, None, y, m, n, k, e, ws=empty(qll.qll_workspace_bytes(qll.QLL_OP_Q4G_MOE, m, n, 1)))
+    torch.cuda.synchronize()
+    want = 0.125 * (h.gather(1, pick) - 1.5)[ids[:, 0].long()].cpu().numpy()
+    bound = R.rounded(want, np.full_like(want, 0.125 * (2.0 ** -17 + 4 * R.U)), dtype)
+    assert np.all(np.abs(R.f64(y) - want) <= bound), np.abs(R.f64(y) - want).max() / 0.125 * 2.0 ** 17
