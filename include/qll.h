@@ -530,8 +530,8 @@ int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const 
  * packed matrices [k][n] likewise; x, residual (or NULL; may be y), y: [m][k] of type T = dtype;
  * ids: int32[m][top], weights: float[m][top].  An id outside [0, e) (padding) adds nothing, and
  * its weight is not read; a row of such ids gets its residual, or 0.  An expert that a token names
- * twice counts with both weights.  The gated products keep 16 bits of
- * precision between the two products, 24 where x is f32.  One token takes two launches, more take
+ * twice counts with both weights.  The gated products keep 24 bits of
+ * precision between the two products, 16 for more than four tokens of a 16-bit type.  One token takes two launches, more take
  * four or five.  Made for few tokens: up to 64 go at once, and an expert's weights are read once for
  * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, or of fewer from
  * top * k > 131072 (k > 32768 with fewer than 64 tokens) on.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;

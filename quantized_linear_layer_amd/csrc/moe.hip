@@ -322,10 +322,11 @@ struct MoeEntry {
 };
 static_assert(kMaxExperts <= 1024 && kMoePairs <= 2048, "the fields of an entry");
 
-// The gated products between the two: two bf16 parts of each where the
-// stream has 16 bits (what is left out is up to 2^-17 of the value, against 2^-9 and 2^-12 of
-// the outputs' own rounding; all 24 bits would take a third part: 2 of 8 experts of 3 x 14336 x 4096, 32 tokens 303
-// us in place of 224, as sixteen such rows do not fit in LDS at once), three (all 24 bits) where it is f32.  The parts are what the
+// The gated products between the two: three bf16 parts of each, all 24 bits, where the stream is f32 or
+// there are up to four tokens.  Two parts for more tokens of a 16-bit stream: what is left out is up to 2^-17 of the value,
+// against 2^-9 and 2^-12 of the outputs' own rounding, and moves one of 350 f16 and of 900 bf16 outputs to the
+// neighbouring value.  (A third part costs one to four tokens 1 to 6%, but 2 of 8 experts of 3 x 14336 x 4096 on 32
+// tokens 303 us in place of 224, as sixteen such rows do not fit in LDS at once.)  The parts are what the
 // matrix core reads, so the down kernel's waves load them as they stand: splitting
 // f32 values there would be done again for every 16 output rows.
 struct MoeArgs {
@@ -334,7 +335,7 @@ struct MoeArgs {
     const int32_t *ids;
     const float *weights;
     void *y;
-    uint8_t *h; // [part][m * top][n]
+    uint8_t *h; // [part][m * top][n], moe_h_type()
     MoePlan *plan;
     int64_t n, k, gu_bytes, d_bytes; // bytes from one expert to the next
     int m, top, e, fmt, act, dtype;
@@ -409,12 +410,16 @@ __device__ __forceinline__ void store_part(uint8_t *h, int64_t at, float v)
 }
 
 enum { MOE_ONE, MOE_FEW, MOE_ALL }; // one token; up to four; more
+constexpr int moe_h_type(int tx, int kind)
+{
+    return tx == Q4G_X_F32 || tx == Q4G_X_PARTS3 || kind != MOE_ALL ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
+}
 
 // What becomes of an entry's products with one row tile, N a lane.  The waves of a set add up in LDS:
 // KW along k.  GATED: gate and up product meet, in a wave (R = 2) or as the set's KW waves on the
 // gate matrix and KW on the up matrix (R = 1), and the products' parts go to h.  Otherwise the products
 // go to `out` [m * top][k], f32, one row a choice.
-template <bool WIDE, bool GATED, int KIND, int R, int N>
+template <int TX, bool GATED, int KIND, int R, int N>
 __device__ __forceinline__ void moe_outputs(const MoeArgs &a, const MoeEntry &entry, const float (&y)[R][1][N], int64_t rt,
                                             int KW, float *sums, int lane)
 {
@@ -448,7 +453,7 @@ __device__ __forceinline__ void moe_outputs(const MoeArgs &a, const MoeEntry &en
         const int64_t to = (KIND == MOE_ONE ? entry.first : (int)a.plan->row[entry.first + p]) * outs + j;
         if constexpr (GATED) {
             const float h = activate(v[0], a.act) * v[1];
-            if (WIDE) {
+            if constexpr (moe_h_type(TX, KIND) == Q4G_X_PARTS3) {
                 const float rest = below_bf16(h);
                 store_part(a.h, to, h);
                 store_part(a.h, whole + to, rest);
@@ -496,7 +501,7 @@ __device__ __forceinline__ void moe_few(const MoeArgs &a, const MoeEntry &entry,
                 f.w[0] = Q4gRows(a.wd + entry.expert * a.d_bytes, sh, rt, GRP, a.fmt);
             w.run(f, p0, p1, a.fmt & kQ4gBf16, lane);
         }
-        moe_outputs<TX == Q4G_X_F32 || TX == Q4G_X_PARTS3, GATED, KIND>(a, entry, w.y, rt, KW, sums, lane);
+        moe_outputs<TX, GATED, KIND>(a, entry, w.y, rt, KW, sums, lane);
     }
 }
 
@@ -533,7 +538,7 @@ __device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry
             __syncthreads(); // LDS is read
         w.run(rows, rt < sh.rt, src, 0, chunks, kw, KW, a.fmt & kQ4gBf16, chunks == 1 && !first, lds, lane);
         first = false;
-        moe_outputs<TX == Q4G_X_PARTS3, GATED, MOE_ALL>(a, entry, w.y, rt, KW, sums, lane);
+        moe_outputs<TX, GATED, MOE_ALL>(a, entry, w.y, rt, KW, sums, lane);
     }
 }
 
@@ -723,9 +728,9 @@ hipError_t entries(MoeArgs a, int64_t active, int64_t count, hipStream_t s)
 template <int TX, int GRP, int KIND>
 hipError_t experts(const MoeArgs &a, hipStream_t s)
 {
-    constexpr int TH = TX == Q4G_X_F32 || TX == Q4G_X_PARTS3 ? Q4G_X_PARTS3 : Q4G_X_PARTS2;
+    constexpr int TH = moe_h_type(TX, KIND);
     const int64_t pairs = (int64_t)a.m * a.top, active = pairs < a.e ? pairs : a.e;
-    const int64_t count = KIND == MOE_ONE ? pairs : active + pairs / (TH == Q4G_X_PARTS3 ? 8 : 16); // of entries, at most
+    const int64_t count = KIND == MOE_ONE ? pairs : active + pairs / (TX == Q4G_X_PARTS3 ? 8 : 16); // of entries, at most
     hipError_t e = entries<TX, GRP, true, KIND>(a, active, count, s);
     if (e != hipSuccess)
         return e;

@@ -194,10 +194,10 @@ def test_every_bit_through_the_experts(qll_gpu, m, e, group, fmt):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("m,e", [(1, 2), (3, 2), (6, 1), (20, 1)])
+@pytest.mark.parametrize("m,e", [(1, 2), (3, 2), (4, 1), (6, 1), (20, 1)])
 def test_gated_products_of_a_16_bit_stream(qll_gpu, m, e, dtype):
-    """They keep 2^-17 of their leading power of two: each output is the small difference of
-    one in [1, 2) and of 1.5, which shows it; sums of few f32 terms below 2 add 4 u."""
+    """All but 2^-17 of their leading power of two is kept, of up to four tokens all but 2^-23: each output is the
+    small difference of one in [1, 2) and of 1.5, which shows it; sums of few f32 terms below 2 add 4 u."""
     n, k, group = 640, 320, 64
     gate, up, down = (Drawn(*s, group, 0, m + i, e) for i, s in enumerate(((n, k), (n, k), (k, n))))
     g = gate.g
@@ -222,5 +222,5 @@ def test_gated_products_of_a_16_bit_stream(qll_gpu, m, e, dtype):
                     group, 0, qll.QLL_ACT_NONE, None, y, m, n, k, e, ws=empty(qll.qll_workspace_bytes(qll.QLL_OP_Q4G_MOE, m, n, 1)))
     torch.cuda.synchronize()
     want = 0.125 * (h.gather(1, pick) - 1.5)[ids[:, 0].long()].cpu().numpy()
-    bound = R.rounded(want, np.full_like(want, 0.125 * (2.0 ** -17 + 4 * R.U)), dtype)
-    assert np.all(np.abs(R.f64(y) - want) <= bound), np.abs(R.f64(y) - want).max() / 0.125 * 2.0 ** 17
+    bound = R.rounded(want, np.full_like(want, 0.125 * ((2.0 ** -17 if m > 4 else 2.0 ** -23) + 4 * R.U)), dtype)
+    assert np.all(np.abs(R.f64(y) - want) <= bound)
