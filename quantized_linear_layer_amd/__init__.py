@@ -147,8 +147,8 @@ def _stream(stream):
 
 _raw_stream = None  # torch's current stream of a device as a handle, and its current device
 _current_device = None
-_F32, _I32 = QLL_DTYPE_F32, "int32"
-_types = {}  # element types of an argument by its QLL_DTYPE_* value (or _I32): its own, or raw bits
+_F32, _I32, _U8 = QLL_DTYPE_F32, "int32", "uint8"
+_types = {}  # element types of an argument by its QLL_DTYPE_* value (or _I32, _U8): its own, or raw bits
 
 
 def _device(t, what):
@@ -162,7 +162,7 @@ def _device(t, what):
         import torch
         # (the calls that torch.cuda.current_stream() and current_device() wrap, without the objects: 2.5 us a call;
         # the one that is tested above comes last: another thread may be here too)
-        _types = {_F32: (torch.float32, torch.uint8), _I32: (torch.int32, torch.uint8),
+        _types = {_F32: (torch.float32, torch.uint8), _I32: (torch.int32, torch.uint8), _U8: (torch.uint8, torch.int8),
                   QLL_DTYPE_BF16: (torch.bfloat16, torch.int16, torch.uint8),
                   QLL_DTYPE_F16: (torch.float16, torch.int16, torch.uint8)}
         _current_device = torch._C._cuda_getDevice
@@ -505,13 +505,13 @@ def _q4g_need(n, k, group, fmt):
 
 def qll_q4g_pack(codes, scales, zeros, group, fmt, wp, n, k, stream=None):
     """Load-time packing of 4-bit codes with their group scales and, with
-    QLL_Q4G_ZEROS in fmt, zero points (else unused)."""
+    QLL_Q4G_ZEROS in fmt, zero points (else unused); codes and zero points one a byte."""
     d = _device(wp, "wp")
     groups = n * (k // group) if group else 0
     zeros = zeros if fmt & QLL_Q4G_ZEROS else None
-    _call("qll_q4g_pack", _arg(codes, n * k, "codes", d),
+    _call("qll_q4g_pack", _arg(codes, n * k, "codes", d, _U8),
           _arg(scales, groups * 2, "scales", d, QLL_DTYPE_BF16 if fmt & QLL_Q4G_BF16 else QLL_DTYPE_F16),
-          _arg(zeros, groups, "zeros", d), group, fmt, _arg(wp, _q4g_need(n, k, group, fmt), "wp", d), n, k,
+          _arg(zeros, groups, "zeros", d, _U8), group, fmt, _arg(wp, _q4g_need(n, k, group, fmt), "wp", d), n, k,
           _on(d, stream))
 
 
