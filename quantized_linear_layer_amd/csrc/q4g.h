@@ -4,8 +4,8 @@
 // The packed form and the product of one wave on it, shared by the linear
 // layer (q4g.hip) and the experts (moe.hip).
 //
-// Packed form of W[n][k], three regions one after another, each a multiple of
-// 256 bytes, for tiles of 16 rows (index rt, rows past n zero) and 128 weights
+// Packed form of W[n][k], three regions one after another and zero bytes up to a multiple of
+// 256, for tiles of 16 rows (index rt, rows past n zero) and 128 weights
 // (index kt, weights past k zero):
 //   codes   tile (rt, kt) at 1024 * (rt * KT + kt), KT = ceil(k / 128): 16 bytes a
 //           lane of a wave, lane l holding row l % 16; dword j (matrix-core step j) has the
@@ -32,13 +32,14 @@ constexpr int kQ4gBf16 = 1, kQ4gZeros = 2; // the ABI's QLL_Q4G_*
 
 struct Q4gShape {
     int64_t rt, kt, ks;                     // tiles of 16 rows, of 128 weights, pieces of 512
-    int64_t scales, zeros, bytes;           // byte offsets of the regions, and the end
+    int64_t scales, zeros, end, bytes;      // byte offsets of the regions, their end, and that of all bytes
     __host__ __device__ Q4gShape(int64_t n, int64_t k, int64_t group, int fmt)
         : rt((n + 15) / 16), kt((k + 127) / 128), ks((k + 511) / 512)
     {
         scales = rt * kt * 1024;
         zeros = scales + rt * ks * 16 * (1024 / group);
-        bytes = (zeros + ((fmt & kQ4gZeros) ? rt * ks * 16 * (256 / group) : 0) + 255) / 256 * 256;
+        end = zeros + ((fmt & kQ4gZeros) ? rt * ks * 16 * (256 / group) : 0);
+        bytes = (end + 255) / 256 * 256;
     }
 };
 

@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(256) q4g_pack_kernel(Codes codes, Scales from,
             pack_codes(codes, wp, sh, tile, n, k);
     } else {
         const int64_t item = (block - code_blocks) * 256 + threadIdx.x;
+        if (sh.end + item < sh.bytes) // the first of them, the bytes behind the regions too
+            wp[sh.end + item] = 0;
         if (item < sh.rt * sh.ks * 16)
             pack_scales(from, wp + sh.scales, (fmt & kQ4gZeros) ? wp + sh.zeros : nullptr, sh.ks, item, n, k / group, group);
     }
