@@ -533,8 +533,8 @@ int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const 
  * twice counts with both weights.  The gated products keep 24 bits of
  * precision between the two products, 16 for more than four tokens of a 16-bit type.  One token takes two launches, more take
  * four or five.  Made for few tokens: up to 64 go at once, and an expert's weights are read once for
- * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, or of fewer from
- * top * k > 131072 (k > 32768 with fewer than 64 tokens) on.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;
+ * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, and of fewer where
+ * k > 32768 or tokens * max(top, 2) * k > 2^23.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;
  * e and top as in qll_moe_route (else QLL_ERR_SHAPE); QLL_ERR_VALUE for another group, fmt, dtype or act.
  * NaN and infinities, and the size of x and of the gated products: as x in qll_q4g_linear, token by token.
  * The result does not depend on what other tokens are in the call beyond the order of f32 sums.

@@ -686,19 +686,22 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
     }
 }
 
-// Room for the down products of each choice, and before them for f32 rows as parts: up to 32768
-// columns, 32 MiB at most.
+// Room that a token's down products take in a column, 4 bytes a choice, and before them its f32 value as
+// parts, 6 bytes.
+int64_t moe_column_bytes(int64_t top) { return (int64_t)sizeof(float) * (top < 2 ? 2 : top); }
+
+// Room for these of up to 64 tokens: 32768 columns, 32 MiB at most; one token needs none.
 int64_t moe_out_bytes(int64_t m, int64_t top)
 {
-    const int64_t all = m == 1 ? 0 : m * top * 32768 * (int64_t)sizeof(float);
+    const int64_t all = m == 1 ? 0 : m * 32768 * moe_column_bytes(top);
     return all < (int64_t)32 << 20 ? all : (int64_t)32 << 20;
 }
 
-// Tokens that go at once: 64, or as many as have that room; one needs none.
+// Tokens that go at once: 64, or as many as have that room.
 int64_t moe_group(int64_t m, int64_t top, int64_t k)
 {
     const int64_t tokens = m < kMoeTokens ? m : kMoeTokens, room = moe_out_bytes(tokens, top);
-    const int64_t each = k * (int64_t)sizeof(float) * (top < 2 ? 2 : top); // 4 bytes a choice, 6 for a row's parts
+    const int64_t each = k * moe_column_bytes(top);
     return room / each < 2 ? 1 : room / each < tokens ? room / each : tokens;
 }
 
