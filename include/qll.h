@@ -513,8 +513,8 @@ enum { QLL_SCORE_SOFTMAX = 0, QLL_SCORE_SIGMOID = 1 };
 /* The experts of each token.  Logits l = X.Wr^T, summed in f64; scores p = softmax(l) over the
  * e experts, or the sigmoid of each l.  ids[m][top]: the `top` experts with the largest
  * p + bias[expert] (the largest l where bias is NULL), largest first, the lower index first among
- * equal ones.  weights[m][top]: their p, divided by its sum over them where renorm is not 0,
- * times scale.  Scores are f64, so the choice does not depend on the order of a sum; f32 only on
+ * equal ones.  weights[m][top]: their p, divided by its sum over them where renorm is not 0 (also where all of
+ * these are too small for f64), times scale.  Scores are f64, so the choice does not depend on the order of a sum; f32 only on
  * return.  x: [m][k] of type dtype, wr: [e][k] of type wr_dtype, bias: float[e] or
  * NULL, scale finite.  1 <= e <= 1024, 1 <= top <= min(32, e), any k >= 1 below 2^24 (else
  * QLL_ERR_SHAPE); QLL_ERR_VALUE for an unknown dtype or score.  In a row with NaN or an infinity

@@ -237,6 +237,12 @@ __global__ void __launch_bounds__(64) moe_top_kernel(const double *logits, const
             mine = s, chosen = who * PER + at;
         total += s;
     }
+    if (renorm && total < 0x1p-900) { // scores that leave f64's range (all chosen ones far below 1): by their logits
+        const double l = lane < top ? logits[t * e + chosen] : -__builtin_inf();
+        const uint64_t b = wave_max(order_bits(l));
+        mine = exp(l - __builtin_bit_cast(double, b >> 63 ? b & 0x7fffffffffffffffull : ~b));
+        total = wave_sum(mine);
+    }
     if (lane < top) {
         ids[t * top + lane] = chosen;
         weights[t * top + lane] = (float)((renorm ? mine / total : mine) * (double)scale);
