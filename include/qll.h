@@ -496,9 +496,8 @@ int qll_q4g_from_q4_0(const void *w, void *wp, int64_t n, int64_t k, void *strea
  * (QLL_DTYPE_*); bias: float[n] or NULL; act a QLL_ACT_* value; residual: [m][n] of
  * type y_dtype or NULL, may be y itself; y: [m][n] of type T = y_dtype, rounded once, to
  * nearest even.  Products are of c - z itself and sums f32: without an epilogue, before that rounding, within
- * (4 * group + k / group) * 2^-24 * sum_t |x s (c - z)| of the exact sum.  |x| < 2^117, so that a group's sum stays in
- * f32's range.  A row of x with
- * NaN or an infinity in it has unspecified outputs, other rows do not change.  k % group == 0,
+ * (4 * group + k / group) * 2^-24 * sum_t |x s (c - z)| of the exact sum (and 2^-126, below f32's normal range).
+ * |x| < 2^117, so that a group's sum stays in f32's range.  A row of x with NaN or an infinity in it has unspecified outputs, other rows do not change.  k % group == 0,
  * k < 2^24 (else QLL_ERR_SHAPE).  ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_LINEAR,
  * m, n, k) bytes (0 where one launch does without, as up to four rows do: ws may be NULL
  * then); contents on return unspecified.  QLL_ERR_VALUE for another group, fmt, dtype or act. */
@@ -513,9 +512,9 @@ enum { QLL_SCORE_SOFTMAX = 0, QLL_SCORE_SIGMOID = 1 };
 /* The experts of each token.  Logits l = X.Wr^T, summed in f64; scores p = softmax(l) over the
  * e experts, or the sigmoid of each l.  ids[m][top]: the `top` experts with the largest
  * p + bias[expert] (the largest l where bias is NULL), largest first, the lower index first among
- * equal ones.  weights[m][top]: their p, divided by its sum over them where renorm is not 0 (also where all of
- * these are too small for f64), times scale.  Scores are f64, so the choice does not depend on the order of a sum; f32 only on
- * return.  x: [m][k] of type dtype, wr: [e][k] of type wr_dtype, bias: float[e] or
+ * equal ones.  weights[m][top]: their p, divided by its sum over them where renorm is not 0 (also where
+ * all of these are too small for f64), times scale.  Scores are f64, so the choice does not depend on the
+ * order of a sum; f32 only on return.  x: [m][k] of type dtype, wr: [e][k] of type wr_dtype, bias: float[e] or
  * NULL, scale finite.  1 <= e <= 1024, 1 <= top <= min(32, e), any k >= 1 below 2^24 (else
  * QLL_ERR_SHAPE); QLL_ERR_VALUE for an unknown dtype or score.  In a row with NaN or an infinity
  * among its logits the ids are unspecified, different and below e, and the weights unspecified.  ws/ws_bytes: at least
@@ -530,14 +529,15 @@ int qll_moe_route(const void *x, int dtype, const void *wr, int wr_dtype, const 
  * packed matrices [k][n] likewise; x, residual (or NULL; may be y), y: [m][k] of type T = dtype;
  * ids: int32[m][top], weights: float[m][top].  An id outside [0, e) (padding) adds nothing, and
  * its weight is not read; a row of such ids gets its residual, or 0.  An expert that a token names
- * twice counts with both weights.  The gated products keep 24 bits of
- * precision between the two products, 16 for more than four tokens of a 16-bit type.  One token takes two launches, more take
+ * twice counts with both weights.  The gated products keep 24 bits of precision between the two
+ * products, 16 for more than four tokens of a 16-bit type.  One token takes two launches, more take
  * four or five.  Made for few tokens: up to 64 go at once, and an expert's weights are read once for
- * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, and of fewer where
- * k > 32768 or tokens * max(top, 2) * k > 2^23.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;
+ * every 16 tokens that chose it (8 where x is f32); more tokens go in groups of 64, and groups are smaller
+ * where k > 32768 or min(m, 64) * max(top, 2) * k > 2^23.  n % group == 0, k % group == 0, n < 2^20, k < 2^24;
  * e and top as in qll_moe_route (else QLL_ERR_SHAPE); QLL_ERR_VALUE for another group, fmt, dtype or act.
  * NaN and infinities, and the size of x and of the gated products: as x in qll_q4g_linear, token by token.
- * The result does not depend on what other tokens are in the call beyond the order of f32 sums.
+ * The result does not depend on what other tokens are in the call beyond the order of f32 sums and that
+ * precision.
  * ws/ws_bytes: at least qll_workspace_bytes(QLL_OP_Q4G_MOE, m, n, top) bytes (up to 32 MiB and
  * 6 * top * n for each of up to 64 tokens); contents on return unspecified. */
 int qll_q4g_moe(const void *x, int dtype, const int32_t *ids, const float *weights, int64_t top, const void *wg,

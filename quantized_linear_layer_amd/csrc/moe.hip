@@ -548,11 +548,11 @@ __device__ __forceinline__ void moe_more(const MoeArgs &a, const MoeEntry &entry
     }
 }
 
-// The products of entry blockIdx.y.  What bounds them is the experts' weights: one token, two experts of 3 x 14336 x
-// 4096 gate and up in 23 to 26 us (122 MB, 4.7 to 5.3 TB/s); 64 tokens, six of 64 experts of 3 x 1536 x 4096, 79 to 81
-// us (418 MB, 5.2 TB/s) and down 50 to 55 (3.8 to 4.1).  37 f32 tokens, three of 23 experts of 3 x 1440 x 2592, take
-// 47 to 50 us (99 MB, 2.0 TB/s) and 24 to 27: three parts a value are three times the matrix instructions
-// (busy 30% of the time) and LDS reads.
+// The products of entry blockIdx.y.  What bounds them is the experts' weights and the instructions that widen
+// them: one bf16 token, two experts of 3 x 14336 x 4096 gate and up in 27 us (122 MB, 4.5 TB/s); 64 tokens, six of 64 experts of
+// 3 x 1536 x 4096, 88 to 95 us (418 MB, 4.4 to 4.7 TB/s) and down 53 to 58 (3.6 to 3.9).  37 f32 tokens, three of 23
+// experts of 3 x 1440 x 2592, take 42 to 44 us (99 MB, 2.3 TB/s) and 26 to 28: three parts a value are three times the
+// matrix instructions (busy 24% of the time) and LDS reads.
 template <int TX, int GRP, bool GATED, int KIND>
 __global__ void __launch_bounds__(512, 4) moe_entry_kernel(MoeArgs a)
 {
@@ -622,8 +622,8 @@ constexpr int kDownWaves = 16;
 // One token's down products of 16 rows, weighted and added up.  The pieces of its choices' matrices'
 // rows, one choice after another, are one sequence that the waves share evenly, with
 // loads in flight across the choices' ends; at such an end a wave adds its weighted products.  Two experts of
-// 14336 -> 4096: 16 us (61 MB, 3.7 TB/s), 16 waves a row tile that wait a third of their time to issue; eight of
-// 1024 -> 2048 6 to 7 us, latency.
+// 14336 -> 4096: 20 to 21 us (61 MB, 3.0 TB/s), 16 waves a row tile with 1441 vector instructions each, which take half
+// of it, and a third of their time waiting to issue; eight of 1024 -> 2048 7 to 8 us, latency.
 template <int TX, int GRP>
 __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a)
 {

@@ -91,7 +91,8 @@ __device__ __forceinline__ void pack_scales(const Scales &from, uint8_t *scales,
 }
 
 // The first workgroups pack the codes, a tile a wave, the others the scales, an item a thread: one
-// launch, as many a small matrix is packed (an expert's, one at a time).  Its reads and writes bound it.
+// launch, as many a small matrix is packed (an expert's, one at a time: 8.8 us, the host's).  14336 x 4096 with zero
+// points: 28 us (90 MB, 3.1 TB/s).
 template <class Codes, class Scales>
 __global__ void __launch_bounds__(256) q4g_pack_kernel(Codes codes, Scales from, uint8_t *wp, int64_t first, int64_t n,
                                                        int64_t k, int group, int fmt)
@@ -179,10 +180,11 @@ __device__ __forceinline__ void q4g_outputs(const Q4gLinear &a, const float (&y)
 
 // Few activation rows, or a small product: the waves of a set share its row tiles' pieces of k;
 // groups of 16 / PK activation rows along y.  Four steps an operand while there are four rows, each wave
-// fetching them: 4096 -> 14336, one row, 7.7 us (31 MB, 4.0 TB/s; loading alone would take 6.1): memory, with
-// waves that wait a third of their time to issue.  512 -> 512 takes 4.1 us, of which 1.8 is an empty
+// fetching them: 4096 -> 14336, one bf16 row, 8.8 to 9.8 us (31 MB, 3.5 TB/s; loading alone would take 6.1): 613 vector
+// instructions a wave, which are half of that time, and waves that wait a third of theirs to issue; one f32 row 13.4
+// (947, three times the matrix instructions).  512 -> 512 takes 4.2 us, of which 1.8 is an empty
 // launch's and the rest one trip to memory for a wave, the sums and the store.  1440 -> 4099 on 37 rows of f32 13 us:
-// three groups read the codes, and a wave's 144 matrix instructions and 1856 others wait for
+// three groups read the codes, and a wave's 96 matrix instructions and 1968 others wait for
 // one tile at a time (more in flight takes more registers than two workgroups a CU leave).
 template <int TX, int GRP, int RTN, int PK, int D>
 __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
@@ -212,11 +214,11 @@ __global__ void __launch_bounds__(512, 4) q4g_few_kernel(Q4gLinear a)
 // More rows.  Workgroups eight apart land on the same XCD: those of one set of rows follow
 // each other there, so that its weights stay in that L2.
 //
-// 16 rows, 14336 -> 4096: 13 us (33 MB, 2.5 TB/s), 2 to 4 to add up the parts; four waves a SIMD that wait for
+// 16 rows, 14336 -> 4096: 13 to 14 us (33 MB, 2.4 TB/s), 2 to 4 to add up the parts; four waves a SIMD that wait for
 // memory and for instructions to issue, each weight widened for one operand of 16 rows.  512 rows, 4096 ->
-// 14336: 97 to 100 us (600 TFLOP/s; 90 back to back): some 5700 vector instructions a wave against 1024 of the matrix
-// core, which widen the codes (nine for eight weights, again in each of the eight workgroups that share them) and
-// scale each group's sum, and a wait for all eight waves every 512 weights.  64 x 32 outputs a wave: 64 x 64
+// 14336 in f16: 97 to 99 us (610 TFLOP/s; 91 back to back; bf16 112 and 105): some 5700 vector instructions a wave (bf16
+// 7650) against 1024 of the matrix core, which widen the codes (nine for eight weights, 17 as bf16, again in each of
+// the eight workgroups that share them) and scale each group's sum, and a wait for all eight waves every 512 weights.  64 x 32 outputs a wave: 64 x 64
 // takes 106 us and twice as long at 128 rows, 16 x 64 152; sixteen waves at 128 registers spill.
 template <int TX, int GRP, int RTN, int C, int PK, int WPS>
 __global__ void __launch_bounds__(512, WPS) q4g_linear_kernel(Q4gLinear a)
@@ -290,11 +292,11 @@ __global__ void __launch_bounds__(256) q4g_split_kernel(const uint8_t *x, uint8_
 
 // Whether a product takes the waves that fetch their own activations, in one launch and without a
 // workspace: up to four rows; up to 16 while the codes are few (us, so and with the rows in LDS: 14336 x 4096, 16
-// rows 13.9 and 16.6, f32 21 and 25; 32000 x 4096, 22 and 25, f32 49 and 42), but on short and wide matrices
-// with 9 to 16 rows, where four operands a tile are too much (4096 x 14336, 16 rows 19.1 and 14.1); with more
-// rows while the codes that all groups of 16 rows read are few (4096 x 4096, 96 rows 17.9 and 19.4, 128 rows 21.1 and 19.8,
-// f32 32 rows 12.4 and 14.7, 64 rows 20.3 and 18.5; 2048 x 2048, 256 rows 13.1 and 15.3; 14336 x 4096, 17 rows 18.6
-// and 18.2, 64 rows 39 and 27).
+// rows 14.3 and 17.5, f32 22 and 26; 32000 x 4096, 23 and 27, f32 50 and 43), but on short and wide matrices
+// with 9 to 16 rows, where four operands a tile are too much (4096 x 14336, 16 rows 20.0 and 15.5); with more
+// rows while the codes that all groups of 16 rows read are few (4096 x 4096, 96 rows 18.1 and 19.4, 128 rows 21.5 and 19.1,
+// f32 32 rows 12.5 and 15.0, 64 rows 20.6 and 19.3; 2048 x 2048, 256 rows 13.2 and 15.0; 14336 x 4096, 17 rows 20.5
+// and 19.8, 64 rows 44 and 28).
 bool q4g_small(bool wide, int64_t m, int64_t n, int64_t k)
 {
     if (m <= 4)
